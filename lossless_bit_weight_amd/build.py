@@ -23,7 +23,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 # compiled once per x height so the build runs in parallel.
 SOURCES = [("w12_api.hip", "w12_api", []), ("w12_pack.hip", "w12_pack", []),
            ("w12_exc.hip", "w12_exc", []), ("w12_gemm.hip", "w12_gemm", []),
-           ("w12_probe.hip", "w12_probe", [])]
+           ("w12_probe.hip", "w12_probe", []), ("mx4_api.hip", "mx4_api", []),
+           ("mx4_codec.hip", "mx4_codec", []), ("mx4_gemm.hip", "mx4_gemm", []),
+           ("mx4_moe.hip", "mx4_moe", [])]
 SOURCES += [("w12_gemm_inst.hip", "w12_gemv_m%d" % m, ["-DW12_INST_M=%d" % m]) for m in range(1, 9)]
 SOURCES += [("w12_gemm_inst.hip", "w12_mfma", ["-DW12_INST_MFMA"]),
             ("w12_gemm_inst.hip", "w12_mfma8", ["-DW12_INST_MFMA8"]),
