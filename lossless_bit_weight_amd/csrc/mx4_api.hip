@@ -52,6 +52,7 @@ int status_of(hipError_t e) { return e == hipSuccess ? W12_OK : W12_ERR_HIP; }
 
 int check_gemm_shape(int64_t M, int64_t N, int64_t K) {
     if (N < 1 || M < 0 || M > kMaxM) return W12_ERR_SHAPE;
+    if (M > 0 && N >= kMaxElems / M) return W12_ERR_SHAPE;
     return check_container(1, N, K);
 }
 

@@ -56,11 +56,12 @@ __device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x4_t c) 
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// 16x16x128 of two 4-bit operands (format 4) under the scales in the lowest
-// bytes of sa and sb.
+// 16x16x128 of two 4-bit operands (format 4) under the scales in byte J of sa
+// and sb.
+template <int J = 0>
 __device__ __forceinline__ f32x4_t mfma_mx4(i32x8_t a, i32x8_t b, f32x4_t c, uint32_t sa,
                                             uint32_t sb) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, (int)sa, 0, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, J, (int)sa, J, (int)sb);
 }
 
 __device__ __forceinline__ u32x4_t load16_nt(const uint8_t* p) {
