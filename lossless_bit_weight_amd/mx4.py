@@ -15,8 +15,8 @@ call, so calls on different streams, and captured graphs, share nothing.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -82,6 +82,7 @@ def mx4_scales_bytes(B: int, R: int, K: int) -> int:
     return int(lib().mx4_scales_bytes(int(B), int(R), int(K)))
 
 
+@functools.lru_cache(maxsize=4096)
 def mx4_gemm_workspace_bytes(M: int, N: int, K: int, x_mx4: bool = False) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().mx4_gemm_workspace_bytes(int(M), int(N), int(K), int(bool(x_mx4)),
@@ -89,6 +90,7 @@ def mx4_gemm_workspace_bytes(M: int, N: int, K: int, x_mx4: bool = False) -> int
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=4096)
 def mx4_moe_workspace_bytes(T: int, H: int, I: int, E: int, top_k: int,
                             out_dtype: torch.dtype = torch.bfloat16) -> int:
     n = ctypes.c_size_t(0)
@@ -130,14 +132,15 @@ class MX4Tensor:
         return self._code_bytes + self._scale_bytes
 
     def ptrs(self, what: str) -> tuple:
-        """(codes, scales) device pointers."""
-        if not self.data.is_cuda:
+        """(codes, scales) device pointers and the device's index."""
+        d = self.data
+        if not d.is_cuda:
             raise ValueError("%s must be on the GPU" % what)
-        if self.data.dtype != torch.uint8 or not self.data.is_contiguous() \
-                or self.data.numel() < self.nbytes:
+        if d.dtype is not torch.uint8 or d.numel() < self._code_bytes + self._scale_bytes \
+                or not d.is_contiguous():
             raise ValueError("%s: data must be %d contiguous bytes" % (what, self.nbytes))
-        p = self.data.data_ptr()
-        return p, p + self._code_bytes
+        p = d.data_ptr()
+        return p, p + self._code_bytes, d.get_device()
 
 
 # ---- marshalling helpers ---------------------------------------------------
@@ -155,19 +158,28 @@ def _type_of(dtype: torch.dtype) -> int:
     raise TypeError("expected float32 or BF16, got %s" % dtype)
 
 
-_here = contextlib.nullcontext()
+# torch's current stream of a device as the pointer itself (torch.cuda.current_stream
+# builds an object around it, which costs a small call more than its launch)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
-def _on(device: torch.device, *others: torch.device):
-    """Context in which `device` is current; every tensor has to be there."""
+def _call(device: int, fn, args: tuple) -> None:
+    """fn(*args, stream) on torch's current stream of `device`, which is made
+    current for the launch."""
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, _raw_stream(device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device))
+    if status != 0:
+        raise MX4Error(status, fn.__name__)
+
+
+def _same(device: int, *others: int) -> None:
     for o in others:
         if o != device:
-            raise ValueError("tensors on %s and %s in one call" % (device, o))
-    return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+            raise ValueError("tensors on devices %d and %d in one call" % (device, o))
 
 
 def _gpu(t: torch.Tensor, what: str) -> torch.Tensor:
@@ -202,10 +214,11 @@ def _batched(t: torch.Tensor, what: str) -> tuple:
 def _output(y, M: int, N: int, out_dtype: torch.dtype, device) -> tuple:
     """(y, row stride, type) of a given or new [M, N] output."""
     if y is None:
-        if out_dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-        y = torch.empty((M, N), dtype=out_dtype, device=device)
-        return y, N, OUT_F32 if out_dtype == torch.float32 else OUT_BF16
+        if out_dtype is torch.float32:
+            return torch.empty((M, N), dtype=out_dtype, device=device), N, OUT_F32
+        if out_dtype is torch.bfloat16:
+            return torch.empty((M, N), dtype=out_dtype, device=device), N, OUT_BF16
+        raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
     ld = _rows(_gpu(y, "y"), "y")
     if tuple(y.shape) != (M, N):
         raise ValueError("y is %s, this call writes (%d, %d)" % (tuple(y.shape), M, N))
@@ -230,7 +243,7 @@ def empty_mx4(R: int, K: int, batch: int | None = None, device="cuda") -> MX4Ten
     if R < 0 or K < BLOCK or K % BLOCK or (batch is not None and batch < 1):
         raise MX4Error(-2, "empty_mx4(%s, %d, %d)" % (batch, R, K))
     t = MX4Tensor(None, R, K, batch)
-    t.data = torch.empty(t.nbytes, dtype=torch.uint8, device=device)
+    t.data = torch.empty(t._code_bytes + t._scale_bytes, dtype=torch.uint8, device=device)
     return t
 
 
@@ -242,17 +255,17 @@ def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None) -> MX4Tensor:
         out = empty_mx4(R, K, B, x.device)
     elif out.shape != tuple(x.shape):
         raise ValueError("out holds %s, x is %s" % (out.shape, tuple(x.shape)))
-    codes, scales = out.ptrs("out")
-    with _on(x.device, out.data.device):
-        _check(lib().mx4_quantize(x.data_ptr(), xt, 1 if B is None else B, R, K, ld, ldb, codes,
-                                  scales, _stream()), "mx4_quantize")
+    codes, scales, dev = out.ptrs("out")
+    _same(dev, x.get_device())
+    _call(dev, lib().mx4_quantize, (x.data_ptr(), xt, 1 if B is None else B, R, K, ld, ldb, codes,
+                                    scales))
     return out
 
 
 def mx4_dequantize(q: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """The values a container stands for, [R, K] or [B, R, K]."""
-    codes, scales = q.ptrs("q")
+    codes, scales, dev = q.ptrs("q")
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
@@ -261,9 +274,9 @@ def mx4_dequantize(q: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16,
         raise ValueError("out is %s, q holds %s" % (tuple(out.shape), q.shape))
     yt = _type_of(_gpu(out, "out").dtype)
     B, R, K, ld, ldb = _batched(out, "out")
-    with _on(out.device, q.data.device):
-        _check(lib().mx4_dequantize(codes, scales, 1 if B is None else B, R, K, out.data_ptr(), yt,
-                                    ld, ldb, _stream()), "mx4_dequantize")
+    _same(dev, out.get_device())
+    _call(dev, lib().mx4_dequantize, (codes, scales, 1 if B is None else B, R, K, out.data_ptr(),
+                                      yt, ld, ldb))
     return out
 
 
@@ -273,30 +286,30 @@ def mx4_gemm(x, w: MX4Tensor, out_dtype: torch.dtype = torch.float32,
     [M, K] (mx4_gemm) or a container of one [M, K] (mx4_gemm_mx4)."""
     if w.batch is not None:
         raise ValueError("w must hold one matrix")
-    wc, wsc = w.ptrs("w")
-    dev = w.data.device
-    if isinstance(x, MX4Tensor):
-        if x.batch is not None or x.K != w.K:
-            raise ValueError("x %s does not multiply w %s" % (x.shape, w.shape))
-        xc, xsc = x.ptrs("x")
+    wc, wsc, dev = w.ptrs("w")
+    N, K = w.R, w.K
+    device = w.data.device
+    x_mx4 = isinstance(x, MX4Tensor)
+    if x_mx4:
         M = x.R
-        with _on(dev, x.data.device, dev if y is None else y.device):
-            y, ldy, yt = _output(y, M, w.R, out_dtype, dev)
-            keep, wsp, wsb = _workspace(mx4_gemm_workspace_bytes(M, w.R, w.K, True), workspace, dev)
-            _check(lib().mx4_gemm_mx4(xc, xsc, M, wc, wsc, w.R, w.K, y.data_ptr(), ldy, yt, wsp,
-                                      wsb, _stream()), "mx4_gemm_mx4")
-        return y
-    if _gpu(x, "x").dtype not in _BF16_TYPES:
-        raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
-    ldx = _rows(x, "x")
-    M, K = x.shape
-    if K != w.K:
-        raise ValueError("x %s does not multiply w %s" % (tuple(x.shape), w.shape))
-    with _on(dev, x.device, dev if y is None else y.device):
-        y, ldy, yt = _output(y, M, w.R, out_dtype, dev)
-        keep, wsp, wsb = _workspace(mx4_gemm_workspace_bytes(M, w.R, K), workspace, dev)
-        _check(lib().mx4_gemm(x.data_ptr(), M, ldx, wc, wsc, w.R, K, y.data_ptr(), ldy, yt, wsp,
-                              wsb, _stream()), "mx4_gemm")
+        if x.batch is not None or x.K != K:
+            raise ValueError("x %s does not multiply w %s" % (x.shape, w.shape))
+        xc, xsc, x_dev = x.ptrs("x")
+        args = (xc, xsc, M)
+    else:
+        if _gpu(x, "x").dtype not in _BF16_TYPES:
+            raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
+        ldx = _rows(x, "x")
+        M = x.shape[0]
+        if x.shape[1] != K:
+            raise ValueError("x %s does not multiply w %s" % (tuple(x.shape), w.shape))
+        x_dev = x.get_device()
+        args = (x.data_ptr(), M, ldx)
+    y, ldy, yt = _output(y, M, N, out_dtype, device)
+    _same(dev, x_dev, y.get_device())
+    keep, wsp, wsb = _workspace(mx4_gemm_workspace_bytes(M, N, K, x_mx4), workspace, device)
+    _call(dev, lib().mx4_gemm_mx4 if x_mx4 else lib().mx4_gemm,
+          args + (wc, wsc, N, K, y.data_ptr(), ldy, yt, wsp, wsb))
     return y
 
 
@@ -308,7 +321,7 @@ def mx4_moe(x: torch.Tensor, logits: torch.Tensor, w13: MX4Tensor, w2: MX4Tensor
     w2 of E matrices [H, I]; T <= 128."""
     if _gpu(x, "x").dtype not in _BF16_TYPES:
         raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
-    if _gpu(logits, "logits").dtype != torch.float32:
+    if _gpu(logits, "logits").dtype is not torch.float32:
         raise TypeError("logits must be float32, got %s" % logits.dtype)
     ldx, ldl = _rows(x, "x"), _rows(logits, "logits")
     (T, H), E = x.shape, logits.shape[1]
@@ -316,14 +329,14 @@ def mx4_moe(x: torch.Tensor, logits: torch.Tensor, w13: MX4Tensor, w2: MX4Tensor
     if logits.shape[0] != T or w13.shape != (E, 2 * I, H) or w2.shape != (E, H, I):
         raise ValueError("x %s, logits %s, w13 %s and w2 %s do not fit together"
                          % (tuple(x.shape), tuple(logits.shape), w13.shape, w2.shape))
-    c13, s13 = w13.ptrs("w13")
-    c2, s2 = w2.ptrs("w2")
-    dev = x.device
-    with _on(dev, logits.device, w13.data.device, w2.data.device, dev if y is None else y.device):
-        y, ldy, yt = _output(y, T, H, out_dtype, dev)
-        keep, wsp, wsb = _workspace(mx4_moe_workspace_bytes(T, H, I, E, top_k, y.dtype), workspace,
-                                    dev)
-        _check(lib().mx4_moe(x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I,
-                             E, int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp, wsb,
-                             _stream()), "mx4_moe")
+    c13, s13, d13 = w13.ptrs("w13")
+    c2, s2, d2 = w2.ptrs("w2")
+    dev, device = x.get_device(), x.device
+    y, ldy, yt = _output(y, T, H, out_dtype, device)
+    _same(dev, logits.get_device(), d13, d2, y.get_device())
+    need = mx4_moe_workspace_bytes(T, H, I, E, int(top_k), y.dtype)
+    keep, wsp, wsb = _workspace(need, workspace, device)
+    _call(dev, lib().mx4_moe, (x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I,
+                               E, int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp,
+                               wsb))
     return y
