@@ -14,7 +14,7 @@ __device__ __forceinline__ void store_y(const GemmArgs& a, int64_t m, int64_t n,
         static_cast<uint16_t*>(a.y)[m * a.ldy + n] = bf16_bits(v);
 }
 
-// ---- a few rows of x ----------------------------------------------------------
+// ---- a few rows of x, read by every wave ----------------------------------------
 // Up to 16 rows of x a workgroup: its KW waves split K between them and each
 // streams R tiles of 16 weight rows, D groups in flight.  Lane 16 q + c holds
 // piece (c, q) of the weight block and, of x, row c's values of the same 32 k:
@@ -23,8 +23,12 @@ __device__ __forceinline__ void store_y(const GemmArgs& a, int64_t m, int64_t n,
 // one-to-one assignment of k serves, as long as both operands share it) or the
 // whole piece (MX4: one instruction a group).  The result has lane (c, q)
 // holding weight rows 4 q .. 4 q + 3 for row c of x.  The waves' sums meet in
-// LDS in wave order.
-template <int R, int KW, int D, bool XM>
+// LDS in wave order.  Loads take no branch (a row past M reads the last one's
+// values, whose results are not stored): behind one, the compiler waits for
+// loads it need not (QKV M = 1 9.1 -> 6.9 us with R = 2, KW = 4, D = 3).
+// RAGGED: K % 128 != 0, blocks of x past K must be zero (their codes are, and
+// nothing times zero but a finite number is).
+template <int R, int KW, int D, bool XM, bool RAGGED>
 __global__ __launch_bounds__(KW * 64) void small_kernel(GemmArgs a) {
     __shared__ f32x4_t red[KW][R][64];
     const int lane = threadIdx.x & 63;
@@ -44,7 +48,6 @@ __global__ __launch_bounds__(KW * 64) void small_kernel(GemmArgs a) {
         wp[r] = a.w.codes + t * a.G * kCodeBlock + lane * 16;
         sp[r] = a.w.scales + t * a.Q * kScaleBlock + lane * 4;
     }
-    const bool row = m0 + c < a.M;
     const uint16_t* xp = nullptr;
     const uint8_t* xcp = nullptr;
     const uint8_t* xsp = nullptr;
@@ -52,18 +55,13 @@ __global__ __launch_bounds__(KW * 64) void small_kernel(GemmArgs a) {
         xcp = a.xm.codes + (int64_t)blockIdx.y * a.G * kCodeBlock + lane * 16;
         xsp = a.xm.scales + (int64_t)blockIdx.y * a.Q * kScaleBlock + lane * 4;
     } else {
-        xp = a.x + (int64_t)(row ? m0 + c : m0) * a.ldx + 32 * q;
+        const int m = m0 + c < a.M ? m0 + c : a.M - 1;
+        xp = a.x + (int64_t)m * a.ldx + 32 * q;
     }
 
     constexpr int XV = XM ? 1 : 4;
     u32x4_t wb[D][R], xb[D][XV];
     uint32_t ws[D][R], xs[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-        xs[d] = 0;
-#pragma unroll
-        for (int b = 0; b < XV; ++b) xb[d][b] = u32x4_t{0, 0, 0, 0};
-    }
     auto load = [&](int d, int g) {
         const int64_t so = (int64_t)(g >> 2) * kScaleBlock + (g & 3);
 #pragma unroll
@@ -75,19 +73,15 @@ __global__ __launch_bounds__(KW * 64) void small_kernel(GemmArgs a) {
             xb[d][0] = *reinterpret_cast<const u32x4_t*>(xcp + (int64_t)g * kCodeBlock);
             xs[d] = xsp[so];
         } else {
-            // rows past M load nothing: their results are not stored.  Blocks past K
-            // (the last group of a ragged K) must be zero: their codes are, and
-            // nothing times zero but a finite number is.
-            const bool in = row && 128 * (int64_t)g + 32 * q < a.K;
-            const u32x4_t zero = {0, 0, 0, 0};
-            if (g == a.G - 1) {
+            const bool in = !RAGGED || 128 * g + 32 * q < a.K;
+            const uint16_t* p = xp + (in ? 128 * (int64_t)g : -32 * q);
 #pragma unroll
-                for (int b = 0; b < XV; ++b) xb[d][b] = zero;
-            }
-            if (in) {
+            for (int b = 0; b < XV; ++b) {
+                xb[d][b] = *reinterpret_cast<const u32x4_t*>(p + 8 * b);
+                if constexpr (RAGGED) {
 #pragma unroll
-                for (int b = 0; b < XV; ++b)
-                    xb[d][b] = *reinterpret_cast<const u32x4_t*>(xp + 128 * (int64_t)g + 8 * b);
+                    for (int e = 0; e < 4; ++e) xb[d][b][e] = in ? xb[d][b][e] : 0u;
+                }
             }
         }
     };
@@ -147,20 +141,22 @@ __global__ __launch_bounds__(KW * 64) void small_kernel(GemmArgs a) {
     }
 }
 
-template <int R, int KW, int D>
+template <int R, int KW, int D, bool XM>
 hipError_t launch_small(GemmArgs a, hipStream_t s) {
     const unsigned nb = (unsigned)((tiles(a.N) + R - 1) / R);
     const int M = a.M;
     const int most = 65535 * 16;            // rows one grid covers
     for (int m = 0; m < M; m += most) {
         a.M = M - m < most ? M - m : most;
-        const dim3 grid(nb, (unsigned)tiles(a.M));
-        if (a.x == nullptr) {
-            hipLaunchKernelGGL((small_kernel<R, KW, D, true>), grid, dim3(KW * 64), 0, s, a);
+        const dim3 grid(nb, (unsigned)tiles(a.M)), block(KW * 64);
+        if (!XM && a.K % kGroup != 0)
+            hipLaunchKernelGGL((small_kernel<R, KW, D, XM, !XM>), grid, block, 0, s, a);
+        else
+            hipLaunchKernelGGL((small_kernel<R, KW, D, XM, false>), grid, block, 0, s, a);
+        if (XM) {
             a.xm.codes += (int64_t)65535 * a.G * kCodeBlock;
             a.xm.scales += (int64_t)65535 * a.Q * kScaleBlock;
         } else {
-            hipLaunchKernelGGL((small_kernel<R, KW, D, false>), grid, dim3(KW * 64), 0, s, a);
             a.x += (int64_t)most * a.ldx;
         }
         a.y = static_cast<uint8_t*>(a.y) + (int64_t)most * a.ldy * (a.y_f32 ? 4 : 2);
@@ -173,6 +169,227 @@ hipError_t launch_small(GemmArgs a, hipStream_t s) {
 __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
     asm volatile("" : "+s"(p));
     return p;
+}
+
+// ---- a few rows of x, shared through LDS ------------------------------------------
+// A workgroup: ROWS rows of x (4, or 16 and more) by 16 R WN weight rows; KW
+// groups of WN waves take every KW-th unit of UG groups of K.  A unit's weights
+// come to registers one unit ahead of their products; its x goes through LDS,
+// double-buffered, where the WN waves share it: with every wave reading x for
+// itself, the caches deliver as many bytes of x as of weights (gate+up M = 16:
+// 29.2 us there, 27.1 here; with x's reads left out, 18).  LDS row m of a
+// group holds x's 16 pieces of 8 values, piece p at place p ^ (m % 16), so that
+// the rows one read takes a piece from lie in 16 different places.
+template <int ROWS, int WN, int KW, int UG, bool XM>
+struct Mid {
+    static constexpr int kThreads = WN * KW * 64;
+    static constexpr int MT = ROWS < 16 ? 1 : ROWS / 16;
+    static constexpr int kAllPieces = XM ? MT * 64 * UG : ROWS * 16 * UG;   // of x a unit
+    static constexpr int kPieces = (kAllPieces + WN * 64 - 1) / (WN * 64);  // a thread
+    static constexpr int kStage = kPieces * WN * 64 * 16;
+    static constexpr int lds(int R) {
+        const int x = 2 * KW * kStage, red = KW * WN * MT * R * 1024;
+        return x > red ? x : red;
+    }
+};
+
+template <int ROWS, int R, int WN, int KW, int UG, bool XM>
+__global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, int nb) {
+    using T = Mid<ROWS, WN, KW, UG, XM>;
+    constexpr int MT = T::MT, P = T::kPieces;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kw = w / WN, wn = w % WN;
+    const int c = lane & 15, q = lane >> 4;
+    // the row blocks of one weight block run side by side on one XCD (consecutive
+    // workgroups go to the 8 XCDs in turn), so that its L2 serves the weights again
+    int bm = 0, bn = blockIdx.x;
+    if (mb > 1) {
+        const int band = 8 * mb, b = blockIdx.x / band, i = blockIdx.x % band;
+        const int width = nb - 8 * b < 8 ? nb - 8 * b : 8;
+        bn = 8 * b + i % width;
+        bm = i / width;
+    }
+    const int m0 = bm * (ROWS < 16 ? 16 : ROWS);
+    const int U = (a.G + UG - 1) / UG;
+    const int u0 = blockIdx.y * (a.gs / UG);
+    const int u1 = u0 + a.gs / UG < U ? u0 + a.gs / UG : U;
+    const int its = (u1 - u0 + KW - 1) / KW;
+    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+
+    const int64_t last_tile = tiles(a.N) - 1;
+    const uint8_t* wp[R];
+    const uint8_t* sp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        int64_t t = (int64_t)bn * (WN * R) + wn * R + r;
+        if (t > last_tile) t = last_tile;
+        wp[r] = a.w.codes + t * a.G * kCodeBlock;
+        sp[r] = a.w.scales + t * a.Q * kScaleBlock;
+    }
+    uint8_t* mine = lds + kw * 2 * T::kStage;
+    u32x4_t wb[2][UG][R], xb[P];
+    uint32_t ws[2][R], xs[2][XM ? MT : 1];
+    bool xin[P];
+    // (no branch: a place past the last unit, group, row or K is a valid one whose x
+    // is replaced by zeros)
+    auto load = [&](int slot, int it) {
+        const int u = u0 + it * KW + kw;
+        const int uc = u < u1 ? u : u1 - 1;
+        const int64_t so = (int64_t)(uc * UG / 4) * kScaleBlock;
+        const int shift = UG == 4 ? 0 : 8 * UG * (uc % (4 / UG));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            ws[slot][r] = *reinterpret_cast<const uint32_t*>(scalar(sp[r] + so) + lane4) >> shift;
+#pragma unroll
+        for (int j = 0; j < UG; ++j) {
+            const int g = uc * UG + j < a.G ? uc * UG + j : a.G - 1;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                wb[slot][j][r] = load16_nt(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
+        }
+        if constexpr (XM) {
+            const int64_t last = tiles(a.M) - 1;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int64_t tt = m0 / 16 + t < last ? m0 / 16 + t : last;
+                xs[slot][t] = *reinterpret_cast<const uint32_t*>(
+                                  scalar(a.xm.scales + tt * a.Q * kScaleBlock + so) + lane4) >> shift;
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int block = i * WN + wn;          // (tile, group) of the unit
+                const int64_t t = m0 / 16 + block / UG;
+                const int g = u * UG + block % UG;
+                xin[i] = u < u1 && g < a.G;
+                xb[i] = *reinterpret_cast<const u32x4_t*>(
+                    scalar(a.xm.codes + ((t < last ? t : last) * a.G + (g < a.G ? g : a.G - 1)) *
+                                            kCodeBlock) + lane16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int piece = (i * WN + wn) * 64 + lane;
+                int m = m0 + piece / (16 * UG);
+                if (m >= a.M) m = a.M - 1;
+                const int k = u * UG * 128 + piece % (16 * UG) * 8;
+                xin[i] = u < u1 && k < a.K;
+                xb[i] = *reinterpret_cast<const u32x4_t*>(a.x + (int64_t)m * a.ldx +
+                                                          (xin[i] ? k : 0));
+            }
+        }
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int piece = (i * WN + wn) * 64 + lane;
+            int at = piece;
+            if constexpr (!XM) {
+                const int row = piece / (16 * UG), p = piece % (16 * UG);
+                at = row * 16 * UG + (p & ~15) + ((p & 15) ^ (row & 15));
+            }
+            u32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = xin[i] ? xb[i][e] : 0u;
+            *reinterpret_cast<u32x4_t*>(mine + buf * T::kStage + at * 16) = v;
+        }
+    };
+    f32x4_t acc[MT][R];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[t][r] = f32x4_t{0, 0, 0, 0};
+    const int cr = ROWS < 16 ? c & (ROWS - 1) : c;
+    auto product = [&](auto sc) {
+        constexpr int slot = decltype(sc)::value;
+        const uint8_t* xl = mine + slot * T::kStage;
+        if constexpr (XM) {
+            auto group = [&](auto jc) {
+                constexpr int J = decltype(jc)::value;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(
+                        xl + (t * UG + J) * kCodeBlock + lane16);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        acc[t][r] = mfma_mx4<J>(operand4(wb[slot][J][r]), operand4(xv), acc[t][r],
+                                                ws[slot][r], xs[slot][t]);
+                }
+            };
+            group(std::integral_constant<int, 0>{});
+            group(std::integral_constant<int, 1>{});
+            if constexpr (UG == 4) {
+                group(std::integral_constant<int, 2>{});
+                group(std::integral_constant<int, 3>{});
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < UG; ++j) {
+                float s[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) s[r] = scale_f32((ws[slot][r] >> (8 * j)) & 255u);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    bf16x8_t xv[MT];
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        const int row = t * 16 + cr;
+                        xv[t] = *reinterpret_cast<const bf16x8_t*>(
+                            xl + (row * 16 * UG + 16 * j + ((4 * q + b) ^ (row & 15))) * 16);
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const bf16x8_t wv = expand8(wb[slot][j][r][b], s[r]);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) acc[t][r] = mfma_bf16(wv, xv[t], acc[t][r]);
+                    }
+                }
+            }
+        }
+    };
+    load(0, 0);
+    stage(0);
+    __syncthreads();
+    auto step = [&](auto sc, int it) {
+        constexpr int slot = decltype(sc)::value;
+        load(slot ^ 1, it + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        product(sc);
+        __builtin_amdgcn_sched_barrier(0);
+        stage(slot ^ 1);
+        __syncthreads();
+    };
+    for (int it = 0; it < its; it += 2) {
+        step(std::integral_constant<int, 0>{}, it);
+        if (it + 1 >= its) break;
+        step(std::integral_constant<int, 1>{}, it + 1);
+    }
+    __syncthreads();
+
+    // the k groups' sums in their order
+    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][MT][R][256]
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            *reinterpret_cast<f32x4_t*>(red + ((w * MT + t) * R + r) * 256 + lane * 4) = acc[t][r];
+    __syncthreads();
+    constexpr int kCols = 16 * R * WN;
+    for (int i = tid; i < (ROWS < 16 ? ROWS : MT * 16) * kCols; i += T::kThreads) {
+        const int m = i / kCols, col = i % kCols;
+        const int64_t nn = (int64_t)bn * kCols + col;
+        if (m0 + m >= a.M || nn >= a.N) continue;
+        const int v = col / (16 * R), r = col / 16 % R, wr = col & 15, t = m >> 4;
+        const int at = ((v * MT + t) * R + r) * 256 + ((wr >> 2) * 16 + (m & 15)) * 4 + (wr & 3);
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) s += red[k * WN * MT * R * 256 + at];
+        if (a.S > 1)
+            a.part[((int64_t)blockIdx.y * a.M + m0 + m) * a.N + nn] = s;
+        else
+            store_y(a, m0 + m, nn, s);
+    }
 }
 
 // ---- many rows of x -------------------------------------------------------------
@@ -471,6 +688,14 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs a) {
     store_y(a, i / a.N, i % a.N, s);
 }
 
+hipError_t launch_join(const GemmArgs& a, hipStream_t s) {
+    if (a.S > 1) {
+        const int64_t MN = (int64_t)a.M * a.N;
+        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((MN + 255) / 256)), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
 template <int MT, int R, int WM, int WN, bool XM, int MIN_WAVES>
 hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
     using T = Tile<MT, R, WM, WN, XM>;
@@ -479,28 +704,80 @@ hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((tile_kernel<MT, R, WM, WN, XM, MIN_WAVES>),
                        dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S), dim3(T::kThreads), 0, s,
                        a, mb, nb);
-    if (a.S > 1) {
-        const int64_t MN = (int64_t)a.M * a.N;
-        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((MN + 255) / 256)), dim3(256), 0, s, a);
-    }
-    return hipGetLastError();
+    return launch_join(a, s);
+}
+
+template <int ROWS, int R, int WN, int KW, int UG, bool XM>
+hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
+    using T = Mid<ROWS, WN, KW, UG, XM>;
+    static_assert(T::lds(R) <= 65536, "more LDS than a launch gets without asking");
+    constexpr int bm = ROWS < 16 ? 16 : ROWS;
+    const int mb = (a.M + bm - 1) / bm;
+    const int nb = (int)((tiles(a.N) + R * WN - 1) / (R * WN));
+    hipLaunchKernelGGL((mid_kernel<ROWS, R, WN, KW, UG, XM>),
+                       dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S), dim3(T::kThreads),
+                       T::lds(R), s, a, mb, nb);
+    return launch_join(a, s);
 }
 
 // Kernel and split of a product.
+enum Kernel {
+    kSmall, kMid4, kMid4Long, kMid16, kMid16x2, kMid16w, kMid32, kMid32x2, kMid64,
+    kTile64, kTileMid, kTile128
+};
 struct Plan {
-    int bm;                 // rows of x a workgroup: 16 (few-row kernel), 32 .. 256
-    int S, gs;
+    Kernel kernel;
+    int S, gs;              // K slices, groups a slice (a multiple of 4)
 };
 
-Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool x_mx4) {
-    Plan p{16, 1, (int)groups(K)};
-    if (M <= 16) return p;
-    p.bm = M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    if (x_mx4 && M > 128) p.bm = 256;
-    const int64_t bn = p.bm >= 128 ? 256 : 128;
-    const int64_t blocks = (M + p.bm - 1) / p.bm * ((N + bn - 1) / bn);
-    const int Q = (int)quads(K);
-    int64_t S = 512 / blocks;
+// By rows of x (M), tiles of 16 weight rows (nt) and groups of K (G).  Measured on
+// QKV (nt = 448, G = 40), gate+up (2176, 40) and down (320, 136), us:
+//   up to 16 rows, BF16 x: every wave on its own x for few tiles (QKV M = 1 6.9 against
+//     7.8 through LDS, M = 16 9.8 against 11.1); shared through LDS for many tiles
+//     (gate+up M = 1 18.5 against 22.1, M = 16 27.1 against 29.2) or a long K (down
+//     M = 1 14.3 against 15.6, M = 16, K in four slices, 19.1 against 23.5).  MX4 x
+//     is a quarter of the bytes: shared or not within 3%.
+//   17 rows to 128 (MX4 x: 256) and few tiles: 16 (32, 64) rows a workgroup, whose
+//     weights the row blocks beside it find in L2 (QKV M = 64 16.3, M = 128 22.3; a
+//     64 x 128 tile in four slices 21.2 and 24.9).
+//   above: the largest tile that still gives 440 workgroups (QKV M = 512 44.8 with
+//     64 x 128 tiles, 52.5 with 128 x 256; M = 2048 the reverse), K in slices if the
+//     smallest does not.
+Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
+    const int G = (int)groups(K), Q = (int)quads(K);
+    const int64_t nt = tiles(N);
+    const bool many = nt >= 1024, lengthy = G >= 64;
+    const auto blocks = [&](int64_t bm, int64_t bn) {
+        return (M + bm - 1) / bm * ((N + bn - 1) / bn);
+    };
+    Plan p{kSmall, 1, 4 * Q};
+    int64_t S = 1;
+    const auto slices = [](int64_t want, int64_t have) { return (want + have / 2) / have; };
+    if (M <= 16) {
+        if (xm || (!many && !lengthy)) {
+            p.kernel = kSmall;
+        } else if (M <= 4) {
+            p.kernel = many ? kMid4 : kMid4Long;
+        } else {
+            p.kernel = kMid16;
+            S = slices(320, blocks(16, 64));
+        }
+    } else if (xm && (M <= 64 || (M <= 256 && !many))) {
+        p.kernel = many ? (M <= 32 ? kMid32 : kMid64) : lengthy || M > 64 ? kMid64 : kMid32x2;
+        if (lengthy) S = slices(400, blocks(64, 64));
+    } else if (!xm && !many && M <= (lengthy ? 64 : 128)) {
+        p.kernel = lengthy ? kMid16w : M <= 32 ? kMid16x2 : M <= 64 ? kMid16 : kMid16w;
+        if (lengthy) S = slices(480, blocks(16, 128));
+    } else if (!xm && M <= 32) {
+        p.kernel = kMid32;
+    } else if (blocks(128, 256) >= 440) {
+        p.kernel = kTile128;
+    } else if (xm ? blocks(128, 128) >= 440 : blocks(64, 256) >= 440) {
+        p.kernel = kTileMid;
+    } else {
+        p.kernel = kTile64;
+        S = slices(544, blocks(64, 128));
+    }
     if (S > Q) S = Q;
     if (S < 1) S = 1;
     const int qs = (int)((Q + S - 1) / S);      // quads a slice
@@ -523,17 +800,30 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     a.S = p.S;
     a.gs = p.gs;
     a.part = static_cast<float*>(ws);
+    Kernel k = p.kernel;
     // the tile kernel's row offsets are products of 24-bit numbers
-    const int bm = !xm && a.ldx >= (1 << 23) ? 16 : p.bm;
-    switch (bm) {
-        case 32:
-            return xm ? launch_tile<2, 2, 1, 4, true, 2>(a, s) : launch_tile<2, 2, 1, 4, false, 2>(a, s);
-        case 64:
-            return xm ? launch_tile<4, 2, 1, 4, true, 2>(a, s) : launch_tile<4, 2, 1, 4, false, 2>(a, s);
-        case 128:
-            return xm ? launch_tile<8, 4, 1, 4, true, 2>(a, s) : launch_tile<8, 4, 1, 4, false, 2>(a, s);
-        case 256: return launch_tile<8, 4, 2, 4, true, 2>(a, s);
-        default: return launch_small<1, 8, 4>(a, s);
+    if (!xm && k >= kTile64 && a.ldx >= (1 << 23)) k = kSmall;
+    if (k == kSmall) a.S = 1;
+    if (xm) switch (k) {
+        case kMid32: return launch_mid<32, 1, 4, 1, 4, true>(a, s);
+        case kMid32x2: return launch_mid<32, 1, 4, 2, 4, true>(a, s);
+        case kMid64: return launch_mid<64, 1, 4, 1, 4, true>(a, s);
+        case kTile64: return launch_tile<4, 2, 1, 4, true, 2>(a, s);
+        case kTileMid: return launch_tile<8, 2, 1, 4, true, 2>(a, s);
+        case kTile128: return launch_tile<8, 4, 1, 4, true, 2>(a, s);
+        default: return launch_small<2, 8, 2, true>(a, s);
+    }
+    switch (k) {
+        case kMid4: return launch_mid<4, 1, 2, 2, 2, false>(a, s);
+        case kMid4Long: return launch_mid<4, 1, 1, 4, 4, false>(a, s);
+        case kMid16: return launch_mid<16, 1, 4, 1, 4, false>(a, s);
+        case kMid16x2: return launch_mid<16, 1, 4, 2, 4, false>(a, s);
+        case kMid16w: return launch_mid<16, 1, 8, 1, 4, false>(a, s);
+        case kMid32: return launch_mid<32, 2, 8, 1, 4, false>(a, s);
+        case kTile64: return launch_tile<4, 2, 1, 4, false, 2>(a, s);
+        case kTileMid: return launch_tile<4, 4, 1, 4, false, 2>(a, s);
+        case kTile128: return launch_tile<8, 4, 1, 4, false, 2>(a, s);
+        default: return launch_small<2, 4, 3, false>(a, s);
     }
 }
 
