@@ -182,7 +182,7 @@ int mx4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
     *bytes = 0;
     if (type_bytes(y_type) == 0) return W12_ERR_DTYPE;
     if (int rc = check_moe_shape(T, H, I, E, top_k)) return rc;
-    if (T > 0) *bytes = mx4::moe_workspace_bytes(T, I, E, top_k, y_type == W12_OUT_F32);
+    if (T > 0) *bytes = mx4::moe_workspace_bytes(T, H, I, E, top_k, y_type == W12_OUT_F32);
     return W12_OK;
 }
 
@@ -201,7 +201,7 @@ int mx4_moe(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int6
         !aligned(w2_codes, 16) || !aligned(w2_scales, 16))
         return W12_ERR_ALIGN;
     size_t need = 0;
-    if (T > 0) need = mx4::moe_workspace_bytes(T, I, E, top_k, y_type == W12_OUT_F32);
+    if (T > 0) need = mx4::moe_workspace_bytes(T, H, I, E, top_k, y_type == W12_OUT_F32);
     if (int rc = check_ws(workspace, workspace_bytes, need)) return rc;
     if (T == 0) return W12_OK;
     mx4::MoeArgs a{};

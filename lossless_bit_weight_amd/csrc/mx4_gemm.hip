@@ -164,13 +164,6 @@ hipError_t launch_small(GemmArgs a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// A uniform pointer the compiler keeps in scalar registers: folded with the lane's
-// offset it would hold two vector registers through the loop.
-__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
-    asm volatile("" : "+s"(p));
-    return p;
-}
-
 // ---- a few rows of x, shared through LDS ------------------------------------------
 // A workgroup: ROWS rows of x (4, or 16 and more) by 16 R WN weight rows; KW
 // groups of WN waves take every KW-th unit of UG groups of K.  A unit's weights

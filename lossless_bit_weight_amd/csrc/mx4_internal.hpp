@@ -68,6 +68,13 @@ __device__ __forceinline__ u32x4_t load16_nt(const uint8_t* p) {
     return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
 }
 
+// A uniform pointer the compiler keeps in scalar registers: folded with the lane's
+// offset it would hold two vector registers through the loop.
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 // fp32 -> BF16 bits, to nearest even (NaN stays NaN).
 __device__ __forceinline__ uint16_t bf16_bits(float f) {
     const __bf16 h = (__bf16)f;
@@ -101,10 +108,10 @@ constexpr int kMaxTokens = 128;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 
-// Up to 16 of the pairs (token, chosen expert) of one expert.
-struct MoeSlot {
-    int e, p0, count, pad;
-};
+// Up to 16 of the pairs (token, chosen expert) of one expert: words [0] the
+// expert, [1] their number (0: none, nothing to do), [2] the first pair's place
+// among all, [16 + i] the i-th pair's token (past the last: the first's).
+constexpr int kSlotWords = 32;
 
 struct MoeArgs {
     const uint16_t* x;
@@ -118,14 +125,14 @@ struct MoeArgs {
     int y_f32;
     int max_slots;          // min(E, pairs) + pairs / 16
     // workspace: the pairs in the order of (expert, token), cut into slots
-    int* n_slots;
-    MoeSlot* slots;
-    int* pair_token;
-    float* pair_p;
+    int* slots;             // [max_slots][kSlotWords]
+    int* place;             // [T][top_k] place of token t's j-th pair, or -1
+    float* share;           // [T][top_k]
+    float* out;             // [pairs][H] an expert's output for a token
     uint16_t* h;            // [parts][pairs][I], hidden values as sums of BF16 parts
 };
 
-size_t moe_workspace_bytes(int64_t T, int64_t I, int64_t E, int64_t top_k, bool y_f32);
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bool y_f32);
 // Point the workspace fields of `a` at `ws` (moe_workspace_bytes) and launch.
 hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s);
 

@@ -1,13 +1,15 @@
 // mx4_moe.hip -- a mixture-of-experts layer for a few tokens on MX4 weights
 // (../../include/mx4.h states the operation).
 //
-// Three launches.  route: each token's experts and their shares, and the pairs
+// Four launches.  route: each token's experts and their shares, and the pairs
 // (token, expert) sorted by expert and cut into slots of at most 16.  up: per
-// slot and 16 hidden values the products with the gate and the up rows and
-// h = silu(g) * u.  down: per 16 R outputs all slots' products with h, weighted
-// and added per token.  The chosen experts' weights are read once (an expert
-// with more than 16 tokens: once a slot, the later reads from cache), which is
-// what bounds the layer; everything else is smaller by T / 1000 or so.
+// slot the products with the gate and up rows and h = silu(g) * u.  down: per
+// slot the products of h with the down rows.  join: each token's weighted sum.
+// The chosen experts' weights are read once (an expert with more than 16 tokens:
+// once a slot, the later reads from cache), which is what bounds the layer;
+// activations and pair outputs are hundredths of them.
+#include <type_traits>
+
 #include "mx4_internal.hpp"
 
 namespace mx4 {
@@ -25,13 +27,22 @@ __device__ __forceinline__ uint32_t order_key(float l) {
 }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;    // order_key(-inf)
 
+// Largest value of the wave, in every lane: within rows of 16 lanes, across them,
+// then read from the last lane (a lane without a source keeps its own value).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
+    const auto step = [&](auto ctrl) {
+        constexpr int C = decltype(ctrl)::value;
+        const uint32_t o =
+            (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, C, 0xF, 0xF, false);
         v = v > o ? v : o;
-    }
-    return v;
+    };
+    step(std::integral_constant<int, 0x111>{});     // row_shr:1
+    step(std::integral_constant<int, 0x112>{});     // row_shr:2
+    step(std::integral_constant<int, 0x114>{});     // row_shr:4
+    step(std::integral_constant<int, 0x118>{});     // row_shr:8
+    step(std::integral_constant<int, 0x142>{});     // row_bcast:15
+    step(std::integral_constant<int, 0x143>{});     // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -40,16 +51,16 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // One workgroup.  A wave takes a token: lane l holds the logits of the experts
-// l, l + 64, ...; top_k rounds find the largest key (ties: the lowest expert)
-// and strike it out.  Tokens per expert are kept as 128-bit sets, so the sorted
-// place of a pair is a count of bits and depends on no order of execution.
+// EV l .. EV l + EV - 1, so that the lowest lane of a tie has the lowest expert;
+// top_k rounds find the largest key and strike it out.  Tokens per expert are
+// kept as 128-bit sets, so the sorted place of a pair is a count of bits and
+// depends on no order of execution.
 template <int EV>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
     __shared__ uint32_t set[kMaxExperts][4];
     __shared__ int base[kMaxExperts];
     __shared__ int wave_tot[2][kRouteThreads / 64];
     __shared__ uint16_t chosen[kMaxTokens * kMaxTopK];
-    __shared__ float share[kMaxTokens * kMaxTopK];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     for (int i = tid; i < a.E * 4; i += kRouteThreads) (&set[0][0])[i] = 0;
     __syncthreads();
@@ -59,33 +70,33 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
         float l[EV];
 #pragma unroll
         for (int i = 0; i < EV; ++i) {
-            const int e = lane + 64 * i;
+            const int e = EV * lane + i;
             l[i] = e < a.E ? a.logits[t * a.ldl + e] : -__builtin_inff();
             key[i] = e < a.E ? order_key(l[i]) : 0u;
         }
         float top = 0.f, mine = 0.f;    // the largest logit; lane j: the j-th chosen one
         int mine_e = -1;
         for (int j = 0; j < a.top_k; ++j) {
-            uint32_t best = 0;
-            int be = 0;
+            uint32_t best = key[0];
+            int at = 0;
+            float v = l[0];
 #pragma unroll
-            for (int i = 0; i < EV; ++i)
+            for (int i = 1; i < EV; ++i)
                 if (key[i] > best) {
                     best = key[i];
-                    be = lane + 64 * i;
+                    at = i;
+                    v = l[i];
                 }
             const uint32_t m = wave_max(best);
             if (m <= kKeyNegInf) break;     // only -inf (or nothing) left
-            // the lowest expert with that key
-            const int e = (int)~wave_max(best == m ? ~(uint32_t)be : 0u);
-            float v = 0.f;
+            const int src = __builtin_ctzll(__ballot(best == m));
+            const int e = EV * src + __builtin_amdgcn_readlane(at, src);
+            v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), src));
+            if (lane == src) {
 #pragma unroll
-            for (int i = 0; i < EV; ++i)
-                if (e == lane + 64 * i) {
-                    key[i] = 0;
-                    v = l[i];
-                }
-            v = __shfl(v, e & 63);
+                for (int i = 0; i < EV; ++i)
+                    if (i == at) key[i] = 0;
+            }
             if (j == 0) top = v;
             if (lane == j) {
                 mine = v;
@@ -105,17 +116,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
         }
         if (lane < a.top_k) {
             chosen[t * a.top_k + lane] = (uint16_t)(mine_e < 0 ? 0xFFFF : mine_e);
-            share[t * a.top_k + lane] = mine_e < 0 ? 0.f : ex / sum;
+            a.share[t * a.top_k + lane] = mine_e < 0 ? 0.f : ex / sum;
             if (mine_e >= 0) atomicOr(&set[mine_e][t >> 5], 1u << (t & 31));
         }
     }
     __syncthreads();
 
     // exclusive sums over the experts of their pairs and slots
+    uint32_t mask[4] = {0, 0, 0, 0};
     int cnt = 0;
     if (tid < a.E) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cnt += __popc(set[tid][i]);
+        for (int i = 0; i < 4; ++i) {
+            mask[i] = set[tid][i];
+            cnt += __popc(mask[i]);
+        }
     }
     const int ns = (cnt + 15) >> 4;
     int ip = cnt, is = ns;
@@ -132,277 +147,278 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
         wave_tot[1][w] = is;
     }
     __syncthreads();
-    for (int i = 0; i < w; ++i) {
-        ip += wave_tot[0][i];
-        is += wave_tot[1][i];
+    int total = 0;
+    for (int i = 0; i < kRouteThreads / 64; ++i) {
+        if (i < w) {
+            ip += wave_tot[0][i];
+            is += wave_tot[1][i];
+        }
+        total += wave_tot[1][i];
     }
     if (tid < a.E) {
         base[tid] = ip - cnt;
+        int word = 0, first = 0;
         for (int i = 0; i < ns; ++i) {
-            const int left = cnt - 16 * i;
-            a.slots[is - ns + i] = MoeSlot{tid, ip - cnt + 16 * i, left < 16 ? left : 16, 0};
+            int* s = a.slots + (is - ns + i) * kSlotWords;
+            const int n = cnt - 16 * i < 16 ? cnt - 16 * i : 16;
+            s[0] = tid;
+            s[1] = n;
+            s[2] = ip - cnt + 16 * i;
+            for (int j = 0; j < 16; ++j) {
+                if (j < n) {
+                    while (mask[word] == 0) ++word;
+                    const int t = 32 * word + __builtin_ctz(mask[word]);
+                    mask[word] &= mask[word] - 1;
+                    if (j == 0) first = t;
+                    s[16 + j] = t;
+                } else {
+                    s[16 + j] = first;
+                }
+            }
         }
     }
-    if (tid == kRouteThreads - 1) a.n_slots[0] = is;
+    for (int i = total + tid; i < a.max_slots; i += kRouteThreads) a.slots[i * kSlotWords + 1] = 0;
     __syncthreads();
 
     for (int i = tid; i < a.T * a.top_k; i += kRouteThreads) {
         const int e = chosen[i];
-        if (e == 0xFFFF) continue;
-        const int t = i / a.top_k;
-        int p = base[e];
-        for (int j = 0; j < (t >> 5); ++j) p += __popc(set[e][j]);
-        p += __popc(set[e][t >> 5] & ((1u << (t & 31)) - 1u));
-        a.pair_token[p] = t;
-        a.pair_p[p] = share[i];
+        int p = -1;
+        if (e != 0xFFFF) {
+            const int t = i / a.top_k;
+            p = base[e];
+            for (int j = 0; j < (t >> 5); ++j) p += __popc(set[e][j]);
+            p += __popc(set[e][t >> 5] & ((1u << (t & 31)) - 1u));
+        }
+        a.place[i] = p;
     }
 }
 
-// ---- gate and up ------------------------------------------------------------------
-// A workgroup: one slot, 16 gate rows and the 16 up rows beside them; KW waves
-// split H, D groups in flight, operands as in mx4_gemm.hip's few-row kernel.
-template <int KW, int D, int PARTS>
-__global__ __launch_bounds__(KW * 64) void up_kernel(MoeArgs a) {
-    __shared__ f32x4_t red[KW][2][64];
-    const int it = a.I / 16;
-    const int slot = blockIdx.x / it, j = blockIdx.x % it;
-    if (slot >= a.n_slots[0]) return;
-    const MoeSlot sl = a.slots[slot];
-    const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// ---- the experts' products -----------------------------------------------------------
+// A workgroup: one slot by WN waves' weight tiles (up: a gate tile and the up tile
+// beside it a wave; down: R tiles); KW groups of such waves take every KW-th unit
+// of UG groups of K.  Weights come to registers a unit ahead of their products;
+// the slot's rows (of x, gathered by token, or of h in PARTS parts) go through
+// LDS, double-buffered, in the layout of mx4_gemm.hip's few-row kernel, ROWS of
+// them: slots of up to four rows, the most by far, move a quarter of the bytes.
+template <bool UP, int PARTS, int R, int WN, int KW, int UG>
+struct Expert {
+    static constexpr int kThreads = WN * KW * 64;
+    static constexpr int pieces(int rows) { return rows * 16 * UG * PARTS; }
+    static constexpr int stage(int rows) {
+        return (pieces(rows) + WN * 64 - 1) / (WN * 64) * (WN * 64) * 16;
+    }
+    static constexpr int lds(int rows) {
+        const int x = 2 * KW * stage(rows), red = KW * WN * R * 1024;
+        return x > red ? x : red;
+    }
+};
+
+template <int ROWS, bool UP, int PARTS, int R, int WN, int KW, int UG>
+__device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, int e, int count,
+                                            int p0, int block, uint8_t* lds) {
+    using X = Expert<UP, PARTS, R, WN, KW, UG>;
+    constexpr int kStage = X::stage(ROWS), P = kStage / (WN * 64 * 16);
+    constexpr int kPart = ROWS * 16 * UG;       // pieces of one part of a unit
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kw = w / WN, wn = w % WN;
     const int c = lane & 15, q = lane >> 4;
-    const int G = (int)groups(a.H), Q = (int)quads(a.H);
-    const int g0 = G * w / KW, n = G * (w + 1) / KW - g0;
-
-    const uint8_t* wp[2];
-    const uint8_t* sp[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int64_t t = (int64_t)sl.e * 2 * it + r * it + j;
-        wp[r] = a.w13.codes + t * G * kCodeBlock + lane * 16;
-        sp[r] = a.w13.scales + t * Q * kScaleBlock + lane * 4;
-    }
-    const bool row = c < sl.count;
-    const uint16_t* xp = a.x + (row ? a.pair_token[sl.p0 + c] : 0) * a.ldx + 32 * q;
-
-    u32x4_t wb[D][2], xb[D][4];
-    uint32_t ws[D][2];
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) xb[d][b] = u32x4_t{0, 0, 0, 0};
-    auto load = [&](int d, int g) {
-        const int64_t so = (int64_t)(g >> 2) * kScaleBlock + (g & 3);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            wb[d][r] = load16_nt(wp[r] + (int64_t)g * kCodeBlock);
-            ws[d][r] = sp[r][so];
-        }
-        if (g == G - 1) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) xb[d][b] = u32x4_t{0, 0, 0, 0};
-        }
-        if (row && 128 * g + 32 * q < a.H) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                xb[d][b] = *reinterpret_cast<const u32x4_t*>(xp + 128 * (int64_t)g + 8 * b);
-        }
-    };
-    f32x4_t acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    auto product = [&](int d) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float s = scale_f32(ws[d][r]);
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                acc[r] = mfma_bf16(expand8(wb[d][r][b], s),
-                                   __builtin_bit_cast(bf16x8_t, xb[d][b]), acc[r]);
-        }
-    };
-    if (n > 0) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) load(d, g0 + (d < n ? d : n - 1));
-        int i = 0;
-        for (; i + 2 * D <= n; i += D) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                product(d);
-                load(d, g0 + i + D + d);
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (i + d < n) product(d);
-            if (i + D + d < n) load(d, g0 + i + D + d);
-        }
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            if (i + D + d < n) product(d);
-    }
-    red[w][0][lane] = acc[0];
-    red[w][1][lane] = acc[1];
-    __syncthreads();
-    const float* rf = reinterpret_cast<const float*>(red);
+    const int K = UP ? a.H : a.I;
+    const int G = (int)groups(K), Q = (int)quads(K);
+    const int U = (G + UG - 1) / UG, its = (U + KW - 1) / KW;
+    const int nt = (UP ? a.I : a.H) / 16;       // tiles of this product's outputs
+    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
     const int64_t pairs = (int64_t)a.T * a.top_k;
-    for (int i = threadIdx.x; i < 256; i += KW * 64) {
-        const int m = i >> 4, wr = i & 15;
-        if (m >= sl.count) continue;
-        const int at = ((wr >> 2) * 16 + m) * 4 + (wr & 3);
-        float g = 0.f, u = 0.f;
-#pragma unroll
-        for (int v = 0; v < KW; ++v) {
-            g += rf[v * 512 + at];
-            u += rf[v * 512 + 256 + at];
-        }
-        const float h = g / (1.f + expf(-g)) * u;
-        uint16_t* o = a.h + (int64_t)(sl.p0 + m) * a.I + 16 * j + wr;
-        // h = the sum of PARTS BF16 numbers, each the rounded rest of those before: two
-        // hold 16 bits of its mantissa, three all 24
-        float rest = h;
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-            const uint16_t b = bf16_bits(rest);
-            o[(int64_t)p * pairs * a.I] = b;
-            const float f = __uint_as_float((uint32_t)b << 16);
-            rest = __builtin_isfinite(f) ? rest - f : 0.f;
-        }
-    }
-}
 
-// ---- down ---------------------------------------------------------------------------
-// A workgroup: 16 R outputs for all tokens.  The work (slot, group of 128 hidden
-// values) is one sequence, cut into KW equal runs, one a wave; a wave adds each
-// slot's product, weighted, to its own sums in LDS [token][16 R], and the
-// waves' sums are added in wave order.
-template <int R, int KW, int D, int PARTS>
-__global__ __launch_bounds__(KW * 64) void down_kernel(MoeArgs a) {
-    extern __shared__ float sums[];         // [KW][T][16 R]
-    const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = lane & 15, q = lane >> 4;
-    const int G = (int)groups(a.I), Q = (int)quads(a.I);
-    const int ht = a.H / 16;
-    const int tile0 = blockIdx.x * R;
-    const int n_slots = __builtin_amdgcn_readfirstlane(a.n_slots[0]);
-    const int items = n_slots * G;
-    const int i0 = (int)((int64_t)items * w / KW), n = (int)((int64_t)items * (w + 1) / KW) - i0;
-    const int64_t pairs = (int64_t)a.T * a.top_k;
-    float* mine = sums + (int64_t)w * a.T * 16 * R;
-    for (int i = lane; i < a.T * 16 * R; i += 64) mine[i] = 0.f;
-
-    u32x4_t wb[D][R], hb[D][PARTS][4];
-    uint32_t ws[D][R];
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) hb[d][p][b] = u32x4_t{0, 0, 0, 0};
-
-    // the slot and group that is loaded next, and its pointers
-    int ls = i0 / G, lg = i0 % G;
     const uint8_t* wp[R];
     const uint8_t* sp[R];
-    const uint16_t* hp = nullptr;
-    bool row = false;
-    auto enter = [&]() {
-        const MoeSlot sl = a.slots[ls];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int tt = tile0 + r < ht ? tile0 + r : ht - 1;
-            const int64_t t = (int64_t)sl.e * ht + tt;
-            wp[r] = a.w2.codes + t * G * kCodeBlock + lane * 16;
-            sp[r] = a.w2.scales + t * Q * kScaleBlock + lane * 4;
+    for (int r = 0; r < R; ++r) {
+        int64_t t;
+        if constexpr (UP) {
+            const int j = block * WN + wn;
+            t = (int64_t)e * 2 * nt + r * nt + (j < nt ? j : nt - 1);
+        } else {
+            const int j = (block * WN + wn) * R + r;
+            t = (int64_t)e * nt + (j < nt ? j : nt - 1);
         }
-        row = c < sl.count;
-        hp = a.h + (int64_t)(sl.p0 + (row ? c : 0)) * a.I + 32 * q;
+        const Mat& m = UP ? a.w13 : a.w2;
+        wp[r] = m.codes + t * G * kCodeBlock;
+        sp[r] = m.scales + t * Q * kScaleBlock;
+    }
+    const uint16_t* xp[P];
+    int xk[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int piece = (i * WN + wn) * 64 + lane;
+        int part = piece / kPart;
+        if (part > PARTS - 1) part = PARTS - 1;
+        const int row = piece % kPart / (16 * UG);
+        if constexpr (UP)
+            xp[i] = a.x + (int64_t)slot[16 + row] * a.ldx;
+        else
+            xp[i] = a.h + (part * pairs + p0 + (row < count ? row : 0)) * (int64_t)a.I;
+        xk[i] = piece % (16 * UG) * 8;
+    }
+    uint8_t* mine = lds + kw * 2 * kStage;
+    u32x4_t wb[2][UG][R], xb[P];
+    uint32_t ws[2][R];
+    bool xin[P];
+    // (no branch: a place past the last unit, group or K is a valid one whose x is
+    // replaced by zeros)
+    auto load = [&](int s, int it) {
+        const int u = it * KW + kw;
+        const int uc = u < U ? u : U - 1;
+        const int64_t so = (int64_t)(uc * UG / 4) * kScaleBlock;
+        const int shift = UG == 4 ? 0 : 8 * UG * (uc % (4 / UG));
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            ws[s][r] = *reinterpret_cast<const uint32_t*>(scalar(sp[r] + so) + lane4) >> shift;
+#pragma unroll
+        for (int j = 0; j < UG; ++j) {
+            const int g = uc * UG + j < G ? uc * UG + j : G - 1;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                wb[s][j][r] = load16_nt(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int k = u * UG * 128 + xk[i];
+            xin[i] = u < U && k < K;
+            xb[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[i] ? k : 0));
+        }
     };
-    auto load = [&](int d) {
-        const int g = lg;
-        const int so = (g >> 2) * kScaleBlock + (g & 3);
+    auto stage = [&](int buf) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            wb[d][r] = load16_nt(wp[r] + (int64_t)g * kCodeBlock);
-            ws[d][r] = sp[r][so];
-        }
+        for (int i = 0; i < P; ++i) {
+            const int piece = (i * WN + wn) * 64 + lane;
+            const int row = piece % kPart / (16 * UG);
+            const int at = (piece & ~15) + ((piece & 15) ^ (row & 15));
+            u32x4_t v;
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                hb[d][p][b] = u32x4_t{0, 0, 0, 0};
-                if (row && 128 * g + 32 * q < a.I)
-                    hb[d][p][b] = *reinterpret_cast<const u32x4_t*>(hp + p * pairs * a.I +
-                                                                   128 * g + 8 * b);
-            }
-        if (++lg == G) {
-            lg = 0;
-            if (++ls < n_slots) enter();
+            for (int k = 0; k < 4; ++k) v[k] = xin[i] ? xb[i][k] : 0u;
+            *reinterpret_cast<u32x4_t*>(mine + buf * kStage + at * 16) = v;
         }
     };
     f32x4_t acc[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
-    int cs = ls, cg = lg;                    // the slot and group that is multiplied next
-    auto flush = [&]() {
-        const MoeSlot sl = a.slots[cs];
-        if (c < sl.count) {
-            const int t = a.pair_token[sl.p0 + c];
-            const float p = a.pair_p[sl.p0 + c];
+    const int row = c & (ROWS - 1);
+    auto product = [&](auto sc) {
+        constexpr int s = decltype(sc)::value;
+        const uint8_t* xl = mine + s * kStage;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                f32x4_t* o = reinterpret_cast<f32x4_t*>(mine + (t * R + r) * 16 + 4 * q);
-                f32x4_t v = *o;
+        for (int j = 0; j < UG; ++j) {
+            float f[R];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += p * acc[r][i];
-                *o = v;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
-    };
-    auto product = [&](int d, bool end) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float s = scale_f32(ws[d][r]);
+            for (int r = 0; r < R; ++r) f[r] = scale_f32((ws[s][r] >> (8 * j)) & 255u);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const bf16x8_t wv = expand8(wb[d][r][b], s);
+                bf16x8_t xv[PARTS];
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
-                    acc[r] = mfma_bf16(wv, __builtin_bit_cast(bf16x8_t, hb[d][p][b]), acc[r]);
+                    xv[p] = *reinterpret_cast<const bf16x8_t*>(
+                        xl + (p * kPart + row * 16 * UG + 16 * j + ((4 * q + b) ^ row)) * 16);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const bf16x8_t wv = expand8(wb[s][j][r][b], f[r]);
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p) acc[r] = mfma_bf16(wv, xv[p], acc[r]);
+                }
             }
-        }
-        if (++cg == G || end) {
-            flush();
-            cg = 0;
-            ++cs;
         }
     };
-    if (n > 0) {
-        enter();
-#pragma unroll
-        for (int d = 0; d < D; ++d)
-            if (d < n) load(d);
-        for (int i = 0; i < n; i += D) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (i + d < n) product(d, i + d + 1 == n);
-                if (i + D + d < n) load(d);
-            }
-        }
+    load(0, 0);
+    stage(0);
+    __syncthreads();
+    auto step = [&](auto sc, int it) {
+        constexpr int s = decltype(sc)::value;
+        load(s ^ 1, it + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        product(sc);
+        __builtin_amdgcn_sched_barrier(0);
+        stage(s ^ 1);
+        __syncthreads();
+    };
+    for (int it = 0; it < its; it += 2) {
+        step(std::integral_constant<int, 0>{}, it);
+        if (it + 1 >= its) break;
+        step(std::integral_constant<int, 1>{}, it + 1);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.T * 16 * R; i += KW * 64) {
-        const int t = i / (16 * R), col = i % (16 * R);
-        const int64_t hcol = (int64_t)tile0 * 16 + col;
-        if (hcol >= a.H) continue;
-        float s = 0.f;
+
+    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][R][256]
 #pragma unroll
-        for (int v = 0; v < KW; ++v) s += sums[(int64_t)v * a.T * 16 * R + i];
+    for (int r = 0; r < R; ++r)
+        *reinterpret_cast<f32x4_t*>(red + (w * R + r) * 256 + lane * 4) = acc[r];
+    __syncthreads();
+    constexpr int kCols = UP ? 16 * WN : 16 * R * WN;
+    for (int i = tid; i < ROWS * kCols; i += X::kThreads) {
+        const int m = i / kCols, col = i % kCols;
+        const int n = block * kCols + col, wr = col & 15;
+        if (m >= count || n >= nt * 16) continue;
+        const int in = ((wr >> 2) * 16 + m) * 4 + (wr & 3);
+        if constexpr (UP) {
+            const int at = col / 16 * R * 256 + in;
+            float g = 0.f, u = 0.f;
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                g += red[k * WN * R * 256 + at];
+                u += red[k * WN * R * 256 + 256 + at];
+            }
+            const float h = g / (1.f + expf(-g)) * u;
+            uint16_t* o = a.h + (int64_t)(p0 + m) * a.I + n;
+            // h = the sum of BF16 numbers, each the rounded rest of those before: two hold
+            // 16 bits of its mantissa, three all 24
+            const int parts = a.y_f32 ? 3 : 2;
+            float rest = h;
+            for (int p = 0; p < parts; ++p) {
+                const uint16_t b = bf16_bits(rest);
+                o[p * pairs * a.I] = b;
+                const float f = __uint_as_float((uint32_t)b << 16);
+                rest = __builtin_isfinite(f) ? rest - f : 0.f;
+            }
+        } else {
+            const int at = col / 16 * 256 + in;
+            float s = 0.f;
+#pragma unroll
+            for (int k = 0; k < KW; ++k) s += red[k * WN * R * 256 + at];
+            a.out[(int64_t)(p0 + m) * a.H + n] = s;
+        }
+    }
+}
+
+template <bool MANY, bool UP, int PARTS, int R, int WN, int KW, int UG>
+__global__ __launch_bounds__(WN* KW * 64) void expert_kernel(MoeArgs a, int blocks) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int* slot = a.slots + (blockIdx.x / blocks) * kSlotWords;
+    const int e = slot[0], count = slot[1], p0 = slot[2], block = blockIdx.x % blocks;
+    if (count == 0) return;
+    if (MANY && count > 4)
+        expert_body<16, UP, PARTS, R, WN, KW, UG>(a, slot, e, count, p0, block, lds);
+    else
+        expert_body<4, UP, PARTS, R, WN, KW, UG>(a, slot, e, count, p0, block, lds);
+}
+
+// y[t] = sum of its experts' outputs, weighted, in the order of their choice.
+__global__ __launch_bounds__(256) void join_kernel(MoeArgs a) {
+    const int n = (blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
+    if (n >= a.H) return;
+    f32x4_t s = {0, 0, 0, 0};
+    for (int j = 0; j < a.top_k; ++j) {
+        const int p = a.place[t * a.top_k + j];
+        if (p < 0) continue;
+        const float f = a.share[t * a.top_k + j];
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.out + (int64_t)p * a.H + n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += f * v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
         if (a.y_f32)
-            static_cast<float*>(a.y)[t * a.ldy + hcol] = s;
+            static_cast<float*>(a.y)[t * a.ldy + n + i] = s[i];
         else
-            static_cast<uint16_t*>(a.y)[t * a.ldy + hcol] = bf16_bits(s);
+            static_cast<uint16_t*>(a.y)[t * a.ldy + n + i] = bf16_bits(s[i]);
     }
 }
 
@@ -413,26 +429,41 @@ int64_t max_slots(int64_t T, int64_t E, int64_t top_k) {
     return (E < pairs ? E : pairs) + pairs / 16;
 }
 
+template <bool UP, int PARTS, int R, int WN, int KW, int UG>
+void launch_expert(const MoeArgs& a, hipStream_t s) {
+    using X = Expert<UP, PARTS, R, WN, KW, UG>;
+    static_assert(X::lds(16) <= 65536, "more LDS than a launch gets without asking");
+    const int nt = (UP ? a.I : a.H) / 16, per = UP ? WN : WN * R;
+    const int blocks = (nt + per - 1) / per;
+    const dim3 grid((unsigned)((int64_t)a.max_slots * blocks)), block(X::kThreads);
+    if (a.T <= 4)
+        hipLaunchKernelGGL((expert_kernel<false, UP, PARTS, R, WN, KW, UG>), grid, block, X::lds(4),
+                           s, a, blocks);
+    else
+        hipLaunchKernelGGL((expert_kernel<true, UP, PARTS, R, WN, KW, UG>), grid, block, X::lds(16),
+                           s, a, blocks);
+}
+
 }  // namespace
 
-size_t moe_workspace_bytes(int64_t T, int64_t I, int64_t E, int64_t top_k, bool y_f32) {
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bool y_f32) {
     const int64_t pairs = T * top_k;
-    return 256 + up256((size_t)max_slots(T, E, top_k) * sizeof(MoeSlot)) +
-           2 * up256((size_t)pairs * 4) + (size_t)(y_f32 ? 3 : 2) * pairs * I * 2;
+    return up256((size_t)max_slots(T, E, top_k) * kSlotWords * 4) + 2 * up256((size_t)pairs * 4) +
+           up256((size_t)pairs * H * 4) + (size_t)(y_f32 ? 3 : 2) * pairs * I * 2;
 }
 
 hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     const int64_t pairs = (int64_t)a.T * a.top_k;
     a.max_slots = (int)max_slots(a.T, a.E, a.top_k);
     uint8_t* p = static_cast<uint8_t*>(ws);
-    a.n_slots = reinterpret_cast<int*>(p);
-    p += 256;
-    a.slots = reinterpret_cast<MoeSlot*>(p);
-    p += up256((size_t)a.max_slots * sizeof(MoeSlot));
-    a.pair_token = reinterpret_cast<int*>(p);
+    a.slots = reinterpret_cast<int*>(p);
+    p += up256((size_t)a.max_slots * kSlotWords * 4);
+    a.place = reinterpret_cast<int*>(p);
     p += up256((size_t)pairs * 4);
-    a.pair_p = reinterpret_cast<float*>(p);
+    a.share = reinterpret_cast<float*>(p);
     p += up256((size_t)pairs * 4);
+    a.out = reinterpret_cast<float*>(p);
+    p += up256((size_t)pairs * a.H * 4);
     a.h = reinterpret_cast<uint16_t*>(p);
 
     const dim3 rt(kRouteThreads);
@@ -444,17 +475,13 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
         hipLaunchKernelGGL(route_kernel<4>, dim3(1), rt, 0, s, a);
     else
         hipLaunchKernelGGL(route_kernel<16>, dim3(1), rt, 0, s, a);
-
-    const dim3 ug((unsigned)((int64_t)a.max_slots * (a.I / 16)));
-    const dim3 dg((unsigned)(a.H / 16));
-    const unsigned lds = 8u * (unsigned)a.T * 16u * 4u;
-    if (a.y_f32) {
-        hipLaunchKernelGGL((up_kernel<8, 4, 3>), ug, dim3(512), 0, s, a);
-        hipLaunchKernelGGL((down_kernel<1, 8, 2, 3>), dg, dim3(512), lds, s, a);
-    } else {
-        hipLaunchKernelGGL((up_kernel<8, 4, 2>), ug, dim3(512), 0, s, a);
-        hipLaunchKernelGGL((down_kernel<1, 8, 2, 2>), dg, dim3(512), lds, s, a);
-    }
+    launch_expert<true, 1, 2, 2, 4, 2>(a, s);
+    if (a.y_f32)
+        launch_expert<false, 3, 1, 4, 1, 2>(a, s);
+    else
+        launch_expert<false, 2, 1, 4, 2, 2>(a, s);
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256),
+                       0, s, a);
     return hipGetLastError();
 }
 
