@@ -110,7 +110,8 @@ constexpr int kMaxTopK = 32;
 
 // Up to 16 of the pairs (token, chosen expert) of one expert: words [0] the
 // expert, [1] their number (0: none, nothing to do), [2] the first pair's place
-// among all, [16 + i] the i-th pair's token (past the last: the first's).
+// among all, [16 + i] the i-th pair's token (past the last: the first's).  With
+// one token only words 0, 1 and [3], the expert's share (fp32).
 constexpr int kSlotWords = 32;
 
 struct MoeArgs {

@@ -5,6 +5,9 @@
 // (token, expert) sorted by expert and cut into slots of at most 16.  up: per
 // slot the products with the gate and up rows and h = silu(g) * u.  down: per
 // slot the products of h with the down rows.  join: each token's weighted sum.
+// Above 16 tokens a launch before route chooses the experts.  One token takes two
+// launches: up, which chooses for itself, and down over all its experts, which
+// writes y.
 // The chosen experts' weights are read once (an expert with more than 16 tokens:
 // once a slot, the later reads from cache), which is what bounds the layer;
 // activations and pair outputs are hundredths of them.
@@ -50,74 +53,123 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
-// One workgroup.  A wave takes a token: lane l holds the logits of the experts
-// EV l .. EV l + EV - 1, so that the lowest lane of a tie has the lowest expert;
-// top_k rounds find the largest key and strike it out.  Tokens per expert are
-// kept as 128-bit sets, so the sorted place of a pair is a count of bits and
-// depends on no order of execution.
+// A token's logits over a wave: lane l holds the experts EV l .. EV l + EV - 1, so
+// that the lowest lane of a tie has the lowest expert.
+template <int EV>
+struct Logits {
+    float l[EV];
+    uint32_t key[EV];
+
+    __device__ __forceinline__ void load(const float* p, int E, int lane) {
+#pragma unroll
+        for (int i = 0; i < EV; ++i) {
+            const int e = EV * lane + i;
+            l[i] = e < E ? p[e] : -__builtin_inff();
+        }
+    }
+    __device__ __forceinline__ void rank(int E, int lane) {
+#pragma unroll
+        for (int i = 0; i < EV; ++i) key[i] = EV * lane + i < E ? order_key(l[i]) : 0u;
+    }
+    // The expert with the largest key, struck out, and its logit; -1 when only -inf
+    // is left.
+    __device__ __forceinline__ int take(int lane, float& logit) {
+        uint32_t best = key[0];
+        int at = 0;
+        float v = l[0];
+#pragma unroll
+        for (int i = 1; i < EV; ++i) {
+            const bool more = key[i] > best;
+            const uint32_t k = key[i];
+            const float f = l[i];
+            best = more ? k : best;
+            at = more ? i : at;
+            v = more ? f : v;
+        }
+        const uint32_t m = wave_max(best);
+        if (m <= kKeyNegInf) return -1;
+        const int src = __builtin_ctzll(__ballot(best == m));
+        const int e = EV * src + __builtin_amdgcn_readlane(at, src);
+        logit = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), src));
+#pragma unroll
+        for (int i = 0; i < EV; ++i) key[i] = lane == src && i == at ? 0u : key[i];
+        return e;
+    }
+    // sum of exp(logit - top) over all experts
+    __device__ __forceinline__ float total(float top) const {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < EV; ++i)
+            if (l[i] != -__builtin_inff()) s += expf(l[i] - top);
+        return wave_sum(s);
+    }
+};
+
+// The wave's token t: lane j gets its j-th expert (or -1) and that expert's share.
+template <int EV>
+__device__ __forceinline__ int choose(const MoeArgs& a, int t, int lane, float& p) {
+    Logits<EV> g;
+    g.load(a.logits + t * a.ldl, a.E, lane);
+    g.rank(a.E, lane);
+    float top = 0.f, mine = 0.f;
+    int mine_e = -1;
+    for (int j = 0; j < a.top_k; ++j) {
+        float v = 0.f;
+        const int e = g.take(lane, v);
+        if (e < 0) break;
+        if (j == 0) top = v;
+        if (lane == j) {
+            mine = v;
+            mine_e = e;
+        }
+    }
+    const float ex = mine_e >= 0 ? expf(mine - top) : 0.f;
+    const float sum = a.renormalize ? wave_sum(ex) : g.total(top);
+    p = mine_e < 0 ? 0.f : ex / sum;
+    return mine_e;
+}
+
+// Above 16 tokens: the choice by itself, one token a wave (61 tokens, 8 of 127
+// experts: with 16 waves taking them in turn route took 16 us, most of it
+// issuing the reductions; now 4 + 6).
+constexpr int kRouteTokens = kRouteThreads / 64;
+template <int EV>
+__global__ __launch_bounds__(256) void choose_kernel(MoeArgs a) {
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (t >= a.T) return;
+    float p;
+    const int e = choose<EV>(a, t, lane, p);
+    if (lane < a.top_k) {
+        a.place[t * a.top_k + lane] = e;
+        a.share[t * a.top_k + lane] = p;
+    }
+}
+
+// One workgroup.  Tokens per expert are kept as 128-bit sets, so the sorted place
+// of a pair is a count of bits and depends on no order of execution.
 template <int EV>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
     __shared__ uint32_t set[kMaxExperts][4];
     __shared__ int base[kMaxExperts];
     __shared__ int wave_tot[2][kRouteThreads / 64];
-    __shared__ uint16_t chosen[kMaxTokens * kMaxTopK];
+    __shared__ int16_t chosen[kMaxTokens * kMaxTopK];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     for (int i = tid; i < a.E * 4; i += kRouteThreads) (&set[0][0])[i] = 0;
     __syncthreads();
 
-    for (int t = w; t < a.T; t += kRouteThreads / 64) {
-        uint32_t key[EV];
-        float l[EV];
-#pragma unroll
-        for (int i = 0; i < EV; ++i) {
-            const int e = EV * lane + i;
-            l[i] = e < a.E ? a.logits[t * a.ldl + e] : -__builtin_inff();
-            key[i] = e < a.E ? order_key(l[i]) : 0u;
+    if (a.T > kRouteTokens) {
+        for (int i = tid; i < a.T * a.top_k; i += kRouteThreads) {
+            const int e = a.place[i], t = i / a.top_k;
+            chosen[i] = (int16_t)e;
+            if (e >= 0) atomicOr(&set[e][t >> 5], 1u << (t & 31));
         }
-        float top = 0.f, mine = 0.f;    // the largest logit; lane j: the j-th chosen one
-        int mine_e = -1;
-        for (int j = 0; j < a.top_k; ++j) {
-            uint32_t best = key[0];
-            int at = 0;
-            float v = l[0];
-#pragma unroll
-            for (int i = 1; i < EV; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = i;
-                    v = l[i];
-                }
-            const uint32_t m = wave_max(best);
-            if (m <= kKeyNegInf) break;     // only -inf (or nothing) left
-            const int src = __builtin_ctzll(__ballot(best == m));
-            const int e = EV * src + __builtin_amdgcn_readlane(at, src);
-            v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), src));
-            if (lane == src) {
-#pragma unroll
-                for (int i = 0; i < EV; ++i)
-                    if (i == at) key[i] = 0;
-            }
-            if (j == 0) top = v;
-            if (lane == j) {
-                mine = v;
-                mine_e = e;
-            }
-        }
-        const float ex = mine_e >= 0 ? expf(mine - top) : 0.f;
-        float sum;
-        if (a.renormalize) {
-            sum = wave_sum(ex);
-        } else {
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < EV; ++i)
-                if (l[i] != -__builtin_inff()) s += expf(l[i] - top);
-            sum = wave_sum(s);
-        }
+    } else if (w < a.T) {
+        float p;
+        const int e = choose<EV>(a, w, lane, p);
         if (lane < a.top_k) {
-            chosen[t * a.top_k + lane] = (uint16_t)(mine_e < 0 ? 0xFFFF : mine_e);
-            a.share[t * a.top_k + lane] = mine_e < 0 ? 0.f : ex / sum;
-            if (mine_e >= 0) atomicOr(&set[mine_e][t >> 5], 1u << (t & 31));
+            chosen[w * a.top_k + lane] = (int16_t)e;
+            a.share[w * a.top_k + lane] = p;
+            if (e >= 0) atomicOr(&set[e][w >> 5], 1u << (w & 31));
         }
     }
     __syncthreads();
@@ -183,7 +235,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
     for (int i = tid; i < a.T * a.top_k; i += kRouteThreads) {
         const int e = chosen[i];
         int p = -1;
-        if (e != 0xFFFF) {
+        if (e >= 0) {
             const int t = i / a.top_k;
             p = base[e];
             for (int j = 0; j < (t >> 5); ++j) p += __popc(set[e][j]);
@@ -200,23 +252,26 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
 // the slot's rows (of x, gathered by token, or of h in PARTS parts) go through
 // LDS, double-buffered, in the layout of mx4_gemm.hip's few-row kernel, ROWS of
 // them: slots of up to four rows, the most by far, move a quarter of the bytes.
-template <bool UP, int PARTS, int R, int WN, int KW, int UG>
+template <bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
 struct Expert {
     static constexpr int kThreads = WN * KW * 64;
-    static constexpr int pieces(int rows) { return rows * 16 * UG * PARTS; }
+    static constexpr int ug(int rows) { return rows > 4 ? UG16 : UG4; }
+    static constexpr int pieces(int rows) { return rows * 16 * ug(rows) * PARTS; }
     static constexpr int stage(int rows) {
         return (pieces(rows) + WN * 64 - 1) / (WN * 64) * (WN * 64) * 16;
     }
     static constexpr int lds(int rows) {
-        const int x = 2 * KW * stage(rows), red = KW * WN * R * 1024;
+        const int x4 = 2 * KW * stage(4), x16 = rows > 4 ? 2 * KW * stage(16) : 0;
+        const int x = x4 > x16 ? x4 : x16, red = KW * WN * R * 1024;
         return x > red ? x : red;
     }
 };
 
-template <int ROWS, bool UP, int PARTS, int R, int WN, int KW, int UG>
+template <int ROWS, bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
 __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, int e, int count,
                                             int p0, int block, uint8_t* lds) {
-    using X = Expert<UP, PARTS, R, WN, KW, UG>;
+    using X = Expert<UP, PARTS, R, WN, KW, UG4, UG16>;
+    constexpr int UG = X::ug(ROWS);
     constexpr int kStage = X::stage(ROWS), P = kStage / (WN * 64 * 16);
     constexpr int kPart = ROWS * 16 * UG;       // pieces of one part of a unit
     const int tid = threadIdx.x, lane = tid & 63;
@@ -255,7 +310,7 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
         if (part > PARTS - 1) part = PARTS - 1;
         const int row = piece % kPart / (16 * UG);
         if constexpr (UP)
-            xp[i] = a.x + (int64_t)slot[16 + row] * a.ldx;
+            xp[i] = a.x + (a.T == 1 ? 0 : slot[16 + row] * a.ldx);
         else
             xp[i] = a.h + (part * pairs + p0 + (row < count ? row : 0)) * (int64_t)a.I;
         xk[i] = piece % (16 * UG) * 8;
@@ -388,16 +443,190 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
     }
 }
 
-template <bool MANY, bool UP, int PARTS, int R, int WN, int KW, int UG>
+template <bool MANY, bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
 __global__ __launch_bounds__(WN* KW * 64) void expert_kernel(MoeArgs a, int blocks) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int* slot = a.slots + (blockIdx.x / blocks) * kSlotWords;
     const int e = slot[0], count = slot[1], p0 = slot[2], block = blockIdx.x % blocks;
     if (count == 0) return;
     if (MANY && count > 4)
-        expert_body<16, UP, PARTS, R, WN, KW, UG>(a, slot, e, count, p0, block, lds);
+        expert_body<16, UP, PARTS, R, WN, KW, UG4, UG16>(a, slot, e, count, p0, block, lds);
     else
-        expert_body<4, UP, PARTS, R, WN, KW, UG>(a, slot, e, count, p0, block, lds);
+        expert_body<4, UP, PARTS, R, WN, KW, UG4, UG16>(a, slot, e, count, p0, block, lds);
+}
+
+// up for one token, which chooses for itself: slot s is the token's expert with
+// the s-th largest logit, found by every wave; the slot's first workgroup writes
+// its words for down.
+template <int EV, int WN, int KW, int UG>
+__global__ __launch_bounds__(WN* KW * 64) void up_one_kernel(MoeArgs a, int blocks) {
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int s = blockIdx.x / blocks, block = blockIdx.x % blocks, lane = threadIdx.x & 63;
+    Logits<EV> g;
+    g.load(a.logits, a.E, lane);
+    g.rank(a.E, lane);
+    float top = 0.f, mine = 0.f, sum = 0.f;
+    int e = -1;
+    const int rounds = block == 0 ? a.top_k : s + 1;
+    for (int j = 0; j < rounds; ++j) {
+        float v = 0.f;
+        const int found = g.take(lane, v);
+        if (found < 0) break;
+        if (j == 0) top = v;
+        if (j == s) {
+            e = found;
+            mine = v;
+        }
+        sum += expf(v - top);
+    }
+    if (block == 0) {
+        if (!a.renormalize) sum = g.total(top);
+        if (threadIdx.x == 0) {
+            int* o = a.slots + s * kSlotWords;
+            o[0] = e;
+            o[1] = e >= 0;
+            o[3] = __float_as_int(expf(mine - top) / sum);
+        }
+    }
+    if (e < 0) return;
+    expert_body<4, true, 1, 2, WN, KW, UG, UG>(a, nullptr, e, 1, s, block, lds);
+}
+
+// ---- down for one token -------------------------------------------------------------
+// A workgroup: WN tiles of 16 outputs.  The units (expert, UG groups of its hidden
+// values) are one sequence of which each of the KW groups of waves takes every
+// KW-th; a unit's product is weighted into the sum at once, and no pair's output
+// goes through memory.  All 16 columns of an operand hold the one token.
+template <int PARTS, int WN, int KW, int UG>
+struct One {
+    static constexpr int kThreads = WN * KW * 64;
+    static constexpr int kPieces = 16 * UG * PARTS;
+    static constexpr int kStage = (kPieces + WN * 64 - 1) / (WN * 64) * (WN * 64) * 16;
+    static constexpr int lds() {
+        const int x = 2 * KW * kStage, red = KW * WN * 64;
+        return x > red ? x : red;
+    }
+};
+
+template <int PARTS, int WN, int KW, int UG>
+__global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
+    using X = One<PARTS, WN, KW, UG>;
+    constexpr int P = X::kStage / (WN * 64 * 16), kPart = 16 * UG;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kw = w / WN, wn = w % WN;
+    const int q = lane >> 4;
+    const int G = (int)groups(a.I), Q = (int)quads(a.I), UI = (G + UG - 1) / UG;
+    const int ht = a.H / 16;
+    const int tile = blockIdx.x * WN + wn < ht ? blockIdx.x * WN + wn : ht - 1;
+    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+
+    // lane j holds the j-th expert and its share; the used ones come first
+    int expert = -1;
+    float share = 0.f;
+    if (lane < a.top_k) {
+        const int* s = a.slots + lane * kSlotWords;
+        expert = s[0];
+        share = __int_as_float(s[3]);
+    }
+    const int units = (int)__popcll(__ballot(expert >= 0)) * UI;
+    const int its = (units + KW - 1) / KW;
+
+    uint8_t* mine = lds + kw * 2 * X::kStage;
+    u32x4_t wb[2][UG], xb[P];
+    uint32_t ws[2];
+    bool xin[P];
+    auto load = [&](int s, int it) {
+        const int u = it * KW + kw;
+        const int uc = u < units ? u : units - 1;
+        const int sl = uc / UI, ui = uc % UI;
+        const int64_t t = (int64_t)__builtin_amdgcn_readlane(expert, sl) * ht + tile;
+        const uint8_t* wp = a.w2.codes + t * G * kCodeBlock;
+        ws[s] = *reinterpret_cast<const uint32_t*>(
+                    scalar(a.w2.scales + (t * Q + ui * UG / 4) * kScaleBlock) + lane4) >>
+                (UG == 4 ? 0 : 8 * UG * (ui % (4 / UG)));
+#pragma unroll
+        for (int j = 0; j < UG; ++j) {
+            const int g = ui * UG + j < G ? ui * UG + j : G - 1;
+            wb[s][j] = load16_nt(scalar(wp + (int64_t)g * kCodeBlock) + lane16);
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int piece = (i * WN + wn) * 64 + lane;
+            const int part = piece / kPart < PARTS ? piece / kPart : PARTS - 1;
+            const int k = ui * UG * 128 + piece % kPart * 8;
+            xin[i] = u < units && k < a.I;
+            xb[i] = *reinterpret_cast<const u32x4_t*>(
+                a.h + ((int64_t)part * a.top_k + sl) * a.I + (k < a.I ? k : 0));
+        }
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int piece = (i * WN + wn) * 64 + lane;
+            u32x4_t v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = xin[i] ? xb[i][k] : 0u;
+            *reinterpret_cast<u32x4_t*>(mine + buf * X::kStage + piece * 16) = v;
+        }
+    };
+    f32x4_t sum = {0, 0, 0, 0};
+    auto product = [&](auto sc, int it) {
+        constexpr int s = decltype(sc)::value;
+        const uint8_t* xl = mine + s * X::kStage;
+        f32x4_t acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < UG; ++j) {
+            const float f = scale_f32((ws[s] >> (8 * j)) & 255u);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const bf16x8_t wv = expand8(wb[s][j][b], f);
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+                    acc = mfma_bf16(wv, *reinterpret_cast<const bf16x8_t*>(
+                                            xl + (p * kPart + 16 * j + 4 * q + b) * 16), acc);
+            }
+        }
+        const int u = it * KW + kw;
+        const float f = __int_as_float(__builtin_amdgcn_readlane(
+            __float_as_int(share), (u < units ? u : units - 1) / UI));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += u < units ? f * acc[i] : 0.f;
+    };
+    if (units > 0) {
+        load(0, 0);
+        stage(0);
+        __syncthreads();
+        auto step = [&](auto sc, int it) {
+            constexpr int s = decltype(sc)::value;
+            load(s ^ 1, it + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            product(sc, it);
+            __builtin_amdgcn_sched_barrier(0);
+            stage(s ^ 1);
+            __syncthreads();
+        };
+        for (int it = 0; it < its; it += 2) {
+            step(std::integral_constant<int, 0>{}, it);
+            if (it + 1 >= its) break;
+            step(std::integral_constant<int, 1>{}, it + 1);
+        }
+    }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][16]
+    if ((lane & 15) == 0) *reinterpret_cast<f32x4_t*>(red + w * 16 + 4 * q) = sum;
+    __syncthreads();
+    const int n = blockIdx.x * 16 * WN + tid;
+    if (tid < 16 * WN && n < a.H) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) v += red[k * WN * 16 + tid];
+        if (a.y_f32)
+            static_cast<float*>(a.y)[n] = v;
+        else
+            static_cast<uint16_t*>(a.y)[n] = bf16_bits(v);
+    }
 }
 
 // y[t] = sum of its experts' outputs, weighted, in the order of their choice.
@@ -429,19 +658,44 @@ int64_t max_slots(int64_t T, int64_t E, int64_t top_k) {
     return (E < pairs ? E : pairs) + pairs / 16;
 }
 
-template <bool UP, int PARTS, int R, int WN, int KW, int UG>
+template <bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
 void launch_expert(const MoeArgs& a, hipStream_t s) {
-    using X = Expert<UP, PARTS, R, WN, KW, UG>;
+    using X = Expert<UP, PARTS, R, WN, KW, UG4, UG16>;
     static_assert(X::lds(16) <= 65536, "more LDS than a launch gets without asking");
     const int nt = (UP ? a.I : a.H) / 16, per = UP ? WN : WN * R;
     const int blocks = (nt + per - 1) / per;
     const dim3 grid((unsigned)((int64_t)a.max_slots * blocks)), block(X::kThreads);
     if (a.T <= 4)
-        hipLaunchKernelGGL((expert_kernel<false, UP, PARTS, R, WN, KW, UG>), grid, block, X::lds(4),
-                           s, a, blocks);
+        hipLaunchKernelGGL((expert_kernel<false, UP, PARTS, R, WN, KW, UG4, UG16>), grid, block,
+                           X::lds(4), s, a, blocks);
     else
-        hipLaunchKernelGGL((expert_kernel<true, UP, PARTS, R, WN, KW, UG>), grid, block, X::lds(16),
-                           s, a, blocks);
+        hipLaunchKernelGGL((expert_kernel<true, UP, PARTS, R, WN, KW, UG4, UG16>), grid, block,
+                           X::lds(16), s, a, blocks);
+}
+
+template <int EV>
+void launch_up_one(const MoeArgs& a, hipStream_t s) {
+    constexpr int WN = 1, KW = 4, UG = 4;   // (1, 8, 2): 12.9 against 12.1 us at H = 5120, I = 1280
+    using X = Expert<true, 1, 2, WN, KW, UG, UG>;
+    const int blocks = (a.I / 16 + WN - 1) / WN;
+    hipLaunchKernelGGL((up_one_kernel<EV, WN, KW, UG>), dim3((unsigned)(a.top_k * blocks)),
+                       dim3(X::kThreads), X::lds(4), s, a, blocks);
+}
+
+template <int PARTS, int WN, int KW, int UG>
+void launch_down_one(const MoeArgs& a, hipStream_t s) {
+    using X = One<PARTS, WN, KW, UG>;
+    static_assert(X::lds() <= 65536, "more LDS than a launch gets without asking");
+    hipLaunchKernelGGL((down_one_kernel<PARTS, WN, KW, UG>),
+                       dim3((unsigned)((a.H / 16 + WN - 1) / WN)), dim3(X::kThreads), X::lds(), s,
+                       a);
+}
+
+template <int EV>
+void launch_route(const MoeArgs& a, hipStream_t s) {
+    if (a.T > kRouteTokens)
+        hipLaunchKernelGGL(choose_kernel<EV>, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(route_kernel<EV>, dim3(1), dim3(kRouteThreads), 0, s, a);
 }
 
 }  // namespace
@@ -466,20 +720,31 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     p += up256((size_t)pairs * a.H * 4);
     a.h = reinterpret_cast<uint16_t*>(p);
 
-    const dim3 rt(kRouteThreads);
-    if (a.E <= 64)
-        hipLaunchKernelGGL(route_kernel<1>, dim3(1), rt, 0, s, a);
-    else if (a.E <= 128)
-        hipLaunchKernelGGL(route_kernel<2>, dim3(1), rt, 0, s, a);
-    else if (a.E <= 256)
-        hipLaunchKernelGGL(route_kernel<4>, dim3(1), rt, 0, s, a);
-    else
-        hipLaunchKernelGGL(route_kernel<16>, dim3(1), rt, 0, s, a);
-    launch_expert<true, 1, 2, 2, 4, 2>(a, s);
+    const int ev = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : 16;
+    if (a.T == 1) {
+        switch (ev) {
+            case 1: launch_up_one<1>(a, s); break;
+            case 2: launch_up_one<2>(a, s); break;
+            case 4: launch_up_one<4>(a, s); break;
+            default: launch_up_one<16>(a, s);
+        }
+        if (a.y_f32)
+            launch_down_one<3, 1, 8, 2>(a, s);
+        else
+            launch_down_one<2, 1, 8, 2>(a, s);
+        return hipGetLastError();
+    }
+    switch (ev) {
+        case 1: launch_route<1>(a, s); break;
+        case 2: launch_route<2>(a, s); break;
+        case 4: launch_route<4>(a, s); break;
+        default: launch_route<16>(a, s);
+    }
+    launch_expert<true, 1, 2, 2, 2, 2, 1>(a, s);
     if (a.y_f32)
-        launch_expert<false, 3, 1, 4, 1, 2>(a, s);
+        launch_expert<false, 3, 2, 4, 1, 1, 1>(a, s);
     else
-        launch_expert<false, 2, 1, 4, 2, 2>(a, s);
+        launch_expert<false, 2, 2, 4, 1, 1, 1>(a, s);
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256),
                        0, s, a);
     return hipGetLastError();
