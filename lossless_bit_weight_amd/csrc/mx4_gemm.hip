@@ -179,7 +179,7 @@ struct Mid {
     static constexpr int MT = ROWS < 16 ? 1 : ROWS / 16;
     static constexpr int kAllPieces = XM ? MT * 64 * UG : ROWS * 16 * UG;   // of x a unit
     static constexpr int kPieces = (kAllPieces + WN * 64 - 1) / (WN * 64);  // a thread
-    static constexpr int kStage = kPieces * WN * 64 * 16;
+    static constexpr int kStage = kAllPieces * 16;
     static constexpr int lds(int R) {
         const int x = 2 * KW * kStage, red = KW * WN * MT * R * 1024;
         return x > red ? x : red;
@@ -222,12 +222,56 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         sp[r] = a.w.scales + t * a.Q * kScaleBlock;
     }
     uint8_t* mine = lds + kw * 2 * T::kStage;
+    auto at_piece = [&](int i) {
+        int p = (i * WN + wn) * 64 + lane;
+        if (T::kAllPieces % (WN * 64) != 0 && p > T::kAllPieces - 64 + lane)
+            p = T::kAllPieces - 64 + lane;
+        return p;
+    };
     u32x4_t wb[2][UG][R], xb[P];
     uint32_t ws[2][R], xs[2][XM ? MT : 1];
     bool xin[P];
     // (no branch: a place past the last unit, group, row or K is a valid one whose x
-    // is replaced by zeros)
-    auto load = [&](int slot, int it) {
+    // is replaced by zeros, a piece past the last is the last once more)
+    auto load_x = [&](int slot, int it) {
+        const int u = u0 + it * KW + kw;
+        const int uc = u < u1 ? u : u1 - 1;
+        const int64_t so = (int64_t)(uc * UG / 4) * kScaleBlock;
+        const int shift = UG == 4 ? 0 : 8 * UG * (uc % (4 / UG));
+        (void)so;
+        (void)shift;
+        if constexpr (XM) {
+            const int64_t last = tiles(a.M) - 1;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int block = i * WN + wn < MT * UG ? i * WN + wn : MT * UG - 1;
+                const int64_t t = m0 / 16 + block / UG;     // (tile, group) of the unit
+                const int g = u * UG + block % UG;
+                xin[i] = u < u1 && g < a.G;
+                xb[i] = *reinterpret_cast<const u32x4_t*>(
+                    scalar(a.xm.codes + ((t < last ? t : last) * a.G + (g < a.G ? g : a.G - 1)) *
+                                            kCodeBlock) + lane16);
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const int64_t tt = m0 / 16 + t < last ? m0 / 16 + t : last;
+                xs[slot][t] = *reinterpret_cast<const uint32_t*>(
+                                  scalar(a.xm.scales + tt * a.Q * kScaleBlock + so) + lane4) >> shift;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int piece = at_piece(i);
+                int m = m0 + piece / (16 * UG);
+                if (m >= a.M) m = a.M - 1;
+                const int k = u * UG * 128 + piece % (16 * UG) * 8;
+                xin[i] = u < u1 && k < a.K;
+                xb[i] = *reinterpret_cast<const u32x4_t*>(a.x + (int64_t)m * a.ldx +
+                                                          (xin[i] ? k : 0));
+            }
+        }
+    };
+    auto load_w = [&](int slot, int it) {
         const int u = u0 + it * KW + kw;
         const int uc = u < u1 ? u : u1 - 1;
         const int64_t so = (int64_t)(uc * UG / 4) * kScaleBlock;
@@ -242,41 +286,18 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
             for (int r = 0; r < R; ++r)
                 wb[slot][j][r] = load16_nt(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
         }
-        if constexpr (XM) {
-            const int64_t last = tiles(a.M) - 1;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int64_t tt = m0 / 16 + t < last ? m0 / 16 + t : last;
-                xs[slot][t] = *reinterpret_cast<const uint32_t*>(
-                                  scalar(a.xm.scales + tt * a.Q * kScaleBlock + so) + lane4) >> shift;
-            }
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int block = i * WN + wn;          // (tile, group) of the unit
-                const int64_t t = m0 / 16 + block / UG;
-                const int g = u * UG + block % UG;
-                xin[i] = u < u1 && g < a.G;
-                xb[i] = *reinterpret_cast<const u32x4_t*>(
-                    scalar(a.xm.codes + ((t < last ? t : last) * a.G + (g < a.G ? g : a.G - 1)) *
-                                            kCodeBlock) + lane16);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const int piece = (i * WN + wn) * 64 + lane;
-                int m = m0 + piece / (16 * UG);
-                if (m >= a.M) m = a.M - 1;
-                const int k = u * UG * 128 + piece % (16 * UG) * 8;
-                xin[i] = u < u1 && k < a.K;
-                xb[i] = *reinterpret_cast<const u32x4_t*>(a.x + (int64_t)m * a.ldx +
-                                                          (xin[i] ? k : 0));
-            }
-        }
+    };
+    // x is waited for first; four rows of it arrive before the weights in any order,
+    // and the weights come sooner if asked for first (gate+up M = 1 19.7 -> 18.4 us)
+    auto load = [&](int slot, int it) {
+        if (ROWS < 16) load_w(slot, it);
+        load_x(slot, it);
+        if (ROWS >= 16) load_w(slot, it);
     };
     auto stage = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int piece = (i * WN + wn) * 64 + lane;
+            const int piece = at_piece(i);
             int at = piece;
             if constexpr (!XM) {
                 const int row = piece / (16 * UG), p = piece % (16 * UG);
@@ -715,24 +736,45 @@ hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
 
 // Kernel and split of a product.
 enum Kernel {
-    kSmall, kMid4, kMid4Long, kMid16, kMid16x2, kMid16w, kMid32, kMid32x2, kMid64,
+    kSmall, kMid4, kMid4Long, kMid16, kMid16x2, kMid32, kMid32R2, kMid32x2, kMid64,
     kTile64, kTileMid, kTile128
 };
 struct Plan {
     Kernel kernel;
+    int wn;                 // mid kernels: waves beside each other
     int S, gs;              // K slices, groups a slice (a multiple of 4)
 };
+
+// Waves beside each other that spread `units` of work along N (times mb blocks of
+// rows) best over 256 CUs: the CU with the most of them decides.  Gate+up, 2176
+// tiles, M = 32, us (tiles of that CU): 9 waves 26.4 (9), 12 30.1 (12), 5 33.2
+// (10), 7 35.4 (14), 8 36.8 (16).  Of equals the most waves, which share x.
+int spread(int64_t units, int64_t mb) {
+    static const int kWaves[] = {12, 9, 7, 5, 4};
+    int best = 4;
+    int64_t least = -1;
+    for (const int w : kWaves) {
+        const int64_t load = ((units + w - 1) / w * mb + 255) / 256 * w;
+        if (least < 0 || load < least) {
+            least = load;
+            best = w;
+        }
+    }
+    return best;
+}
 
 // By rows of x (M), tiles of 16 weight rows (nt) and groups of K (G).  Measured on
 // QKV (nt = 448, G = 40), gate+up (2176, 40) and down (320, 136), us:
 //   up to 16 rows, BF16 x: every wave on its own x for few tiles (QKV M = 1 6.9 against
 //     7.8 through LDS, M = 16 9.8 against 11.1); shared through LDS for many tiles
-//     (gate+up M = 1 18.5 against 22.1, M = 16 27.1 against 29.2) or a long K (down
-//     M = 1 14.3 against 15.6, M = 16, K in four slices, 19.1 against 23.5).  MX4 x
+//     (gate+up M = 1 18.5 against 22.1, M = 16 23.6 against 29.2) or a long K (down
+//     M = 1 14.3 against 15.6, M = 16, K in six slices, 17.5 against 23.5).  MX4 x
 //     is a quarter of the bytes: shared or not within 3%.
 //   17 rows to 128 (MX4 x: 256) and few tiles: 16 (32, 64) rows a workgroup, whose
 //     weights the row blocks beside it find in L2 (QKV M = 64 16.3, M = 128 22.3; a
 //     64 x 128 tile in four slices 21.2 and 24.9).
+//   17 to 64 and many tiles: 32 rows (MX4 x: up to 64), waves as spread() says
+//     (gate+up M = 64 42.5 with two tiles a wave, 50.4 with 64 x 128 tiles).
 //   above: the largest tile that still gives 440 workgroups (QKV M = 512 44.8 with
 //     64 x 128 tiles, 52.5 with 128 x 256; M = 2048 the reverse), K in slices if the
 //     smallest does not.
@@ -743,7 +785,7 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
     const auto blocks = [&](int64_t bm, int64_t bn) {
         return (M + bm - 1) / bm * ((N + bn - 1) / bn);
     };
-    Plan p{kSmall, 1, 4 * Q};
+    Plan p{kSmall, 4, 1, 4 * Q};
     int64_t S = 1;
     const auto slices = [](int64_t want, int64_t have) { return (want + have / 2) / have; };
     if (M <= 16) {
@@ -753,16 +795,24 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
             p.kernel = many ? kMid4 : kMid4Long;
         } else {
             p.kernel = kMid16;
-            S = slices(320, blocks(16, 64));
+            if (many)
+                p.wn = spread(nt, 1);
+            else
+                S = slices(480, blocks(16, 64));
         }
-    } else if (xm && (M <= 64 || (M <= 256 && !many))) {
-        p.kernel = many ? (M <= 32 ? kMid32 : kMid64) : lengthy || M > 64 ? kMid64 : kMid32x2;
+    } else if (many && M <= 64) {
+        if (xm)
+            p.kernel = M <= 32 ? kMid32 : kMid64;
+        else
+            p.kernel = M <= 32 ? kMid32 : kMid32R2;
+        p.wn = p.kernel == kMid32R2 ? spread((nt + 1) / 2, (M + 31) / 32) : spread(nt, 1);
+    } else if (xm && !many && M <= 256) {
+        p.kernel = lengthy || M > 64 ? kMid64 : kMid32x2;
         if (lengthy) S = slices(400, blocks(64, 64));
     } else if (!xm && !many && M <= (lengthy ? 64 : 128)) {
-        p.kernel = lengthy ? kMid16w : M <= 32 ? kMid16x2 : M <= 64 ? kMid16 : kMid16w;
+        p.kernel = !lengthy && M <= 32 ? kMid16x2 : kMid16;
+        p.wn = lengthy || M > 64 ? 8 : 4;
         if (lengthy) S = slices(480, blocks(16, 128));
-    } else if (!xm && M <= 32) {
-        p.kernel = kMid32;
     } else if (blocks(128, 256) >= 440) {
         p.kernel = kTile128;
     } else if (xm ? blocks(128, 128) >= 440 : blocks(64, 256) >= 440) {
@@ -777,6 +827,17 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
     p.S = (Q + qs - 1) / qs;
     p.gs = 4 * qs;
     return p;
+}
+
+template <int ROWS, int R, bool XM>
+hipError_t launch_mid_waves(int wn, GemmArgs& a, hipStream_t s) {
+    switch (wn) {
+        case 5: return launch_mid<ROWS, R, 5, 1, 4, XM>(a, s);
+        case 7: return launch_mid<ROWS, R, 7, 1, 4, XM>(a, s);
+        case 9: return launch_mid<ROWS, R, 9, 1, 4, XM>(a, s);
+        case 12: return launch_mid<ROWS, R, 12, 1, 4, XM>(a, s);
+        default: return launch_mid<ROWS, R, 4, 1, 4, XM>(a, s);
+    }
 }
 
 }  // namespace
@@ -798,9 +859,9 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     if (!xm && k >= kTile64 && a.ldx >= (1 << 23)) k = kSmall;
     if (k == kSmall) a.S = 1;
     if (xm) switch (k) {
-        case kMid32: return launch_mid<32, 1, 4, 1, 4, true>(a, s);
+        case kMid32: return launch_mid_waves<32, 1, true>(p.wn, a, s);
         case kMid32x2: return launch_mid<32, 1, 4, 2, 4, true>(a, s);
-        case kMid64: return launch_mid<64, 1, 4, 1, 4, true>(a, s);
+        case kMid64: return launch_mid_waves<64, 1, true>(p.wn, a, s);
         case kTile64: return launch_tile<4, 2, 1, 4, true, 2>(a, s);
         case kTileMid: return launch_tile<8, 2, 1, 4, true, 2>(a, s);
         case kTile128: return launch_tile<8, 4, 1, 4, true, 2>(a, s);
@@ -809,10 +870,12 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     switch (k) {
         case kMid4: return launch_mid<4, 1, 2, 2, 2, false>(a, s);
         case kMid4Long: return launch_mid<4, 1, 1, 4, 4, false>(a, s);
-        case kMid16: return launch_mid<16, 1, 4, 1, 4, false>(a, s);
+        case kMid16:
+            return p.wn == 8 ? launch_mid<16, 1, 8, 1, 4, false>(a, s)
+                             : launch_mid_waves<16, 1, false>(p.wn, a, s);
         case kMid16x2: return launch_mid<16, 1, 4, 2, 4, false>(a, s);
-        case kMid16w: return launch_mid<16, 1, 8, 1, 4, false>(a, s);
-        case kMid32: return launch_mid<32, 2, 8, 1, 4, false>(a, s);
+        case kMid32: return launch_mid_waves<32, 1, false>(p.wn, a, s);
+        case kMid32R2: return launch_mid_waves<32, 2, false>(p.wn, a, s);
         case kTile64: return launch_tile<4, 2, 1, 4, false, 2>(a, s);
         case kTileMid: return launch_tile<4, 4, 1, 4, false, 2>(a, s);
         case kTile128: return launch_tile<8, 4, 1, 4, false, 2>(a, s);

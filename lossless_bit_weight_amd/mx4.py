@@ -30,6 +30,7 @@ MAX_E = 1024
 MAX_TOP_K = 32
 
 _BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)
+_u8 = torch.uint8
 
 
 class MX4Error(W12Error):
@@ -134,13 +135,14 @@ class MX4Tensor:
     def ptrs(self, what: str) -> tuple:
         """(codes, scales) device pointers and the device's index."""
         d = self.data
-        if not d.is_cuda:
+        dev = d.get_device()
+        if dev < 0:
             raise ValueError("%s must be on the GPU" % what)
-        if d.dtype is not torch.uint8 or d.numel() < self._code_bytes + self._scale_bytes \
+        if d.dtype is not _u8 or d.numel() < self._code_bytes + self._scale_bytes \
                 or not d.is_contiguous():
             raise ValueError("%s: data must be %d contiguous bytes" % (what, self.nbytes))
         p = d.data_ptr()
-        return p, p + self._code_bytes, d.get_device()
+        return p, p + self._code_bytes, dev
 
 
 # ---- marshalling helpers ---------------------------------------------------
@@ -150,12 +152,14 @@ def _check(status: int, what: str) -> None:
         raise MX4Error(status, what)
 
 
+_TYPES = {torch.float32: OUT_F32, **{t: OUT_BF16 for t in _BF16_TYPES}}
+
+
 def _type_of(dtype: torch.dtype) -> int:
-    if dtype == torch.float32:
-        return OUT_F32
-    if dtype in _BF16_TYPES:
-        return OUT_BF16
-    raise TypeError("expected float32 or BF16, got %s" % dtype)
+    t = _TYPES.get(dtype)
+    if t is None:
+        raise TypeError("expected float32 or BF16, got %s" % dtype)
+    return t
 
 
 # torch's current stream of a device as the pointer itself (torch.cuda.current_stream
@@ -164,10 +168,14 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     else lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
-def _call(device: int, fn, args: tuple) -> None:
+_current = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+
+
+def _call(device: int, fn, *args) -> None:
     """fn(*args, stream) on torch's current stream of `device`, which is made
     current for the launch."""
-    if torch._C._cuda_getDevice() == device:
+    if _current() == device:
         status = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -243,7 +251,7 @@ def empty_mx4(R: int, K: int, batch: int | None = None, device="cuda") -> MX4Ten
     if R < 0 or K < BLOCK or K % BLOCK or (batch is not None and batch < 1):
         raise MX4Error(-2, "empty_mx4(%s, %d, %d)" % (batch, R, K))
     t = MX4Tensor(None, R, K, batch)
-    t.data = torch.empty(t._code_bytes + t._scale_bytes, dtype=torch.uint8, device=device)
+    t.data = torch.empty(t._code_bytes + t._scale_bytes, dtype=_u8, device=device)
     return t
 
 
@@ -257,8 +265,7 @@ def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None) -> MX4Tensor:
         raise ValueError("out holds %s, x is %s" % (out.shape, tuple(x.shape)))
     codes, scales, dev = out.ptrs("out")
     _same(dev, x.get_device())
-    _call(dev, lib().mx4_quantize, (x.data_ptr(), xt, 1 if B is None else B, R, K, ld, ldb, codes,
-                                    scales))
+    _call(dev, lib().mx4_quantize, x.data_ptr(), xt, B or 1, R, K, ld, ldb, codes, scales)
     return out
 
 
@@ -275,8 +282,7 @@ def mx4_dequantize(q: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16,
     yt = _type_of(_gpu(out, "out").dtype)
     B, R, K, ld, ldb = _batched(out, "out")
     _same(dev, out.get_device())
-    _call(dev, lib().mx4_dequantize, (codes, scales, 1 if B is None else B, R, K, out.data_ptr(),
-                                      yt, ld, ldb))
+    _call(dev, lib().mx4_dequantize, codes, scales, B or 1, R, K, out.data_ptr(), yt, ld, ldb)
     return out
 
 
@@ -295,7 +301,7 @@ def mx4_gemm(x, w: MX4Tensor, out_dtype: torch.dtype = torch.float32,
         if x.batch is not None or x.K != K:
             raise ValueError("x %s does not multiply w %s" % (x.shape, w.shape))
         xc, xsc, x_dev = x.ptrs("x")
-        args = (xc, xsc, M)
+        a0, a1, a2 = xc, xsc, M
     else:
         if _gpu(x, "x").dtype not in _BF16_TYPES:
             raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
@@ -304,12 +310,13 @@ def mx4_gemm(x, w: MX4Tensor, out_dtype: torch.dtype = torch.float32,
         if x.shape[1] != K:
             raise ValueError("x %s does not multiply w %s" % (tuple(x.shape), w.shape))
         x_dev = x.get_device()
-        args = (x.data_ptr(), M, ldx)
+        a0, a1, a2 = x.data_ptr(), M, ldx
     y, ldy, yt = _output(y, M, N, out_dtype, device)
     _same(dev, x_dev, y.get_device())
     keep, wsp, wsb = _workspace(mx4_gemm_workspace_bytes(M, N, K, x_mx4), workspace, device)
-    _call(dev, lib().mx4_gemm_mx4 if x_mx4 else lib().mx4_gemm,
-          args + (wc, wsc, N, K, y.data_ptr(), ldy, yt, wsp, wsb))
+    L = lib()
+    _call(dev, L.mx4_gemm_mx4 if x_mx4 else L.mx4_gemm, a0, a1, a2, wc, wsc, N, K, y.data_ptr(),
+          ldy, yt, wsp, wsb)
     return y
 
 
@@ -336,7 +343,6 @@ def mx4_moe(x: torch.Tensor, logits: torch.Tensor, w13: MX4Tensor, w2: MX4Tensor
     _same(dev, logits.get_device(), d13, d2, y.get_device())
     need = mx4_moe_workspace_bytes(T, H, I, E, int(top_k), y.dtype)
     keep, wsp, wsb = _workspace(need, workspace, device)
-    _call(dev, lib().mx4_moe, (x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I,
-                               E, int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp,
-                               wsb))
+    _call(dev, lib().mx4_moe, x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I,
+          E, int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp, wsb)
     return y
