@@ -100,8 +100,8 @@ int mx4_dequantize(const void *codes, const void *scales, int64_t B, int64_t R, 
  *   y  : device output [M, N], row stride ldy >= N, BF16 bits (2-byte aligned)
  *        or fp32 (4-byte aligned) as y_type says.
  *   workspace : mx4_gemm_workspace_bytes(M, N, K, 0) bytes; NULL if that is 0.
- * Errors: W12_ERR_NULL, W12_ERR_SHAPE (N < 1, M < 0 or M > 2^24 beside those of
- *         the sizes), W12_ERR_ALIGN, W12_ERR_DTYPE, W12_ERR_WORKSPACE,
+ * Errors: W12_ERR_NULL, W12_ERR_SHAPE (N < 1, N > 2^28, M < 0, M > 2^24 or
+ *         M*N > 2^37 beside those of the sizes), W12_ERR_ALIGN, W12_ERR_DTYPE, W12_ERR_WORKSPACE,
  *         W12_ERR_HIP.
  */
 int mx4_gemm(const uint16_t *x, int64_t M, int64_t ldx, const void *w_codes,
@@ -143,7 +143,8 @@ int mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_mx4, size_t 
  *   y      : device output [T, H], as mx4_gemm's.
  *   workspace : mx4_moe_workspace_bytes(T, H, I, E, top_k, y_type) bytes.
  * H % 32 == 0, I % 32 == 0, 1 <= top_k <= min(E, MX4_MAX_TOP_K),
- * E <= MX4_MAX_E.
+ * E <= MX4_MAX_E; (min(E, T*top_k) + T*top_k/16) times H/16 and times I/16 at
+ * most 2^24.
  * Errors: W12_ERR_NULL, W12_ERR_SHAPE, W12_ERR_ALIGN, W12_ERR_DTYPE,
  *         W12_ERR_UNSUPPORTED (T, E or top_k over its limit),
  *         W12_ERR_WORKSPACE, W12_ERR_HIP.

@@ -14,6 +14,12 @@ namespace {
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxK = (int64_t)1 << 24;
 constexpr int64_t kMaxM = (int64_t)1 << 24;
+// A launch counts its work items along x in 32 bits: N and M * N below these keep
+// every product's grid within.
+constexpr int64_t kMaxN = (int64_t)1 << 28;
+constexpr int64_t kMaxMN = (int64_t)1 << 37;
+// The same for the expert layer: slots times tiles of its outputs.
+constexpr int64_t kMaxMoeBlocks = (int64_t)1 << 24;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -51,8 +57,8 @@ int check_ws(const void* ws, size_t have, size_t need) {
 int status_of(hipError_t e) { return e == hipSuccess ? W12_OK : W12_ERR_HIP; }
 
 int check_gemm_shape(int64_t M, int64_t N, int64_t K) {
-    if (N < 1 || M < 0 || M > kMaxM) return W12_ERR_SHAPE;
-    if (M > 0 && N >= kMaxElems / M) return W12_ERR_SHAPE;
+    if (N < 1 || M < 0 || M > kMaxM || N > kMaxN) return W12_ERR_SHAPE;
+    if (M > 0 && N > kMaxMN / M) return W12_ERR_SHAPE;
     return check_container(1, N, K);
 }
 
@@ -171,8 +177,9 @@ static int check_moe_shape(int64_t T, int64_t H, int64_t I, int64_t E, int64_t t
     if (H % MX4_BLOCK != 0 || I < MX4_BLOCK || I % MX4_BLOCK != 0) return W12_ERR_SHAPE;
     if (T > MX4_MAX_T || E > MX4_MAX_E || top_k > MX4_MAX_TOP_K) return W12_ERR_UNSUPPORTED;
     if (int rc = check_container(E, H, I)) return rc;
-    if (I >= kMaxK) return W12_ERR_SHAPE;
     if (int rc = check_container(E, 2 * I, H)) return rc;
+    const int64_t pairs = T * top_k, slots = (E < pairs ? E : pairs) + pairs / 16;
+    if (slots * (H / 16) > kMaxMoeBlocks || slots * (I / 16) > kMaxMoeBlocks) return W12_ERR_SHAPE;
     return W12_OK;
 }
 

@@ -21,6 +21,17 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// A grid's x holds fewer than 2^24 workgroups of 256 (work items are counted in 32
+// bits); more go along y.
+constexpr int64_t kGridX = (int64_t)1 << 22;
+dim3 grid_of(int64_t blocks) {
+    return blocks <= kGridX ? dim3((unsigned)blocks)
+                            : dim3((unsigned)kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+__device__ __forceinline__ int64_t block_index() {
+    return (int64_t)blockIdx.y * kGridX + blockIdx.x;
+}
+
 // max over the four lanes of a quad
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);   // 1 0 3 2
@@ -92,10 +103,13 @@ template <bool F32>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restrict__ x, int64_t R,
                                                             int64_t K, int64_t ldx, int64_t ldb,
                                                             int G, int Q, int64_t tiles_mat,
+                                                            int64_t blocks,
                                                             uint8_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
-    const int64_t T = blockIdx.x / Q;               // tile over all matrices
-    const int Qi = (int)(blockIdx.x % Q);
+    const int64_t block = block_index();
+    if (block >= blocks) return;
+    const int64_t T = block / Q;                    // tile over all matrices
+    const int Qi = (int)(block % Q);
     const int64_t mat = T / tiles_mat;
     const int lane = threadIdx.x & 63;
     const int c = (threadIdx.x >> 6) * 4 + (lane >> 4);   // row of the tile
@@ -146,10 +160,13 @@ __device__ __forceinline__ void store16(void* p, u32x4_t v) {
 template <bool F32>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(Mat m, int64_t R, int64_t K, int G,
                                                               int Q, int64_t tiles_mat,
+                                                              int64_t blocks,
                                                               void* __restrict__ y, int64_t ldy,
                                                               int64_t ldb) {
-    const int64_t T = blockIdx.x / Q;
-    const int Qi = (int)(blockIdx.x % Q);
+    const int64_t block = block_index();
+    if (block >= blocks) return;
+    const int64_t T = block / Q;
+    const int Qi = (int)(block % Q);
     const int64_t mat = T / tiles_mat;
     const int lane = threadIdx.x & 63;
     const int c = (threadIdx.x >> 6) * 4 + (lane >> 4);
@@ -215,13 +232,14 @@ hipError_t launch_quantize(const void* x, int x_f32, int64_t B, int64_t R, int64
                            int64_t ldb, uint8_t* codes, uint8_t* scales, hipStream_t s) {
     const int G = (int)groups(K), Q = (int)quads(K);
     const int64_t tm = tiles(R);
-    const dim3 grid((unsigned)(B * tm * Q));
+    const int64_t blocks = B * tm * Q;
+    const dim3 grid = grid_of(blocks);
     if (x_f32)
         hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(kThreads), 0, s, x, R, K, ldx, ldb, G,
-                           Q, tm, codes, scales);
+                           Q, tm, blocks, codes, scales);
     else
         hipLaunchKernelGGL(quantize_kernel<false>, grid, dim3(kThreads), 0, s, x, R, K, ldx, ldb, G,
-                           Q, tm, codes, scales);
+                           Q, tm, blocks, codes, scales);
     return hipGetLastError();
 }
 
@@ -229,13 +247,14 @@ hipError_t launch_dequantize(Mat m, int64_t B, int64_t R, int64_t K, void* y, in
                              int64_t ldy, int64_t ldb, hipStream_t s) {
     const int G = (int)groups(K), Q = (int)quads(K);
     const int64_t tm = tiles(R);
-    const dim3 grid((unsigned)(B * tm * Q));
+    const int64_t blocks = B * tm * Q;
+    const dim3 grid = grid_of(blocks);
     if (y_f32)
         hipLaunchKernelGGL(dequantize_kernel<true>, grid, dim3(kThreads), 0, s, m, R, K, G, Q, tm,
-                           y, ldy, ldb);
+                           blocks, y, ldy, ldb);
     else
         hipLaunchKernelGGL(dequantize_kernel<false>, grid, dim3(kThreads), 0, s, m, R, K, G, Q, tm,
-                           y, ldy, ldb);
+                           blocks, y, ldy, ldb);
     return hipGetLastError();
 }
 
