@@ -301,7 +301,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
             int at = piece;
             if constexpr (!XM) {
                 const int row = piece / (16 * UG), p = piece % (16 * UG);
-                at = row * 16 * UG + (p & ~15) + ((p & 15) ^ (row & 15));
+                at = row * 16 * UG + (p & ~15) + x_place(p & 15, row);
             }
             u32x4_t v;
 #pragma unroll
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
                     for (int t = 0; t < MT; ++t) {
                         const int row = t * 16 + cr;
                         xv[t] = *reinterpret_cast<const bf16x8_t*>(
-                            xl + (row * 16 * UG + 16 * j + ((4 * q + b) ^ (row & 15))) * 16);
+                            xl + (row * 16 * UG + 16 * j + x_place(q, b, row)) * 16);
                     }
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
@@ -429,7 +429,7 @@ template <int MT, int R, int WM, int WN, bool XM, int MIN_WAVES>
 __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a, int mb, int nb) {
     using T = Tile<MT, R, WM, WN, XM>;
     constexpr int P = T::kPieces;
-    constexpr int H0 = XM ? P : (P + 1) / 2;    // x pieces in flight in the first half step
+    constexpr int H0 = XM ? P : (P + 3) / 4;    // x pieces in flight (a quarter step)
     __shared__ __align__(16) uint8_t xs[2][T::kStage];
 
     // Consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
@@ -544,7 +544,7 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
             at = (tid + i * T::kThreads) * 16;
         } else {
             const int r = (tid >> 4) + i * (T::kThreads / 16);
-            at = r * 256 + (((tid & 15) ^ (r & 15)) << 4);
+            at = r * 256 + (x_place(tid & 15, r) << 4);
         }
         u32x4_t v;
 #pragma unroll
@@ -602,39 +602,40 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
             float s[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) s[r] = scale_f32((ws[0][r] >> (8 * J)) & 255u);
-            bf16x8_t xv[2][2], wv[R];
+            bf16x8_t xv[2][2], wv[2][R];
             const uint8_t* xrow = xl + (wm * MT * 16 + c) * 256;
             auto read = [&](int slot, int v) {
                 const int b = v / U, u = v % U;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     xv[slot][h] = *reinterpret_cast<const bf16x8_t*>(
-                        xrow + (2 * u + h) * 4096 + (((4 * q + b) ^ c) << 4));
+                        xrow + (2 * u + h) * 4096 + (x_place(q, b, c) << 4));
             };
             read(0, 0);
 #pragma unroll
+            for (int r = 0; r < R; ++r) wv[0][r] = expand8(wreg[cur][r][0], s[r]);
+#pragma unroll
             for (int v = 0; v < 4 * U; ++v) {
                 const int b = v / U, u = v % U;
-                if (u == 0) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r) wv[r] = expand8(wreg[cur][r][b], s[r]);
-                }
                 if (v + 1 < 4 * U) read((v + 1) & 1, v + 1);
+                if (b < 3) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (r * U / R == u) wv[(b + 1) & 1][r] = expand8(wreg[cur][r][b + 1], s[r]);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        acc[2 * u + h][r] = mfma_bf16(wv[r], xv[v & 1][h], acc[2 * u + h][r]);
+                        acc[2 * u + h][r] = mfma_bf16(wv[b & 1][r], xv[v & 1][h], acc[2 * u + h][r]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (v == 2 * U - 1) {
+                if (u == U - 1) {           // the next quarter of x
 #pragma unroll
-                    for (int i = 0; i < H0; ++i) store_x(i, nxt);
+                    for (int i = b * H0; i < (b + 1) * H0 && i < P; ++i) store_x(i, nxt);
 #pragma unroll
-                    for (int i = H0; i < P; ++i) load_x(i, g + 1);
+                    for (int i = (b + 1) * H0; i < (b + 2) * H0 && i < P; ++i) load_x(i, g + 1);
                 }
             }
-#pragma unroll
-            for (int i = H0; i < P; ++i) store_x(i, nxt);
         }
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);

@@ -81,6 +81,19 @@ __device__ __forceinline__ uint16_t bf16_bits(float f) {
     return __builtin_bit_cast(uint16_t, h);
 }
 
+// Place, of 16, of x's piece q, b (values 32 q + 8 b .. + 7 of a group) in LDS row
+// `row`.  A read takes one b from 16 rows for each q; the LDS serves it 16 lanes
+// at a time, rows 0-3 and 12-15 of one q with rows 4-11 of the next, whose places
+// differ for this order of the pieces (with 4 q + b in front of the row's bits they
+// coincide: a third of the LDS cycles of QKV M = 2048 were such conflicts).
+__host__ __device__ constexpr int x_place(int q, int b, int row) {
+    return (4 * b + q) ^ (row & 15);
+}
+// The same for piece p = 4 q + b.
+__host__ __device__ constexpr int x_place(int p, int row) {
+    return x_place((p >> 2) & 3, p & 3, row);
+}
+
 struct GemmArgs {
     const uint16_t* x;      // BF16 activations (or NULL: xm)
     int64_t ldx;

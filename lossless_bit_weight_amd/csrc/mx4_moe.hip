@@ -348,7 +348,7 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
         for (int i = 0; i < P; ++i) {
             const int piece = (i * WN + wn) * 64 + lane;
             const int row = piece % kPart / (16 * UG);
-            const int at = (piece & ~15) + ((piece & 15) ^ (row & 15));
+            const int at = (piece & ~15) + x_place(piece & 15, row);
             u32x4_t v;
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[k] = xin[i] ? xb[i][k] : 0u;
@@ -373,7 +373,7 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
 #pragma unroll
                 for (int p = 0; p < PARTS; ++p)
                     xv[p] = *reinterpret_cast<const bf16x8_t*>(
-                        xl + (p * kPart + row * 16 * UG + 16 * j + ((4 * q + b) ^ row)) * 16);
+                        xl + (p * kPart + row * 16 * UG + 16 * j + x_place(q, b, row)) * 16);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const bf16x8_t wv = expand8(wb[s][j][r][b], f[r]);
