@@ -655,38 +655,51 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
     }
 
     // lane (c, q): row c of a 16-row tile of x, weight rows 4 q .. 4 q + 3
-    const int64_t n0 = (int64_t)bn * T::BN + wn * R * 16 + 4 * q;
+    const int64_t n0 = (int64_t)bn * T::BN + wn * R * 16;
     const bool f32 = a.S > 1 || a.y_f32;
     const int64_t ld = a.S > 1 ? a.N : a.ldy;
     uint8_t* out = a.S > 1 ? reinterpret_cast<uint8_t*>(a.part + (int64_t)slice * a.M * a.N)
                            : static_cast<uint8_t*>(a.y);
     const int size = f32 ? 4 : 2;
-    // four outputs in one store where every row of y starts on such a boundary
-    const bool wide = ld % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (4 * size - 1)) == 0;
+    // 16 bytes at a time where every row of y starts on such a boundary
+    const bool wide = ld % (16 / size) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int64_t m = m0 + (wm * MT + i) * 16 + c;
         uint8_t* o = out + (m * ld + n0) * size;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int left = m < a.M ? (int)(a.N - n0 - 16 * r < 4 ? a.N - n0 - 16 * r : 4) : 0;
-            uint8_t* p = o + 16 * r * size;
-            const f32x4_t v = acc[i][r];
-            if (left == 4 && wide) {
-                if (f32)
-                    *reinterpret_cast<f32x4_t*>(p) = v;
-                else
-                    *reinterpret_cast<u32x2_t*>(p) =
-                        u32x2_t{bf16_bits(v[0]) | (uint32_t)bf16_bits(v[1]) << 16,
-                                bf16_bits(v[2]) | (uint32_t)bf16_bits(v[3]) << 16};
-            } else {
+        for (int r = 0; r < R; r += 2) {
+            if (!f32 && wide && n0 + 16 * (r + 2) <= a.N) {
+                // BF16: lanes q and q ^ 1 trade halves of two tiles, and hold eight outputs
+                // in a row each (64 bytes of a row a store instead of 32)
+                const f32x4_t v = acc[i][r], w2 = acc[i][r + 1];
+                uint32_t p0 = bf16_bits(v[0]) | (uint32_t)bf16_bits(v[1]) << 16;
+                uint32_t p1 = bf16_bits(v[2]) | (uint32_t)bf16_bits(v[3]) << 16;
+                uint32_t p2 = bf16_bits(w2[0]) | (uint32_t)bf16_bits(w2[1]) << 16;
+                uint32_t p3 = bf16_bits(w2[2]) | (uint32_t)bf16_bits(w2[3]) << 16;
+                swap16(p0, p2);
+                swap16(p1, p3);
+                if (m < a.M)
+                    *reinterpret_cast<u32x4_t*>(o + 2 * (16 * (r + (q & 1)) + 8 * (q >> 1))) =
+                        u32x4_t{p0, p1, p2, p3};
+                continue;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 16 * (r + h) + 4 * q;
+                const f32x4_t v = acc[i][r + h];
+                const int64_t left = m < a.M ? a.N - n0 - n : 0;
+                if (f32 && wide && left >= 4) {
+                    *reinterpret_cast<f32x4_t*>(o + 4 * n) = v;
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if (e >= left) continue;
                     if (f32)
-                        reinterpret_cast<float*>(p)[e] = v[e];
+                        reinterpret_cast<float*>(o)[n + e] = v[e];
                     else
-                        reinterpret_cast<uint16_t*>(p)[e] = bf16_bits(v[e]);
+                        reinterpret_cast<uint16_t*>(o)[n + e] = bf16_bits(v[e]);
                 }
             }
         }

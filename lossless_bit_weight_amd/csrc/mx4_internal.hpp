@@ -81,6 +81,13 @@ __device__ __forceinline__ uint16_t bf16_bits(float f) {
     return __builtin_bit_cast(uint16_t, h);
 }
 
+// Odd rows of 16 lanes of a and even rows of b change places.
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
 // Place, of 16, of x's piece q, b (values 32 q + 8 b .. + 7 of a group) in LDS row
 // `row`.  A read takes one b from 16 rows for each q; the LDS serves it 16 lanes
 // at a time, rows 0-3 and 12-15 of one q with rows 4-11 of the next, whose places
