@@ -284,7 +284,8 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
             const int g = uc * UG + j < a.G ? uc * UG + j : a.G - 1;
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                wb[slot][j][r] = load16_nt(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
+                wb[slot][j][r] =
+                    load16<ROWS == 4>(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
         }
     };
     // x is waited for first; four rows of it arrive before the weights in any order,
@@ -785,8 +786,9 @@ int spread(int64_t units, int64_t mb) {
 //     M = 1 14.3 against 15.6, M = 16, K in six slices, 17.5 against 23.5).  MX4 x
 //     is a quarter of the bytes: shared or not within 3%.
 //   17 rows to 128 (MX4 x: 256) and few tiles: 16 (32, 64) rows a workgroup, whose
-//     weights the row blocks beside it find in L2 (QKV M = 64 16.3, M = 128 22.3; a
-//     64 x 128 tile in four slices 21.2 and 24.9).
+//     weights the row blocks beside it find in L2 (QKV M = 64 13.9, M = 128 19.7; a
+//     64 x 128 tile in four slices 21.2 and 24.9.  MX4 x: 16 rows at M = 32 7.5, 32
+//     rows 9.1; 32 rows at M = 128 11.5, 64 rows 14.0).
 //   17 to 64 and many tiles: 32 rows (MX4 x: up to 64), waves as spread() says
 //     (gate+up M = 64 42.5 with two tiles a wave, 50.4 with 64 x 128 tiles).
 //   above: the largest tile that still gives 440 workgroups (QKV M = 512 44.8 with
@@ -821,11 +823,12 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
             p.kernel = M <= 32 ? kMid32 : kMid32R2;
         p.wn = p.kernel == kMid32R2 ? spread((nt + 1) / 2, (M + 31) / 32) : spread(nt, 1);
     } else if (xm && !many && M <= 256) {
-        p.kernel = lengthy || M > 64 ? kMid64 : kMid32x2;
+        p.kernel = lengthy ? kMid64 : M <= 32 ? kMid16x2 : M <= 128 ? kMid32x2 : kMid32;
+        if (p.kernel == kMid32) p.wn = spread(nt, (M + 31) / 32);
         if (lengthy) S = slices(400, blocks(64, 64));
     } else if (!xm && !many && M <= (lengthy ? 64 : 128)) {
         p.kernel = !lengthy && M <= 32 ? kMid16x2 : kMid16;
-        p.wn = lengthy || M > 64 ? 8 : 4;
+        p.wn = 8;
         if (lengthy) S = slices(480, blocks(16, 128));
     } else if (blocks(128, 256) >= 440) {
         p.kernel = kTile128;
@@ -873,6 +876,7 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     if (!xm && k >= kTile64 && a.ldx >= (1 << 23)) k = kSmall;
     if (k == kSmall) a.S = 1;
     if (xm) switch (k) {
+        case kMid16x2: return launch_mid<16, 1, 2, 2, 4, true>(a, s);
         case kMid32: return launch_mid_waves<32, 1, true>(p.wn, a, s);
         case kMid32x2: return launch_mid<32, 1, 4, 2, 4, true>(a, s);
         case kMid64: return launch_mid_waves<64, 1, true>(p.wn, a, s);

@@ -75,6 +75,12 @@ __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
     return p;
 }
 
+template <bool NT>
+__device__ __forceinline__ u32x4_t load16(const uint8_t* p) {
+    if constexpr (NT) return load16_nt(p);
+    return *reinterpret_cast<const u32x4_t*>(p);
+}
+
 // fp32 -> BF16 bits, to nearest even (NaN stays NaN).
 __device__ __forceinline__ uint16_t bf16_bits(float f) {
     const __bf16 h = (__bf16)f;

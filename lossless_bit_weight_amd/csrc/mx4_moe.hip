@@ -251,7 +251,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
 // of UG groups of K.  Weights come to registers a unit ahead of their products;
 // the slot's rows (of x, gathered by token, or of h in PARTS parts) go through
 // LDS, double-buffered, in the layout of mx4_gemm.hip's few-row kernel, ROWS of
-// them: slots of up to four rows, the most by far, move a quarter of the bytes.
+// them: slots of up to four rows, the most by far, move a quarter of the bytes, and
+// read weights that no other slot does (16 tokens 106 us past the caches, 116
+// through them; 128 tokens at 16 an expert the reverse, 109 and 102).
 template <bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
 struct Expert {
     static constexpr int kThreads = WN * KW * 64;
@@ -334,7 +336,8 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
             const int g = uc * UG + j < G ? uc * UG + j : G - 1;
 #pragma unroll
             for (int r = 0; r < R; ++r)
-                wb[s][j][r] = load16_nt(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
+                wb[s][j][r] =
+                    load16<ROWS == 4>(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
