@@ -430,7 +430,11 @@ template <int MT, int R, int WM, int WN, bool XM, int MIN_WAVES>
 __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a, int mb, int nb) {
     using T = Tile<MT, R, WM, WN, XM>;
     constexpr int P = T::kPieces;
-    constexpr int H0 = XM ? P : (P + 3) / 4;    // x pieces in flight (a quarter step)
+    // BF16 x comes in kRuns runs of H0 pieces a step, each asked for when the one before
+    // is stored: as few in flight as the registers left of 8 x 4 sums ask for, but time
+    // to arrive with fewer (64 rows in quarters: QKV M = 512 61.5 us, in halves 45)
+    constexpr int kRuns = MT * R >= 32 ? 4 : 2;
+    constexpr int H0 = XM ? P : (P + kRuns - 1) / kRuns;
     __shared__ __align__(16) uint8_t xs[2][T::kStage];
 
     // Consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
@@ -630,11 +634,14 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
                     for (int r = 0; r < R; ++r)
                         acc[2 * u + h][r] = mfma_bf16(wv[b & 1][r], xv[v & 1][h], acc[2 * u + h][r]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (u == U - 1) {           // the next quarter of x
+                if ((v + 1) % (4 * U / kRuns) == 0) {
+                    constexpr int kLen = 4 * U / kRuns;
+                    const int run = v / kLen;
 #pragma unroll
-                    for (int i = b * H0; i < (b + 1) * H0 && i < P; ++i) store_x(i, nxt);
+                    for (int i = run * H0; i < (run + 1) * H0 && i < P; ++i) store_x(i, nxt);
 #pragma unroll
-                    for (int i = (b + 1) * H0; i < (b + 2) * H0 && i < P; ++i) load_x(i, g + 1);
+                    for (int i = (run + 1) * H0; i < (run + 2) * H0 && i < P; ++i)
+                        load_x(i, g + 1);
                 }
             }
         }
