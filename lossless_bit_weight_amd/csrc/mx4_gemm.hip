@@ -410,8 +410,11 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
 // ---- many rows of x -------------------------------------------------------------
 // A workgroup of WM x WN waves computes 16 MT WM rows of x by 16 R WN weight
 // rows; a wave 16 MT by 16 R, its sums in registers.  Weight pieces go from
-// memory to registers in the layout the matrix instructions take them (a group
-// ahead), x through LDS, double-buffered, where the WN waves share it.
+// memory to registers in the layout the matrix instructions take them, x through
+// LDS, double-buffered, where the WN waves share it; both are asked for one group
+// ahead, or two (DEEP) where the sums leave the registers for it.  64 x 128 tiles,
+// us, one group ahead / two: gate+up M = 128 71 / 58, MX4 x 37.4 / 30.5; 128 x 256
+// tiles of MX4 x, QKV M = 4096, 90.9 / 87.9.
 // BF16 x: LDS row m holds 16 pieces of 8 values, piece p at place p ^ (m % 16),
 // so that the 16 rows a read takes one piece from lie in 16 different places.
 // MX4 x: its own blocks, in lane order.
@@ -426,15 +429,16 @@ struct Tile {
     static constexpr int kStage = kPieces * kThreads * 16;          // bytes of LDS a group
 };
 
-template <int MT, int R, int WM, int WN, bool XM, int MIN_WAVES>
-__global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a, int mb, int nb) {
+template <int MT, int R, int WM, int WN, bool XM, bool DEEP>
+__global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(GemmArgs a, int mb, int nb) {
     using T = Tile<MT, R, WM, WN, XM>;
     constexpr int P = T::kPieces;
     // BF16 x comes in kRuns runs of H0 pieces a step, each asked for when the one before
-    // is stored: as few in flight as the registers left of 8 x 4 sums ask for, but time
-    // to arrive with fewer (64 rows in quarters: QKV M = 512 61.5 us, in halves 45)
-    constexpr int kRuns = MT * R >= 32 ? 4 : 2;
-    constexpr int H0 = XM ? P : (P + kRuns - 1) / kRuns;
+    // is stored: no more in flight than the registers that 8 x 4 sums leave.  DEEP has
+    // the registers to ask for all of them, a step earlier.
+    constexpr int kRuns = XM || DEEP ? 1 : 4;
+    constexpr int H0 = (P + kRuns - 1) / kRuns;
+    constexpr int kAhead = DEEP ? 2 : 1;        // steps
     __shared__ __align__(16) uint8_t xs[2][T::kStage];
 
     // Consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
@@ -500,8 +504,8 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
         xbase = reinterpret_cast<const uint8_t*>(a.x + (int64_t)m0 * a.ldx);
     }
 
-    u32x4_t wreg[2][R], xreg[P];
-    bool xin = true;
+    u32x4_t wreg[2 * kAhead][R], xreg[kAhead][P];
+    bool xin[kAhead];
     uint32_t ws[2][R], xsc[2][XM ? MT : 1];
     auto load_w = [&](int slot, int g) {
         const int gg = g < ge ? g : ge - 1;
@@ -523,11 +527,11 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
     };
     // (no branch: a load past the last group, row or K reads a valid place and is
     // replaced by zeros or, past the last tile and step, never used)
-    auto load_x = [&](int i, int g) {
+    auto load_x = [&](int set, int i, int g) {
         const int gg = g < ge ? g : ge - 1;
         bool in = g < ge;
         if constexpr (XM) {
-            xreg[i] = *reinterpret_cast<const u32x4_t*>(
+            xreg[set][i] = *reinterpret_cast<const u32x4_t*>(
                 scalar(xbase + ((int64_t)voff[i] * a.G + gg) * kCodeBlock) + lane16);
         } else {
             const bool k_in = 128 * gg + 8 * (tid & 15) < a.K;
@@ -538,12 +542,12 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
             asm volatile("" : "+s"(stride));
             uint32_t r = (tid >> 4) + i * (T::kThreads / 16);
             r = r < row_last ? r : row_last;
-            xreg[i] = *reinterpret_cast<const u32x4_t*>(
+            xreg[set][i] = *reinterpret_cast<const u32x4_t*>(
                 xbase + 256 * (int64_t)gg + (__umul24(r, stride) + (k_in ? 16u * (tid & 15) : 0u)));
         }
-        xin = in;
+        xin[set] = in;
     };
-    auto store_x = [&](int i, int buf) {
+    auto store_x = [&](int set, int i, int buf) {
         int at;
         if constexpr (XM) {
             at = (tid + i * T::kThreads) * 16;
@@ -553,7 +557,7 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
         }
         u32x4_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = xin ? xreg[i][e] : 0u;
+        for (int e = 0; e < 4; ++e) v[e] = xin[set] ? xreg[set][i][e] : 0u;
         *reinterpret_cast<u32x4_t*>(&xs[buf][at]) = v;
     };
 
@@ -563,20 +567,29 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[i][r] = f32x4_t{0, 0, 0, 0};
 
+#pragma unroll
+    for (int i = 0; i < P; ++i) load_x(0, i, gb);
     load_w(0, gb);
     load_scales(0, gb);
+    if constexpr (DEEP) load_w(1, gb + 1);
 #pragma unroll
-    for (int i = 0; i < P; ++i) load_x(i, gb);
+    for (int i = 0; i < P; ++i) store_x(0, i, 0);
+    if constexpr (DEEP) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) store_x(i, 0);
+        for (int i = 0; i < P; ++i) load_x(1, i, gb + 1);
+    }
     __syncthreads();
 
     auto step = [&](auto jc, int g) {
         constexpr int J = decltype(jc)::value;
         constexpr int cur = J & 1, nxt = cur ^ 1;
-        load_w(nxt, g + 1);
+        // DEEP: the registers of x that hold this step's, stored before it, take the
+        // step's after the next
+        constexpr int set = DEEP ? cur : 0, next_set = DEEP ? nxt : 0;
+        constexpr int wcur = J & (2 * kAhead - 1);
+        load_w((J + kAhead) & (2 * kAhead - 1), g + kAhead);
 #pragma unroll
-        for (int i = 0; i < H0; ++i) load_x(i, g + 1);
+        for (int i = 0; i < H0; ++i) load_x(set, i, g + kAhead);
         // x operands are read two tiles (of 16 rows) ahead of the products on them
         constexpr int U = MT / 2;
         const uint8_t* xl = &xs[cur][0];
@@ -597,12 +610,12 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
 #pragma unroll
                     for (int r = 0; r < R; ++r)
                         acc[2 * u + h][r] =
-                            mfma_mx4<J>(operand4(wreg[cur][r]), operand4(xv[u & 1][h]),
+                            mfma_mx4<J>(operand4(wreg[wcur][r]), operand4(xv[u & 1][h]),
                                         acc[2 * u + h][r], ws[0][r], xsc[0][2 * u + h]);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int i = 0; i < P; ++i) store_x(i, nxt);
+            for (int i = 0; i < P; ++i) store_x(next_set, i, nxt);
         } else {
             float s[R];
 #pragma unroll
@@ -618,7 +631,7 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
             };
             read(0, 0);
 #pragma unroll
-            for (int r = 0; r < R; ++r) wv[0][r] = expand8(wreg[cur][r][0], s[r]);
+            for (int r = 0; r < R; ++r) wv[0][r] = expand8(wreg[wcur][r][0], s[r]);
 #pragma unroll
             for (int v = 0; v < 4 * U; ++v) {
                 const int b = v / U, u = v % U;
@@ -626,7 +639,8 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
                 if (b < 3) {
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        if (r * U / R == u) wv[(b + 1) & 1][r] = expand8(wreg[cur][r][b + 1], s[r]);
+                        if (r * U / R == u) 
+                            wv[(b + 1) & 1][r] = expand8(wreg[wcur][r][b + 1], s[r]);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -638,10 +652,11 @@ __global__ __launch_bounds__(WM* WN * 64, MIN_WAVES) void tile_kernel(GemmArgs a
                     constexpr int kLen = 4 * U / kRuns;
                     const int run = v / kLen;
 #pragma unroll
-                    for (int i = run * H0; i < (run + 1) * H0 && i < P; ++i) store_x(i, nxt);
+                    for (int i = run * H0; i < (run + 1) * H0 && i < P; ++i)
+                        store_x(next_set, i, nxt);
 #pragma unroll
                     for (int i = (run + 1) * H0; i < (run + 2) * H0 && i < P; ++i)
-                        load_x(i, g + 1);
+                        load_x(set, i, g + 1);
                 }
             }
         }
@@ -732,12 +747,12 @@ hipError_t launch_join(const GemmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int MT, int R, int WM, int WN, bool XM, int MIN_WAVES>
+template <int MT, int R, int WM, int WN, bool XM, bool DEEP>
 hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
     using T = Tile<MT, R, WM, WN, XM>;
     const int mb = (a.M + T::BM - 1) / T::BM;
     const int nb = (int)((a.N + T::BN - 1) / T::BN);
-    hipLaunchKernelGGL((tile_kernel<MT, R, WM, WN, XM, MIN_WAVES>),
+    hipLaunchKernelGGL((tile_kernel<MT, R, WM, WN, XM, DEEP>),
                        dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S), dim3(T::kThreads), 0, s,
                        a, mb, nb);
     return launch_join(a, s);
@@ -759,7 +774,7 @@ hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
 // Kernel and split of a product.
 enum Kernel {
     kSmall, kMid4, kMid4Long, kMid16, kMid16x2, kMid32, kMid32R2, kMid32x2, kMid64,
-    kTile64, kTileMid, kTile128
+    kTileSmall, kTileMid, kTile128
 };
 struct Plan {
     Kernel kernel;
@@ -798,9 +813,12 @@ int spread(int64_t units, int64_t mb) {
 //     rows 9.1; 32 rows at M = 128 11.5, 64 rows 14.0).
 //   17 to 64 and many tiles: 32 rows (MX4 x: up to 64), waves as spread() says
 //     (gate+up M = 64 42.5 with two tiles a wave, 50.4 with 64 x 128 tiles).
-//   above: the largest tile that still gives 440 workgroups (QKV M = 512 44.8 with
-//     64 x 128 tiles, 52.5 with 128 x 256; M = 2048 the reverse), K in slices if the
-//     smallest does not.
+//   above: 128 x 256 if that gives 440 workgroups (QKV M = 2048 115, 64 x 256 125.5);
+//     else, BF16 x, 64 x 256 if that gives 440 (QKV M = 1024 64.9, 128 x 256 75.5) or
+//     nearly one a CU (QKV M = 512 39.2, 128 x 256 51.7), then 32 x 256 (QKV M = 256
+//     29.2, 64 x 256 in two slices 32.4; gate+up M = 128 59.4, 64 x 256 on 272
+//     workgroups 64.1); MX4 x 128 x 128, then 64 x 128 (QKV M = 512 21.8, 128 x 256
+//     30.2); K in slices if that is too few.
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
     const int G = (int)groups(K), Q = (int)quads(K);
     const int64_t nt = tiles(N);
@@ -839,11 +857,17 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         if (lengthy) S = slices(480, blocks(16, 128));
     } else if (blocks(128, 256) >= 440) {
         p.kernel = kTile128;
-    } else if (xm ? blocks(128, 128) >= 440 : blocks(64, 256) >= 440) {
+    } else if (xm) {
+        p.kernel = blocks(128, 128) >= 440 ? kTileMid : kTileSmall;
+        if (p.kernel == kTileSmall) S = slices(544, blocks(64, 128));
+    } else if (blocks(64, 256) >= 440 || (blocks(64, 256) >= 200 &&
+                                          (lengthy || blocks(64, 256) <= 256))) {
         p.kernel = kTileMid;
+        if (lengthy && blocks(64, 256) < 440) S = slices(960, blocks(64, 256));
     } else {
-        p.kernel = kTile64;
-        S = slices(544, blocks(64, 128));
+        p.kernel = kTileSmall;
+        S = slices(480, blocks(32, 256));
+        if (!lengthy && blocks(32, 256) >= 200) S = 1;
     }
     if (S > Q) S = Q;
     if (S < 1) S = 1;
@@ -880,16 +904,16 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     a.part = static_cast<float*>(ws);
     Kernel k = p.kernel;
     // the tile kernel's row offsets are products of 24-bit numbers
-    if (!xm && k >= kTile64 && a.ldx >= (1 << 23)) k = kSmall;
+    if (!xm && k >= kTileSmall && a.ldx >= (1 << 23)) k = kSmall;
     if (k == kSmall) a.S = 1;
     if (xm) switch (k) {
         case kMid16x2: return launch_mid<16, 1, 2, 2, 4, true>(a, s);
         case kMid32: return launch_mid_waves<32, 1, true>(p.wn, a, s);
         case kMid32x2: return launch_mid<32, 1, 4, 2, 4, true>(a, s);
         case kMid64: return launch_mid_waves<64, 1, true>(p.wn, a, s);
-        case kTile64: return launch_tile<4, 2, 1, 4, true, 2>(a, s);
-        case kTileMid: return launch_tile<8, 2, 1, 4, true, 2>(a, s);
-        case kTile128: return launch_tile<8, 4, 1, 4, true, 2>(a, s);
+        case kTileSmall: return launch_tile<4, 2, 1, 4, true, true>(a, s);
+        case kTileMid: return launch_tile<8, 2, 1, 4, true, true>(a, s);
+        case kTile128: return launch_tile<8, 4, 1, 4, true, true>(a, s);
         default: return launch_small<2, 8, 2, true>(a, s);
     }
     switch (k) {
@@ -901,9 +925,9 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
         case kMid16x2: return launch_mid<16, 1, 4, 2, 4, false>(a, s);
         case kMid32: return launch_mid_waves<32, 1, false>(p.wn, a, s);
         case kMid32R2: return launch_mid_waves<32, 2, false>(p.wn, a, s);
-        case kTile64: return launch_tile<4, 2, 1, 4, false, 2>(a, s);
-        case kTileMid: return launch_tile<4, 4, 1, 4, false, 2>(a, s);
-        case kTile128: return launch_tile<8, 4, 1, 4, false, 2>(a, s);
+        case kTileSmall: return launch_tile<2, 4, 1, 4, false, true>(a, s);
+        case kTileMid: return launch_tile<4, 4, 1, 4, false, true>(a, s);
+        case kTile128: return launch_tile<8, 4, 1, 4, false, false>(a, s);
         default: return launch_small<2, 4, 3, false>(a, s);
     }
 }
