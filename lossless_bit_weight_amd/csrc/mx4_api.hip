@@ -14,9 +14,9 @@ namespace {
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 constexpr int64_t kMaxK = (int64_t)1 << 24;
 constexpr int64_t kMaxM = (int64_t)1 << 24;
-// A launch counts its work items along x in 32 bits: N and M * N below these keep
-// every product's grid within.
-constexpr int64_t kMaxN = (int64_t)1 << 28;
+// A launch counts its work items along x in 32 bits: N and M * N up to these keep
+// every product's grid within (2^27 / 32 workgroups of 512 in the few-row kernel).
+constexpr int64_t kMaxN = (int64_t)1 << 27;
 constexpr int64_t kMaxMN = (int64_t)1 << 37;
 // The same for the expert layer: slots times tiles of its outputs.
 constexpr int64_t kMaxMoeBlocks = (int64_t)1 << 24;
@@ -70,7 +70,8 @@ int gemm(const uint16_t* x, int64_t ldx, mx4::Mat xm, int64_t M, mx4::Mat w, int
          void* y, int64_t ldy, int y_type, void* ws, size_t ws_bytes, void* stream) {
     if (int rc = check_y(y, N, ldy, y_type)) return rc;
     if (!aligned(w.codes, 16) || !aligned(w.scales, 16)) return W12_ERR_ALIGN;
-    if (int rc = check_ws(ws, ws_bytes, mx4::gemm_workspace_bytes(M, N, K, x == nullptr))) return rc;
+    const size_t need = mx4::gemm_workspace_bytes(M, N, K, x == nullptr);
+    if (int rc = check_ws(ws, ws_bytes, need)) return rc;
     if (M == 0) return W12_OK;
     mx4::GemmArgs a{};
     a.x = x;
@@ -96,10 +97,14 @@ const char* mx4_status_string(int status) {
     switch (status) {
         case W12_OK: return "ok";
         case W12_ERR_NULL: return "a required pointer is NULL";
-        case W12_ERR_SHAPE: return "bad shape (K and I are positive multiples of 32 below 2^24, N >= 1, row strides cover their rows, 1 <= top_k <= E)";
-        case W12_ERR_ALIGN: return "misaligned pointer or stride (16-byte rows of x, containers and decoded rows)";
+        case W12_ERR_SHAPE:
+            return "bad shape (K and I are positive multiples of 32 below 2^24, N >= 1, row "
+                   "strides cover their rows, 1 <= top_k <= E)";
+        case W12_ERR_ALIGN:
+            return "misaligned pointer or stride (16-byte rows of x, containers and decoded rows)";
         case W12_ERR_DTYPE: return "unknown element type";
-        case W12_ERR_UNSUPPORTED: return "more tokens, experts or experts a token than mx4_moe takes";
+        case W12_ERR_UNSUPPORTED:
+            return "more tokens, experts or experts a token than mx4_moe takes";
         case W12_ERR_HIP: return "HIP launch failed";
         case W12_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
         default: return "unknown status";

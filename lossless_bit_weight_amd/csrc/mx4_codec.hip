@@ -189,8 +189,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(Mat m, int64_t R, 
             for (int j = 0; j < 4; ++j) {
                 d[j][h] = 0;
                 if (k0 + 128 * j + 64 * h + 4 * p < K)
-                    d[j][h] = *reinterpret_cast<const uint16_t*>(codes + j * kCodeBlock + piece * 16 +
-                                                                 2 * (p & 7));
+                    d[j][h] = *reinterpret_cast<const uint16_t*>(
+                        codes + j * kCodeBlock + piece * 16 + 2 * (p & 7));
             }
         }
 #pragma unroll

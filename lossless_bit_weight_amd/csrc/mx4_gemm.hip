@@ -255,8 +255,8 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int64_t tt = m0 / 16 + t < last ? m0 / 16 + t : last;
-                xs[slot][t] = *reinterpret_cast<const uint32_t*>(
-                                  scalar(a.xm.scales + tt * a.Q * kScaleBlock + so) + lane4) >> shift;
+                const uint8_t* p = scalar(a.xm.scales + tt * a.Q * kScaleBlock + so);
+                xs[slot][t] = *reinterpret_cast<const uint32_t*>(p + lane4) >> shift;
             }
         } else {
 #pragma unroll
@@ -517,7 +517,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(GemmArgs a, int mb
     auto load_scales = [&](int slot, int g) {
         const int64_t o = (int64_t)((g < ge ? g : ge - 1) >> 2) * kScaleBlock;
 #pragma unroll
-        for (int r = 0; r < R; ++r) 
+        for (int r = 0; r < R; ++r)
             ws[slot][r] = *reinterpret_cast<const uint32_t*>(scalar(sp[r] + o) + lane4);
         if constexpr (XM) {
 #pragma unroll
@@ -639,14 +639,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void tile_kernel(GemmArgs a, int mb
                 if (b < 3) {
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        if (r * U / R == u) 
+                        if (r * U / R == u)
                             wv[(b + 1) & 1][r] = expand8(wreg[wcur][r][b + 1], s[r]);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        acc[2 * u + h][r] = mfma_bf16(wv[b & 1][r], xv[v & 1][h], acc[2 * u + h][r]);
+                        acc[2 * u + h][r] =
+                            mfma_bf16(wv[b & 1][r], xv[v & 1][h], acc[2 * u + h][r]);
                 __builtin_amdgcn_sched_barrier(0);
                 if ((v + 1) % (4 * U / kRuns) == 0) {
                     constexpr int kLen = 4 * U / kRuns;

@@ -76,7 +76,7 @@ GEMM_BAD = [(dict(w=None), -1), (dict(ws=None), -1), (dict(y=None), -1), (dict(M
             (dict(M=(1 << 24) + 1), -2), (dict(N=0), -2), (dict(K=33), -2), (dict(ldy=31), -2),
             (dict(yt=2), -4), (dict(w=MIS), -3), (dict(ws=MIS), -3), (dict(y=P(4097)), -3),
             (dict(yt=1, y=P(4098)), -3), (dict(x=None), -1), (dict(x=MIS), -3),
-            (dict(N=1 << 40, ldy=1 << 40), -2), (dict(N=(1 << 28) + 1, ldy=1 << 29), -2),
+            (dict(N=1 << 40, ldy=1 << 40), -2), (dict(N=(1 << 27) + 1, ldy=1 << 29), -2),
             (dict(M=1 << 24, N=(1 << 13) + 1, ldy=1 << 14), -2)]
 
 
@@ -112,6 +112,7 @@ def test_gemm_workspace(x_mx4):
     assert L.mx4_gemm_workspace_bytes(1, 16, 33, 0, ctypes.byref(n)) == -2 and n.value == 0
     assert L.mx4_gemm_workspace_bytes(1, 16, 32, 0, None) == -1
     assert mx4.mx4_gemm_workspace_bytes(0, 16, 32) == 0
+    assert mx4.mx4_gemm_workspace_bytes(1, 1 << 27, 32, x_mx4) == 0
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -123,7 +124,8 @@ def test_gemm_workspace(x_mx4):
     (dict(ldl=3), -2), (dict(ldy=63), -2), (dict(yt=2), -4), (dict(x=MIS), -3),
     (dict(l=P(4098)), -3), (dict(a=MIS), -3), (dict(b=MIS), -3), (dict(c=MIS), -3),
     (dict(d=MIS), -3), (dict(y=P(4097)), -3), (dict(w=None), -8), (dict(w=MIS), -8),
-    (dict(n=100), -8), (dict(I=1 << 24), -2), (dict(H=1 << 23, ldx=1 << 23, ldy=1 << 23, T=128, E=64, ldl=64, k=32), -2)])
+    (dict(n=100), -8), (dict(I=1 << 24), -2),
+    (dict(H=1 << 23, ldx=1 << 23, ldy=1 << 23, T=128, E=64, ldl=64, k=32), -2)])
 def test_moe_rejects(kw, status):
     a = dict(x=A, T=2, ldx=64, l=A, ldl=4, a=A, b=A, c=A, d=A, H=64, I=32, E=4, k=2, y=A, ldy=64,
              yt=0, w=A, n=1 << 30)
