@@ -190,57 +190,67 @@ def _same(device: int, *others: int) -> None:
             raise ValueError("tensors on devices %d and %d in one call" % (device, o))
 
 
-def _gpu(t: torch.Tensor, what: str) -> torch.Tensor:
-    if not t.is_cuda:
+def _gpu(t: torch.Tensor, what: str) -> int:
+    """The index of the tensor's GPU."""
+    device = t.get_device()
+    if device < 0:
         raise ValueError("%s must be a GPU tensor" % what)
-    return t
+    return device
 
 
-def _rows(t: torch.Tensor, what: str) -> int:
-    """Row stride of a 2-D tensor with contiguous rows (its width if it has
-    one row: such a stride says nothing)."""
-    if t.dim() != 2:
+def _rows(t: torch.Tensor, what: str) -> tuple:
+    """(rows, width, row stride) of a 2-D tensor with contiguous rows (one row:
+    its width, as its stride says nothing)."""
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("%s must be 2-D" % what)
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    R, K = shape
+    ld, unit = t.stride()
+    if unit != 1 and K > 1:
         raise ValueError("%s must have unit column stride" % what)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return R, K, ld if R > 1 else K
 
 
 def _batched(t: torch.Tensor, what: str) -> tuple:
     """(batch or None, R, K, row stride, matrix stride) of a 2-D or 3-D tensor."""
-    if t.dim() not in (2, 3):
+    shape = t.shape
+    if len(shape) == 2:
+        return None, *_rows(t, what), 0
+    if len(shape) != 3:
         raise ValueError("%s must be 2-D or 3-D" % what)
-    R, K = t.shape[-2:]
-    if t.stride(-1) != 1 and K > 1:
+    B, R, K = shape
+    ldb, ld, unit = t.stride()
+    if unit != 1 and K > 1:
         raise ValueError("%s must have unit column stride" % what)
-    ld = t.stride(-2) if R > 1 else K
-    if t.dim() == 2:
-        return None, R, K, ld, 0
-    return t.shape[0], R, K, ld, t.stride(0)
+    return B, R, K, ld if R > 1 else K, ldb
 
 
-def _output(y, M: int, N: int, out_dtype: torch.dtype, device) -> tuple:
-    """(y, row stride, type) of a given or new [M, N] output."""
+# (new_empty on a tensor at hand takes 0.4 us less of the host than torch.empty with
+# its device)
+def _output(y, M: int, N: int, out_dtype: torch.dtype, device: int, like: torch.Tensor) -> tuple:
+    """(y, row stride, type) of a given [M, N] output or a new one beside `like`."""
     if y is None:
         if out_dtype is torch.float32:
-            return torch.empty((M, N), dtype=out_dtype, device=device), N, OUT_F32
+            return like.new_empty((M, N), dtype=out_dtype), N, OUT_F32
         if out_dtype is torch.bfloat16:
-            return torch.empty((M, N), dtype=out_dtype, device=device), N, OUT_BF16
+            return like.new_empty((M, N), dtype=out_dtype), N, OUT_BF16
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-    ld = _rows(_gpu(y, "y"), "y")
-    if tuple(y.shape) != (M, N):
+    _same(device, _gpu(y, "y"))
+    R, K, ld = _rows(y, "y")
+    if R != M or K != N:
         raise ValueError("y is %s, this call writes (%d, %d)" % (tuple(y.shape), M, N))
     return y, ld, _type_of(y.dtype)
 
 
-def _workspace(need: int, given, device) -> tuple:
+def _workspace(need: int, given, like: torch.Tensor) -> tuple:
     """(tensor to keep until the launch, pointer, bytes)."""
     if need == 0:
         return None, None, 0
     if given is None:
-        given = torch.empty(need, dtype=torch.uint8, device=device)
-    elif given.device != device or not given.is_contiguous():
-        raise ValueError("workspace must be contiguous and on %s" % device)
+        given = like.new_empty(need, dtype=_u8)
+        return given, given.data_ptr(), need
+    if given.device != like.device or not given.is_contiguous():
+        raise ValueError("workspace must be contiguous and on %s" % like.device)
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
@@ -248,23 +258,32 @@ def _workspace(need: int, given, device) -> tuple:
 
 def empty_mx4(R: int, K: int, batch: int | None = None, device="cuda") -> MX4Tensor:
     """A container of the given shape, contents undefined."""
-    if R < 0 or K < BLOCK or K % BLOCK or (batch is not None and batch < 1):
-        raise MX4Error(-2, "empty_mx4(%s, %d, %d)" % (batch, R, K))
-    t = MX4Tensor(None, R, K, batch)
-    t.data = torch.empty(t._code_bytes + t._scale_bytes, dtype=_u8, device=device)
+    t = _container(R, K, batch)
+    t.data = torch.empty(t.nbytes, dtype=_u8, device=device)
     return t
+
+
+def _container(R: int, K: int, batch: int | None) -> MX4Tensor:
+    if R < 0 or K < BLOCK or K % BLOCK or (batch is not None and batch < 1):
+        raise MX4Error(-2, "container of (%s, %d, %d)" % (batch, R, K))
+    return MX4Tensor(None, R, K, batch)
 
 
 def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None) -> MX4Tensor:
     """x [R, K] or [B, R, K] (BF16 or fp32, unit column stride) as MX4."""
-    xt = _type_of(_gpu(x, "x").dtype)
+    dev = _gpu(x, "x")
+    xt = _type_of(x.dtype)
     B, R, K, ld, ldb = _batched(x, "x")
     if out is None:
-        out = empty_mx4(R, K, B, x.device)
-    elif out.shape != tuple(x.shape):
-        raise ValueError("out holds %s, x is %s" % (out.shape, tuple(x.shape)))
-    codes, scales, dev = out.ptrs("out")
-    _same(dev, x.get_device())
+        out = _container(R, K, B)
+        out.data = x.new_empty(out.nbytes, dtype=_u8)
+        codes = out.data.data_ptr()
+        scales = codes + out._code_bytes
+    else:
+        if out.shape != tuple(x.shape):
+            raise ValueError("out holds %s, x is %s" % (out.shape, tuple(x.shape)))
+        codes, scales, out_dev = out.ptrs("out")
+        _same(dev, out_dev)
     _call(dev, lib().mx4_quantize, x.data_ptr(), xt, B or 1, R, K, ld, ldb, codes, scales)
     return out
 
@@ -276,12 +295,15 @@ def mx4_dequantize(q: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16,
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.data.device)
-    elif tuple(out.shape) != q.shape:
-        raise ValueError("out is %s, q holds %s" % (tuple(out.shape), q.shape))
-    yt = _type_of(_gpu(out, "out").dtype)
-    B, R, K, ld, ldb = _batched(out, "out")
-    _same(dev, out.get_device())
+        out = q.data.new_empty(q.shape, dtype=out_dtype)
+        B, R, K = q.batch, q.R, q.K
+        ld, ldb = K, R * K
+    else:
+        _same(dev, _gpu(out, "out"))
+        if tuple(out.shape) != q.shape:
+            raise ValueError("out is %s, q holds %s" % (tuple(out.shape), q.shape))
+        B, R, K, ld, ldb = _batched(out, "out")
+    yt = _type_of(out.dtype)
     _call(dev, lib().mx4_dequantize, codes, scales, B or 1, R, K, out.data_ptr(), yt, ld, ldb)
     return out
 
@@ -294,7 +316,6 @@ def mx4_gemm(x, w: MX4Tensor, out_dtype: torch.dtype = torch.float32,
         raise ValueError("w must hold one matrix")
     wc, wsc, dev = w.ptrs("w")
     N, K = w.R, w.K
-    device = w.data.device
     x_mx4 = isinstance(x, MX4Tensor)
     if x_mx4:
         M = x.R
@@ -303,17 +324,16 @@ def mx4_gemm(x, w: MX4Tensor, out_dtype: torch.dtype = torch.float32,
         xc, xsc, x_dev = x.ptrs("x")
         a0, a1, a2 = xc, xsc, M
     else:
-        if _gpu(x, "x").dtype not in _BF16_TYPES:
+        x_dev = _gpu(x, "x")
+        if x.dtype not in _BF16_TYPES:
             raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
-        ldx = _rows(x, "x")
-        M = x.shape[0]
-        if x.shape[1] != K:
+        M, xk, ldx = _rows(x, "x")
+        if xk != K:
             raise ValueError("x %s does not multiply w %s" % (tuple(x.shape), w.shape))
-        x_dev = x.get_device()
         a0, a1, a2 = x.data_ptr(), M, ldx
-    y, ldy, yt = _output(y, M, N, out_dtype, device)
-    _same(dev, x_dev, y.get_device())
-    keep, wsp, wsb = _workspace(mx4_gemm_workspace_bytes(M, N, K, x_mx4), workspace, device)
+    _same(dev, x_dev)
+    y, ldy, yt = _output(y, M, N, out_dtype, dev, w.data)
+    keep, wsp, wsb = _workspace(mx4_gemm_workspace_bytes(M, N, K, x_mx4), workspace, w.data)
     L = lib()
     _call(dev, L.mx4_gemm_mx4 if x_mx4 else L.mx4_gemm, a0, a1, a2, wc, wsc, N, K, y.data_ptr(),
           ldy, yt, wsp, wsb)
@@ -326,23 +346,23 @@ def mx4_moe(x: torch.Tensor, logits: torch.Tensor, w13: MX4Tensor, w2: MX4Tensor
     """The expert layer of include/mx4.h: x BF16 [T, H], router logits fp32
     [T, E], w13 a container of E matrices [2 I, H] (gate rows, then up rows),
     w2 of E matrices [H, I]; T <= 128."""
-    if _gpu(x, "x").dtype not in _BF16_TYPES:
+    dev, logits_dev = _gpu(x, "x"), _gpu(logits, "logits")
+    if x.dtype not in _BF16_TYPES:
         raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
-    if _gpu(logits, "logits").dtype is not torch.float32:
+    if logits.dtype is not torch.float32:
         raise TypeError("logits must be float32, got %s" % logits.dtype)
-    ldx, ldl = _rows(x, "x"), _rows(logits, "logits")
-    (T, H), E = x.shape, logits.shape[1]
+    T, H, ldx = _rows(x, "x")
+    T_logits, E, ldl = _rows(logits, "logits")
     I = w2.K
-    if logits.shape[0] != T or w13.shape != (E, 2 * I, H) or w2.shape != (E, H, I):
+    if T_logits != T or w13.shape != (E, 2 * I, H) or w2.shape != (E, H, I):
         raise ValueError("x %s, logits %s, w13 %s and w2 %s do not fit together"
                          % (tuple(x.shape), tuple(logits.shape), w13.shape, w2.shape))
     c13, s13, d13 = w13.ptrs("w13")
     c2, s2, d2 = w2.ptrs("w2")
-    dev, device = x.get_device(), x.device
-    y, ldy, yt = _output(y, T, H, out_dtype, device)
-    _same(dev, logits.get_device(), d13, d2, y.get_device())
+    _same(dev, logits_dev, d13, d2)
+    y, ldy, yt = _output(y, T, H, out_dtype, dev, x)
     need = mx4_moe_workspace_bytes(T, H, I, E, int(top_k), y.dtype)
-    keep, wsp, wsb = _workspace(need, workspace, device)
+    keep, wsp, wsb = _workspace(need, workspace, x)
     _call(dev, lib().mx4_moe, x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I,
           E, int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp, wsb)
     return y
