@@ -5,9 +5,9 @@
 // (token, expert) sorted by expert and cut into slots of at most 16.  up: per
 // slot the products with the gate and up rows and h = silu(g) * u.  down: per
 // slot the products of h with the down rows.  join: each token's weighted sum.
-// Above 16 tokens a launch before route chooses the experts.  One token takes two
-// launches: up, which chooses for itself, and down over all its experts, which
-// writes y.
+// Above 16 tokens a launch before route chooses the experts.  One token, and few
+// that would seldom share an expert, take two launches: up, where a token chooses
+// for itself, and down over all its experts, which writes y.
 // The chosen experts' weights are read once (an expert with more than 16 tokens:
 // once a slot, the later reads from cache), which is what bounds the layer;
 // activations and pair outputs are hundredths of them.
@@ -312,7 +312,7 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
         if (part > PARTS - 1) part = PARTS - 1;
         const int row = piece % kPart / (16 * UG);
         if constexpr (UP)
-            xp[i] = a.x + (a.T == 1 ? 0 : slot[16 + row] * a.ldx);
+            xp[i] = a.x + (slot == nullptr ? 0 : slot[16 + row] * a.ldx);
         else
             xp[i] = a.h + (part * pairs + p0 + (row < count ? row : 0)) * (int64_t)a.I;
         xk[i] = piece % (16 * UG) * 8;
@@ -458,15 +458,17 @@ __global__ __launch_bounds__(WN* KW * 64) void expert_kernel(MoeArgs a, int bloc
         expert_body<4, UP, PARTS, R, WN, KW, UG4, UG16>(a, slot, e, count, p0, block, lds);
 }
 
-// up for one token, which chooses for itself: slot s is the token's expert with
-// the s-th largest logit, found by every wave; the slot's first workgroup writes
-// its words for down.
+// up for few tokens, each by itself (blockIdx.y): the token chooses for itself, slot
+// s is its expert with the s-th largest logit, found by every wave; the slot's first
+// workgroup writes its words for down.
 template <int EV, int WN, int KW, int UG>
 __global__ __launch_bounds__(WN* KW * 64) void up_one_kernel(MoeArgs a, int blocks) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int s = blockIdx.x / blocks, block = blockIdx.x % blocks, lane = threadIdx.x & 63;
+    const int t = blockIdx.y, pair = t * a.top_k + s;
+    a.x += t * a.ldx;
     Logits<EV> g;
-    g.load(a.logits, a.E, lane);
+    g.load(a.logits + t * a.ldl, a.E, lane);
     g.rank(a.E, lane);
     float top = 0.f, mine = 0.f, sum = 0.f;
     int e = -1;
@@ -485,21 +487,21 @@ __global__ __launch_bounds__(WN* KW * 64) void up_one_kernel(MoeArgs a, int bloc
     if (block == 0) {
         if (!a.renormalize) sum = g.total(top);
         if (threadIdx.x == 0) {
-            int* o = a.slots + s * kSlotWords;
+            int* o = a.slots + pair * kSlotWords;
             o[0] = e;
             o[1] = e >= 0;
             o[3] = __float_as_int(expf(mine - top) / sum);
         }
     }
     if (e < 0) return;
-    expert_body<4, true, 1, 2, WN, KW, UG, UG>(a, nullptr, e, 1, s, block, lds);
+    expert_body<4, true, 1, 2, WN, KW, UG, UG>(a, nullptr, e, 1, pair, block, lds);
 }
 
-// ---- down for one token -------------------------------------------------------------
-// A workgroup: WN tiles of 16 outputs.  The units (expert, UG groups of its hidden
-// values) are one sequence of which each of the KW groups of waves takes every
-// KW-th; a unit's product is weighted into the sum at once, and no pair's output
-// goes through memory.  All 16 columns of an operand hold the one token.
+// ---- down for few tokens -------------------------------------------------------------
+// A workgroup: WN tiles of 16 outputs of one token (blockIdx.y).  The units (expert,
+// UG groups of its hidden values) are one sequence of which each of the KW groups of
+// waves takes every KW-th; a unit's product is weighted into the sum at once, and no
+// pair's output goes through memory.  All 16 columns of an operand hold the one token.
 template <int PARTS, int WN, int KW, int UG>
 struct One {
     static constexpr int kThreads = WN * KW * 64;
@@ -519,7 +521,7 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kw = w / WN, wn = w % WN;
-    const int q = lane >> 4;
+    const int q = lane >> 4, first = blockIdx.y * a.top_k;      // the token's first pair
     const int G = (int)groups(a.I), Q = (int)quads(a.I), UI = (G + UG - 1) / UG;
     const int ht = a.H / 16;
     const int tile = blockIdx.x * WN + wn < ht ? blockIdx.x * WN + wn : ht - 1;
@@ -529,7 +531,7 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
     int expert = -1;
     float share = 0.f;
     if (lane < a.top_k) {
-        const int* s = a.slots + lane * kSlotWords;
+        const int* s = a.slots + (first + lane) * kSlotWords;
         expert = s[0];
         share = __int_as_float(s[3]);
     }
@@ -561,7 +563,7 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
             const int k = ui * UG * 128 + piece % kPart * 8;
             xin[i] = u < units && k < a.I;
             xb[i] = *reinterpret_cast<const u32x4_t*>(
-                a.h + ((int64_t)part * a.top_k + sl) * a.I + (k < a.I ? k : 0));
+                a.h + ((int64_t)part * a.T * a.top_k + first + sl) * a.I + (k < a.I ? k : 0));
         }
     };
     auto stage = [&](int buf) {
@@ -625,10 +627,11 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
         float v = 0.f;
 #pragma unroll
         for (int k = 0; k < KW; ++k) v += red[k * WN * 16 + tid];
+        const int64_t at = blockIdx.y * a.ldy + n;
         if (a.y_f32)
-            static_cast<float*>(a.y)[n] = v;
+            static_cast<float*>(a.y)[at] = v;
         else
-            static_cast<uint16_t*>(a.y)[n] = bf16_bits(v);
+            static_cast<uint16_t*>(a.y)[at] = bf16_bits(v);
     }
 }
 
@@ -656,9 +659,23 @@ __global__ __launch_bounds__(256) void join_kernel(MoeArgs a) {
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-int64_t max_slots(int64_t T, int64_t E, int64_t top_k) {
+// Each token by itself, weights that several of them chose read again: two launches
+// instead of four, at the cost of the repeated bytes.  Whole layer, us, so / by slots,
+// and the bytes expected: 2 tokens, 2 of 8 experts, H = 5120, I = 1280 17.6 / 24.4 (5 MB);
+// 4 tokens, 8 of 127, H = 2080, I = 736 31.0 / 32.2 (7 MB); 3 tokens, 6 of 64, H = 4096,
+// I = 1408 41.9 / 42.0 (16 MB); 16 tokens, 4 of 64, H = 1024, I = 512 24.6 / 21.6 (25 MB);
+// 4 tokens, 6 of 64, H = 5120, I = 1280 58.2 / 53.8 (35 MB).
+constexpr int kOneByOne = 16;               // tokens
+constexpr int64_t kRepeatedBytes = 16 << 20;
+bool one_by_one(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
+    if (T > kOneByOne) return false;
+    // tokens that choose evenly: two of them share top_k^2 / E experts
+    return T * (T - 1) / 2 * top_k * top_k * (3 * H * I / 32 * 17 / E) <= kRepeatedBytes;
+}
+
+int64_t max_slots(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     const int64_t pairs = T * top_k;
-    return (E < pairs ? E : pairs) + pairs / 16;
+    return one_by_one(T, H, I, E, top_k) ? pairs : (E < pairs ? E : pairs) + pairs / 16;
 }
 
 template <bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
@@ -676,12 +693,38 @@ void launch_expert(const MoeArgs& a, hipStream_t s) {
                            X::lds(16), s, a, blocks);
 }
 
+// Waves beside each other share a slot's rows, waves that split K let a few slots fill
+// the GPU.  Up, H = 5120, I = 1280, 12 tokens, 2 of 8 experts (at most 360 workgroups of
+// 2 x 2 waves): whole layer 38.6 us, with 1 x 4 waves 34.2; 48 tokens, 2 of 16 (880):
+// 53.4 and 55.6.
+void launch_up(const MoeArgs& a, hipStream_t s) {
+    if ((int64_t)a.max_slots * ((a.I + 31) / 32) < 512)
+        launch_expert<true, 1, 2, 1, 4, 2, 1>(a, s);
+    else
+        launch_expert<true, 1, 2, 2, 2, 2, 1>(a, s);
+}
+
+// Down, by workgroups of 4 x 1 waves: 16 tokens, 6 of 64 experts (2800) 104.9 us, with
+// 2 x 2 waves 106.5; 16 tokens, 4 of 32, H = 2048, I = 768 (576) 31.6 and 29.6; 2 of 8
+// experts, H = 4096, I = 14336: 128 tokens (768) 304, with 2 x 4 waves 319, 80 tokens
+// (576) 259 and 249, 12 tokens (288) 193 and 139, with 2 x 2 waves 154 (three parts of h
+// for 16 rows leave no LDS for 2 x 4).
+template <int PARTS>
+void launch_down(const MoeArgs& a, hipStream_t s) {
+    if ((int64_t)a.max_slots * ((a.H + 127) / 128) >= 640)
+        launch_expert<false, PARTS, 2, 4, 1, 1, 1>(a, s);
+    else if (PARTS == 2 && a.I >= 4096)
+        launch_expert<false, 2, 2, 2, 4, 1, 1>(a, s);
+    else
+        launch_expert<false, PARTS, 2, 2, 2, 1, 1>(a, s);
+}
+
 template <int EV>
 void launch_up_one(const MoeArgs& a, hipStream_t s) {
     constexpr int WN = 1, KW = 4, UG = 4;   // (1, 8, 2): 12.9 against 12.1 us at H = 5120, I = 1280
     using X = Expert<true, 1, 2, WN, KW, UG, UG>;
     const int blocks = (a.I / 16 + WN - 1) / WN;
-    hipLaunchKernelGGL((up_one_kernel<EV, WN, KW, UG>), dim3((unsigned)(a.top_k * blocks)),
+    hipLaunchKernelGGL((up_one_kernel<EV, WN, KW, UG>), dim3((unsigned)(a.top_k * blocks), (unsigned)a.T),
                        dim3(X::kThreads), X::lds(4), s, a, blocks);
 }
 
@@ -690,8 +733,8 @@ void launch_down_one(const MoeArgs& a, hipStream_t s) {
     using X = One<PARTS, WN, KW, UG>;
     static_assert(X::lds() <= 65536, "more LDS than a launch gets without asking");
     hipLaunchKernelGGL((down_one_kernel<PARTS, WN, KW, UG>),
-                       dim3((unsigned)((a.H / 16 + WN - 1) / WN)), dim3(X::kThreads), X::lds(), s,
-                       a);
+                       dim3((unsigned)((a.H / 16 + WN - 1) / WN), (unsigned)a.T),
+                       dim3(X::kThreads), X::lds(), s, a);
 }
 
 template <int EV>
@@ -705,13 +748,13 @@ void launch_route(const MoeArgs& a, hipStream_t s) {
 
 size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bool y_f32) {
     const int64_t pairs = T * top_k;
-    return up256((size_t)max_slots(T, E, top_k) * kSlotWords * 4) + 2 * up256((size_t)pairs * 4) +
+    return up256((size_t)max_slots(T, H, I, E, top_k) * kSlotWords * 4) + 2 * up256((size_t)pairs * 4) +
            up256((size_t)pairs * H * 4) + (size_t)(y_f32 ? 3 : 2) * pairs * I * 2;
 }
 
 hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     const int64_t pairs = (int64_t)a.T * a.top_k;
-    a.max_slots = (int)max_slots(a.T, a.E, a.top_k);
+    a.max_slots = (int)max_slots(a.T, a.H, a.I, a.E, a.top_k);
     uint8_t* p = static_cast<uint8_t*>(ws);
     a.slots = reinterpret_cast<int*>(p);
     p += up256((size_t)a.max_slots * kSlotWords * 4);
@@ -724,7 +767,7 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     a.h = reinterpret_cast<uint16_t*>(p);
 
     const int ev = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : 16;
-    if (a.T == 1) {
+    if (one_by_one(a.T, a.H, a.I, a.E, a.top_k)) {
         switch (ev) {
             case 1: launch_up_one<1>(a, s); break;
             case 2: launch_up_one<2>(a, s); break;
@@ -743,11 +786,11 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
         case 4: launch_route<4>(a, s); break;
         default: launch_route<16>(a, s);
     }
-    launch_expert<true, 1, 2, 2, 2, 2, 1>(a, s);
+    launch_up(a, s);
     if (a.y_f32)
-        launch_expert<false, 3, 2, 4, 1, 1, 1>(a, s);
+        launch_down<3>(a, s);
     else
-        launch_expert<false, 2, 2, 4, 1, 1, 1>(a, s);
+        launch_down<2>(a, s);
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256),
                        0, s, a);
     return hipGetLastError();

@@ -216,7 +216,12 @@ def _moe_case(T, H, I, E, seed):
 
 MOE_SHAPES = [(1, 64, 32, 1, 1), (1, 256, 96, 8, 2), (2, 160, 64, 5, 5), (7, 416, 160, 16, 3),
               (16, 512, 128, 64, 6), (33, 96, 544, 12, 4), (61, 288, 96, 127, 8),
-              (128, 128, 64, 4, 2), (128, 96, 32, 300, 32), (3, 544, 1056, 70, 7)]
+              (128, 128, 64, 4, 2), (128, 96, 32, 300, 32), (3, 544, 1056, 70, 7),
+              # few tokens that share most experts; few experts with a long I; many
+              # workgroups of the down product; one token on every width of the choice
+              (4, 512, 448, 8, 8), (9, 512, 256, 24, 12), (16, 288, 608, 70, 32),
+              (6, 96, 4128, 4, 4), (40, 96, 4128, 4, 2), (40, 1056, 64, 64, 4),
+              (1, 160, 96, 100, 3), (2, 96, 64, 250, 32), (1, 96, 64, 1024, 32)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -241,11 +246,11 @@ def test_moe(T, H, I, E, k, renormalize, out):
     assert torch.equal(z, y)
 
 
-@pytest.mark.parametrize("E", [6, 200])
-def test_moe_routing_edges(E):
+@pytest.mark.parametrize("E,H,I", [(6, 128, 64), (200, 128, 64), (6, 512, 1024)])
+def test_moe_routing_edges(E, H, I):
     """Ties (also of -0 and +0), masked experts, a token with fewer experts than
     top_k, one with none, and NaN and infinite logits."""
-    T, H, I, k = 9, 128, 64, 4
+    T, k = 9, 4
     xv, logits, w13, w2, q13, q2 = _moe_case(T, H, I, E, 40)
     logits[0] = 0.0
     logits[1] = np.where(np.arange(E) % 2, 0.0, -0.0)
@@ -310,11 +315,14 @@ def test_graphs_and_streams():
     xs = [_dev(xv), _dev(_values((T, H), 72))]
     big = [_dev(_values((40, H), 73)), _dev(_values((40, H), 74))]
     lg = torch.from_numpy(logits).cuda()
+    lg40 = torch.from_numpy(np.random.default_rng(75).standard_normal((40, E))
+                            .astype(np.float32)).cuda()
 
     def step(x, b):
         q = mx4.mx4_quantize(x)
         return (mx4.mx4_dequantize(q), mx4.mx4_gemm(x, wq), mx4.mx4_gemm(q, wq),
-                mx4.mx4_gemm(b, wq), mx4.mx4_moe(x, lg, q13, q2, k))
+                mx4.mx4_gemm(b, wq), mx4.mx4_moe(x, lg, q13, q2, k),
+                mx4.mx4_moe(b, lg40, q13, q2, k))
 
     want = [[t.clone() for t in step(x, b)] for x, b in zip(xs, big)]
     torch.cuda.synchronize()
