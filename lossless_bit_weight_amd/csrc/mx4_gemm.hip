@@ -736,6 +736,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs a) {
     const int64_t MN = (int64_t)a.M * a.N;
     if (i >= MN) return;
     float s = 0.f;
+#pragma unroll 8
     for (int v = 0; v < a.S; ++v) s += a.part[v * MN + i];
     store_y(a, i / a.N, i % a.N, s);
 }
@@ -835,6 +836,7 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
             p.kernel = kSmall;
         } else if (M <= 4) {
             p.kernel = many ? kMid4 : kMid4Long;
+            if (!many) S = slices(256, nt);
         } else {
             p.kernel = kMid16;
             if (many)
@@ -848,11 +850,13 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         else
             p.kernel = M <= 32 ? kMid32 : kMid32R2;
         p.wn = p.kernel == kMid32R2 ? spread((nt + 1) / 2, (M + 31) / 32) : spread(nt, 1);
-    } else if (xm && !many && M <= 256) {
+    } else if (xm && !many &&
+               (M <= (lengthy ? 192 : 256) || (!lengthy && blocks(32, 64) <= 640))) {
         p.kernel = lengthy ? kMid64 : M <= 32 ? kMid16x2 : M <= 128 ? kMid32x2 : kMid32;
         if (p.kernel == kMid32) p.wn = spread(nt, (M + 31) / 32);
         if (lengthy) S = slices(400, blocks(64, 64));
-    } else if (!xm && !many && M <= (lengthy ? 64 : 128)) {
+    } else if (!xm && !many &&
+               (M <= (lengthy ? 64 : 128) || (!lengthy && blocks(16, 128) <= 448))) {
         p.kernel = !lengthy && M <= 32 ? kMid16x2 : kMid16;
         p.wn = 8;
         if (lengthy) S = slices(480, blocks(16, 128));
@@ -860,15 +864,17 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         p.kernel = kTile128;
     } else if (xm) {
         p.kernel = blocks(128, 128) >= 440 ? kTileMid : kTileSmall;
-        if (p.kernel == kTileSmall) S = slices(544, blocks(64, 128));
+        if (lengthy && p.kernel == kTileSmall) S = slices(544, blocks(64, 128));
     } else if (blocks(64, 256) >= 440 || (blocks(64, 256) >= 200 &&
                                           (lengthy || blocks(64, 256) <= 256))) {
         p.kernel = kTileMid;
         if (lengthy && blocks(64, 256) < 440) S = slices(960, blocks(64, 256));
     } else {
         p.kernel = kTileSmall;
-        S = slices(480, blocks(32, 256));
-        if (!lengthy && blocks(32, 256) >= 200) S = 1;
+        if (lengthy)
+            S = slices(480, blocks(32, 256));
+        else if (G >= 32 && blocks(32, 256) < 200)
+            S = blocks(32, 256) < 100 ? 4 : 3;
     }
     if (S > Q) S = Q;
     if (S < 1) S = 1;
