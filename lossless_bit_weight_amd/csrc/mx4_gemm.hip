@@ -808,11 +808,15 @@ int spread(int64_t units, int64_t mb) {
 //     7.8 through LDS, M = 16 9.8 against 11.1); shared through LDS for many tiles
 //     (gate+up M = 1 18.5 against 22.1, M = 16 23.6 against 29.2) or a long K (down
 //     M = 1 14.3 against 15.6, M = 16, K in six slices, 17.5 against 23.5).  MX4 x
-//     is a quarter of the bytes: shared or not within 3%.
-//   17 rows to 128 (MX4 x: 256) and few tiles: 16 (32, 64) rows a workgroup, whose
-//     weights the row blocks beside it find in L2 (QKV M = 64 13.9, M = 128 19.7; a
-//     64 x 128 tile in four slices 21.2 and 24.9.  MX4 x: 16 rows at M = 32 7.5, 32
-//     rows 9.1; 32 rows at M = 128 11.5, 64 rows 14.0).
+//     is a quarter of the bytes: shared or not within 3%.  A long K for so few tiles
+//     that they leave CUs idle is cut (M = 1, K = 17408, N = 1024 8.9, uncut 11.5; MX4 x
+//     8.0 and 11.4).
+//   above and few tiles: 16 (MX4 x: 16, 32) rows a workgroup, whose weights the row
+//     blocks beside it find in L2, up to the grids that those fill (QKV M = 64 16.9,
+//     M = 128 21.5; 64 x 128 tiles in four slices 21.2 and 24.9.  N = K = 1024, M = 512
+//     6.0, tiles 9.2.  MX4 x: 16 rows at M = 48 10.4, 32 rows 11.1, at M = 128 17.6 and
+//     14.4; N = 896 on K = 5120, M = 128, 6.3 and 8.7); a long K in slices (down M = 33 24.5,
+//     MX4 x, M = 17, six slices, 16.3; 64 rows, five slices, 20.7).
 //   17 to 64 and many tiles: 32 rows (MX4 x: up to 64), waves as spread() says
 //     (gate+up M = 64 42.5 with two tiles a wave, 50.4 with 64 x 128 tiles).
 //   above: 128 x 256 if that gives 440 workgroups (QKV M = 2048 115, 64 x 256 125.5);
@@ -820,7 +824,10 @@ int spread(int64_t units, int64_t mb) {
 //     nearly one a CU (QKV M = 512 39.2, 128 x 256 51.7), then 32 x 256 (QKV M = 256
 //     29.2, 64 x 256 in two slices 32.4; gate+up M = 128 59.4, 64 x 256 on 272
 //     workgroups 64.1); MX4 x 128 x 128, then 64 x 128 (QKV M = 512 21.8, 128 x 256
-//     30.2); K in slices if that is too few.
+//     30.2).  Slices cost about 4 us to write, wait for and join: for a long K (down
+//     M = 256, MX4 x, four slices of 64 x 128 37.2, one 60), and BF16 x on K = 4096 and more
+//     where one slice leaves CUs idle (O M = 192 22.9 with three, 28.1 with one; K = 2560
+//     18.9 and 16.7).
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
     const int G = (int)groups(K), Q = (int)quads(K);
     const int64_t nt = tiles(N);
@@ -832,11 +839,14 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
     int64_t S = 1;
     const auto slices = [](int64_t want, int64_t have) { return (want + have / 2) / have; };
     if (M <= 16) {
-        if (xm || (!many && !lengthy)) {
+        if (xm && lengthy && nt <= 160) {
+            p.kernel = kMid16x2;
+            S = slices(512, blocks(16, 32));
+        } else if (xm || (!many && !lengthy)) {
             p.kernel = kSmall;
         } else if (M <= 4) {
             p.kernel = many ? kMid4 : kMid4Long;
-            if (!many) S = slices(256, nt);
+            if (!many) S = slices(400, nt);
         } else {
             p.kernel = kMid16;
             if (many)
@@ -852,19 +862,24 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         p.wn = p.kernel == kMid32R2 ? spread((nt + 1) / 2, (M + 31) / 32) : spread(nt, 1);
     } else if (xm && !many &&
                (M <= (lengthy ? 192 : 256) || (!lengthy && blocks(32, 64) <= 640))) {
-        p.kernel = lengthy ? kMid64 : M <= 32 ? kMid16x2 : M <= 128 ? kMid32x2 : kMid32;
-        if (p.kernel == kMid32) p.wn = spread(nt, (M + 31) / 32);
-        if (lengthy) S = slices(400, blocks(64, 64));
+        if (lengthy) {
+            p.kernel = M <= 64 ? kMid32 : kMid64;
+            S = M <= 64 ? slices(480, blocks(32, 64)) : slices(640, blocks(64, 64));
+        } else {
+            p.kernel = blocks(16, 32) <= 1024  ? kMid16x2
+                       : blocks(32, 64) <= 512 ? kMid32x2
+                                               : kMid32;
+        }
     } else if (!xm && !many &&
                (M <= (lengthy ? 64 : 128) || (!lengthy && blocks(16, 128) <= 448))) {
-        p.kernel = !lengthy && M <= 32 ? kMid16x2 : kMid16;
+        p.kernel = !lengthy && (M <= 32 || blocks(16, 64) <= 256) ? kMid16x2 : kMid16;
         p.wn = 8;
         if (lengthy) S = slices(480, blocks(16, 128));
     } else if (blocks(128, 256) >= 440) {
         p.kernel = kTile128;
     } else if (xm) {
         p.kernel = blocks(128, 128) >= 440 ? kTileMid : kTileSmall;
-        if (lengthy && p.kernel == kTileSmall) S = slices(544, blocks(64, 128));
+        if (lengthy && p.kernel == kTileSmall) S = slices(640, blocks(64, 128));
     } else if (blocks(64, 256) >= 440 || (blocks(64, 256) >= 200 &&
                                           (lengthy || blocks(64, 256) <= 256))) {
         p.kernel = kTileMid;
@@ -874,7 +889,7 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         if (lengthy)
             S = slices(480, blocks(32, 256));
         else if (G >= 32 && blocks(32, 256) < 200)
-            S = blocks(32, 256) < 100 ? 4 : 3;
+            S = 3;
     }
     if (S > Q) S = Q;
     if (S < 1) S = 1;

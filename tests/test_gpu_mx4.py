@@ -161,12 +161,36 @@ def test_gemm(M, N, K, x_mx4, out):
     assert torch.equal(z, y)
 
 
-@pytest.mark.parametrize("M", [1, 16, 30, 64, 200])
-def test_gemm_special_values(M):
+# every kernel, tile, count of waves and cut of K that a product is given
+GEMM_KERNELS = [(M, N, 416) for M in (3, 11, 27, 50)
+                for N in (16390, 21390, 29390, 33390, 41390)] + [
+    (2, 2600, 8224), (4, 40, 8736), (13, 2700, 8224), (16, 300, 8224), (40, 100, 17376),
+    (70, 130, 8256), (150, 200, 8288), (200, 3000, 160), (250, 4200, 96), (700, 2000, 96),
+    (96, 16400, 544), (129, 56330, 160), (450, 7170, 96), (300, 3000, 4128), (129, 28200, 160),
+    (300, 1000, 8224), (1030, 3100, 8224)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMM_KERNELS)
+def test_gemm_kernels(M, N, K):
+    xv = _values((M, K), M + K)
+    wq = mx4.mx4_quantize(torch.randn(N, K, device="cuda",
+                                      generator=torch.Generator("cuda").manual_seed(N)))
+    wv = _host(mx4.mx4_dequantize(wq, torch.float32))
+    x = _dev(xv)
+    for a, av in ((x, xv), (mx4.mx4_quantize(x), ref.rounded(xv))):
+        want, tol = ref.matmul(av, wv)
+        ref.assert_close(_host(mx4.mx4_gemm(a, wq)), want, tol, "f32", "gemm")
+        out = torch.empty((M, N), dtype=torch.bfloat16, device="cuda")
+        ref.assert_close(_host(mx4.mx4_gemm(a, wq, y=out)), want, tol, "bf16", "gemm")
+
+
+@pytest.mark.parametrize("M,N", [(1, 70), (16, 70), (30, 70), (64, 70), (200, 70), (3, 16390),
+                                 (11, 16390), (27, 16390), (50, 16390), (96, 16400), (200, 3000),
+                                 (250, 4200), (450, 7170), (129, 28200), (129, 56330)])
+def test_gemm_special_values(M, N):
     """NaN scales, infinities and NaN of x reach their own rows and columns only;
     rows behind x and columns behind K are never read into the sums."""
-    N, K = 70, 416
-    rng = np.random.default_rng(3)
+    K = 416
     xv, wv = _values((M, K), 1), _values((N, K), 2)
     wv[3, 40] = np.inf                             # one block of row 3 is NaN
     xv[0, 5] = np.inf
