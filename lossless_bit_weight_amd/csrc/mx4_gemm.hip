@@ -165,7 +165,7 @@ hipError_t launch_small(GemmArgs a, hipStream_t s) {
 }
 
 // ---- a few rows of x, shared through LDS ------------------------------------------
-// A workgroup: ROWS rows of x (4, or 16 and more) by 16 R WN weight rows; KW
+// A workgroup: ROWS rows of x (4, or 16 and more) by 16 WN weight rows; KW
 // groups of WN waves take every KW-th unit of UG groups of K.  A unit's weights
 // come to registers one unit ahead of their products; its x goes through LDS,
 // double-buffered, where the WN waves share it: with every wave reading x for
@@ -180,16 +180,17 @@ struct Mid {
     static constexpr int kAllPieces = XM ? MT * 64 * UG : ROWS * 16 * UG;   // of x a unit
     static constexpr int kPieces = (kAllPieces + WN * 64 - 1) / (WN * 64);  // a thread
     static constexpr int kStage = kAllPieces * 16;
-    static constexpr int lds(int R) {
-        const int x = 2 * KW * kStage, red = KW * WN * MT * R * 1024;
+    static constexpr int lds() {
+        const int x = 2 * KW * kStage, red = KW * WN * MT * 1024;
         return x > red ? x : red;
     }
 };
 
-template <int ROWS, int R, int WN, int KW, int UG, bool XM>
+template <int ROWS, int WN, int KW, int UG, bool XM>
 __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, int nb) {
     using T = Mid<ROWS, WN, KW, UG, XM>;
     constexpr int MT = T::MT, P = T::kPieces;
+    static_assert(!XM || UG == 4, "a scale's dword serves four groups");
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -212,15 +213,10 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
 
     const int64_t last_tile = tiles(a.N) - 1;
-    const uint8_t* wp[R];
-    const uint8_t* sp[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        int64_t t = (int64_t)bn * (WN * R) + wn * R + r;
-        if (t > last_tile) t = last_tile;
-        wp[r] = a.w.codes + t * a.G * kCodeBlock;
-        sp[r] = a.w.scales + t * a.Q * kScaleBlock;
-    }
+    int64_t tile = (int64_t)bn * WN + wn;
+    if (tile > last_tile) tile = last_tile;
+    const uint8_t* wp = a.w.codes + tile * a.G * kCodeBlock;
+    const uint8_t* sp = a.w.scales + tile * a.Q * kScaleBlock;
     uint8_t* mine = lds + kw * 2 * T::kStage;
     auto at_piece = [&](int i) {
         int p = (i * WN + wn) * 64 + lane;
@@ -228,19 +224,16 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
             p = T::kAllPieces - 64 + lane;
         return p;
     };
-    u32x4_t wb[2][UG][R], xb[P];
-    uint32_t ws[2][R], xs[2][XM ? MT : 1];
+    u32x4_t wb[2][UG], xb[P];
+    uint32_t ws[2], xs[2][XM ? MT : 1];
     bool xin[P];
     // (no branch: a place past the last unit, group, row or K is a valid one whose x
     // is replaced by zeros, a piece past the last is the last once more)
     auto load_x = [&](int slot, int it) {
         const int u = u0 + it * KW + kw;
         const int uc = u < u1 ? u : u1 - 1;
-        const int64_t so = (int64_t)(uc * UG / 4) * kScaleBlock;
-        const int shift = UG == 4 ? 0 : 8 * UG * (uc % (4 / UG));
-        (void)so;
-        (void)shift;
         if constexpr (XM) {
+            const int64_t so = (int64_t)uc * kScaleBlock;
             const int64_t last = tiles(a.M) - 1;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -256,7 +249,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
             for (int t = 0; t < MT; ++t) {
                 const int64_t tt = m0 / 16 + t < last ? m0 / 16 + t : last;
                 const uint8_t* p = scalar(a.xm.scales + tt * a.Q * kScaleBlock + so);
-                xs[slot][t] = *reinterpret_cast<const uint32_t*>(p + lane4) >> shift;
+                xs[slot][t] = *reinterpret_cast<const uint32_t*>(p + lane4);
             }
         } else {
 #pragma unroll
@@ -276,16 +269,11 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         const int uc = u < u1 ? u : u1 - 1;
         const int64_t so = (int64_t)(uc * UG / 4) * kScaleBlock;
         const int shift = UG == 4 ? 0 : 8 * UG * (uc % (4 / UG));
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            ws[slot][r] = *reinterpret_cast<const uint32_t*>(scalar(sp[r] + so) + lane4) >> shift;
+        ws[slot] = *reinterpret_cast<const uint32_t*>(scalar(sp + so) + lane4) >> shift;
 #pragma unroll
         for (int j = 0; j < UG; ++j) {
             const int g = uc * UG + j < a.G ? uc * UG + j : a.G - 1;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                wb[slot][j][r] =
-                    load16<ROWS == 4>(scalar(wp[r] + (int64_t)g * kCodeBlock) + lane16);
+            wb[slot][j] = load16<ROWS == 4>(scalar(wp + (int64_t)g * kCodeBlock) + lane16);
         }
     };
     // x is waited for first; four rows of it arrive before the weights in any order,
@@ -310,11 +298,9 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
             *reinterpret_cast<u32x4_t*>(mine + buf * T::kStage + at * 16) = v;
         }
     };
-    f32x4_t acc[MT][R];
+    f32x4_t acc[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[t][r] = f32x4_t{0, 0, 0, 0};
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0, 0, 0, 0};
     const int cr = ROWS < 16 ? c & (ROWS - 1) : c;
     auto product = [&](auto sc) {
         constexpr int slot = decltype(sc)::value;
@@ -326,24 +312,18 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
                 for (int t = 0; t < MT; ++t) {
                     const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(
                         xl + (t * UG + J) * kCodeBlock + lane16);
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        acc[t][r] = mfma_mx4<J>(operand4(wb[slot][J][r]), operand4(xv), acc[t][r],
-                                                ws[slot][r], xs[slot][t]);
+                    acc[t] = mfma_mx4<J>(operand4(wb[slot][J]), operand4(xv), acc[t], ws[slot],
+                                         xs[slot][t]);
                 }
             };
             group(std::integral_constant<int, 0>{});
             group(std::integral_constant<int, 1>{});
-            if constexpr (UG == 4) {
-                group(std::integral_constant<int, 2>{});
-                group(std::integral_constant<int, 3>{});
-            }
+            group(std::integral_constant<int, 2>{});
+            group(std::integral_constant<int, 3>{});
         } else {
 #pragma unroll
             for (int j = 0; j < UG; ++j) {
-                float s[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) s[r] = scale_f32((ws[slot][r] >> (8 * j)) & 255u);
+                const float s = scale_f32((ws[slot] >> (8 * j)) & 255u);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     bf16x8_t xv[MT];
@@ -353,12 +333,9 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
                         xv[t] = *reinterpret_cast<const bf16x8_t*>(
                             xl + (row * 16 * UG + 16 * j + x_place(q, b, row)) * 16);
                     }
+                    const bf16x8_t wv = expand8(wb[slot][j][b], s);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const bf16x8_t wv = expand8(wb[slot][j][r][b], s[r]);
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) acc[t][r] = mfma_bf16(wv, xv[t], acc[t][r]);
-                    }
+                    for (int t = 0; t < MT; ++t) acc[t] = mfma_bf16(wv, xv[t], acc[t]);
                 }
             }
         }
@@ -383,23 +360,21 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
     __syncthreads();
 
     // the k groups' sums in their order
-    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][MT][R][256]
+    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][MT][256]
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            *reinterpret_cast<f32x4_t*>(red + ((w * MT + t) * R + r) * 256 + lane * 4) = acc[t][r];
+        *reinterpret_cast<f32x4_t*>(red + (w * MT + t) * 256 + lane * 4) = acc[t];
     __syncthreads();
-    constexpr int kCols = 16 * R * WN;
+    constexpr int kCols = 16 * WN;
     for (int i = tid; i < (ROWS < 16 ? ROWS : MT * 16) * kCols; i += T::kThreads) {
         const int m = i / kCols, col = i % kCols;
         const int64_t nn = (int64_t)bn * kCols + col;
         if (m0 + m >= a.M || nn >= a.N) continue;
-        const int v = col / (16 * R), r = col / 16 % R, wr = col & 15, t = m >> 4;
-        const int at = ((v * MT + t) * R + r) * 256 + ((wr >> 2) * 16 + (m & 15)) * 4 + (wr & 3);
+        const int wr = col & 15, in = ((wr >> 2) * 16 + (m & 15)) * 4 + (wr & 3);
+        const int at = ((col >> 4) * MT + (m >> 4)) * 256 + in;
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < KW; ++k) s += red[k * WN * MT * R * 256 + at];
+        for (int k = 0; k < KW; ++k) s += red[k * WN * MT * 256 + at];
         if (a.S > 1)
             a.part[((int64_t)blockIdx.y * a.M + m0 + m) * a.N + nn] = s;
         else
@@ -760,22 +735,22 @@ hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
     return launch_join(a, s);
 }
 
-template <int ROWS, int R, int WN, int KW, int UG, bool XM>
+template <int ROWS, int WN, int KW, int UG, bool XM>
 hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
     using T = Mid<ROWS, WN, KW, UG, XM>;
-    static_assert(T::lds(R) <= 65536, "more LDS than a launch gets without asking");
+    static_assert(T::lds() <= 65536, "more LDS than a launch gets without asking");
     constexpr int bm = ROWS < 16 ? 16 : ROWS;
     const int mb = (a.M + bm - 1) / bm;
-    const int nb = (int)((tiles(a.N) + R * WN - 1) / (R * WN));
-    hipLaunchKernelGGL((mid_kernel<ROWS, R, WN, KW, UG, XM>),
+    const int nb = (int)((tiles(a.N) + WN - 1) / WN);
+    hipLaunchKernelGGL((mid_kernel<ROWS, WN, KW, UG, XM>),
                        dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S), dim3(T::kThreads),
-                       T::lds(R), s, a, mb, nb);
+                       T::lds(), s, a, mb, nb);
     return launch_join(a, s);
 }
 
 // Kernel and split of a product.
 enum Kernel {
-    kSmall, kMid4, kMid4Long, kMid16, kMid16x2, kMid32, kMid32R2, kMid32x2, kMid64,
+    kSmall, kMid4, kMid4Long, kMid16, kMid16x2, kMid32, kMid32x2, kMid64,
     kTileSmall, kTileMid, kTile128
 };
 struct Plan {
@@ -784,16 +759,16 @@ struct Plan {
     int S, gs;              // K slices, groups a slice (a multiple of 4)
 };
 
-// Waves beside each other that spread `units` of work along N (times mb blocks of
-// rows) best over 256 CUs: the CU with the most of them decides.  Gate+up, 2176
-// tiles, M = 32, us (tiles of that CU): 9 waves 26.4 (9), 12 30.1 (12), 5 33.2
-// (10), 7 35.4 (14), 8 36.8 (16).  Of equals the most waves, which share x.
-int spread(int64_t units, int64_t mb) {
+// Waves beside each other that spread nt tiles best over 256 CUs: the CU with the
+// most of them decides.  Gate+up, 2176 tiles, M = 32, us (tiles of that CU): 9 waves
+// 26.4 (9), 12 30.1 (12), 5 33.2 (10), 7 35.4 (14), 8 36.8 (16).  Of equals the most
+// waves, which share x.
+int spread(int64_t nt) {
     static const int kWaves[] = {12, 9, 7, 5, 4};
     int best = 4;
     int64_t least = -1;
     for (const int w : kWaves) {
-        const int64_t load = ((units + w - 1) / w * mb + 255) / 256 * w;
+        const int64_t load = ((nt + w - 1) / w + 255) / 256 * w;
         if (least < 0 || load < least) {
             least = load;
             best = w;
@@ -817,8 +792,9 @@ int spread(int64_t units, int64_t mb) {
 //     6.0, tiles 9.2.  MX4 x: 16 rows at M = 48 10.4, 32 rows 11.1, at M = 128 17.6 and
 //     14.4; N = 896 on K = 5120, M = 128, 6.3 and 8.7); a long K in slices (down M = 33 24.5,
 //     MX4 x, M = 17, six slices, 16.3; 64 rows, five slices, 20.7).
-//   17 to 64 and many tiles: 32 rows (MX4 x: up to 64), waves as spread() says
-//     (gate+up M = 64 42.5 with two tiles a wave, 50.4 with 64 x 128 tiles).
+//   17 to 32 and many tiles: 32 rows, waves as spread() says (MX4 x: four), unless BF16
+//     tiles of 32 x 256 nearly fill the GPU (gate+up M = 32, 136 of them, 37.2, by waves
+//     29.8; N = 65536 on K = 2048, 256 of them, 20.0 and 26.8).
 //   above: 128 x 256 if that gives 440 workgroups (QKV M = 2048 115, 64 x 256 125.5);
 //     else, BF16 x, 64 x 256 if that gives 440 (QKV M = 1024 64.9, 128 x 256 75.5) or
 //     nearly one a CU (QKV M = 512 39.2, 128 x 256 51.7), then 32 x 256 (QKV M = 256
@@ -850,16 +826,13 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         } else {
             p.kernel = kMid16;
             if (many)
-                p.wn = spread(nt, 1);
+                p.wn = spread(nt);
             else
                 S = slices(480, blocks(16, 64));
         }
-    } else if (many && M <= 64) {
-        if (xm)
-            p.kernel = M <= 32 ? kMid32 : kMid64;
-        else
-            p.kernel = M <= 32 ? kMid32 : kMid32R2;
-        p.wn = p.kernel == kMid32R2 ? spread((nt + 1) / 2, (M + 31) / 32) : spread(nt, 1);
+    } else if (many && M <= 32 && (xm || blocks(32, 256) < 200)) {
+        p.kernel = kMid32;
+        p.wn = spread(nt);
     } else if (xm && !many &&
                (M <= (lengthy ? 192 : 256) || (!lengthy && blocks(32, 64) <= 640))) {
         if (lengthy) {
@@ -875,13 +848,13 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         p.kernel = !lengthy && (M <= 32 || blocks(16, 64) <= 256) ? kMid16x2 : kMid16;
         p.wn = 8;
         if (lengthy) S = slices(480, blocks(16, 128));
-    } else if (blocks(128, 256) >= 440) {
+    } else if (M > 64 && blocks(128, 256) >= 440) {
         p.kernel = kTile128;
     } else if (xm) {
-        p.kernel = blocks(128, 128) >= 440 ? kTileMid : kTileSmall;
+        p.kernel = M > 64 && blocks(128, 128) >= 440 ? kTileMid : kTileSmall;
         if (lengthy && p.kernel == kTileSmall) S = slices(640, blocks(64, 128));
-    } else if (blocks(64, 256) >= 440 || (blocks(64, 256) >= 200 &&
-                                          (lengthy || blocks(64, 256) <= 256))) {
+    } else if (M > 32 && (blocks(64, 256) >= 440 ||
+                          (blocks(64, 256) >= 200 && (lengthy || blocks(64, 256) <= 256)))) {
         p.kernel = kTileMid;
         if (lengthy && blocks(64, 256) < 440) S = slices(960, blocks(64, 256));
     } else {
@@ -899,14 +872,14 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
     return p;
 }
 
-template <int ROWS, int R, bool XM>
+template <int ROWS>
 hipError_t launch_mid_waves(int wn, GemmArgs& a, hipStream_t s) {
     switch (wn) {
-        case 5: return launch_mid<ROWS, R, 5, 1, 4, XM>(a, s);
-        case 7: return launch_mid<ROWS, R, 7, 1, 4, XM>(a, s);
-        case 9: return launch_mid<ROWS, R, 9, 1, 4, XM>(a, s);
-        case 12: return launch_mid<ROWS, R, 12, 1, 4, XM>(a, s);
-        default: return launch_mid<ROWS, R, 4, 1, 4, XM>(a, s);
+        case 5: return launch_mid<ROWS, 5, 1, 4, false>(a, s);
+        case 7: return launch_mid<ROWS, 7, 1, 4, false>(a, s);
+        case 9: return launch_mid<ROWS, 9, 1, 4, false>(a, s);
+        case 12: return launch_mid<ROWS, 12, 1, 4, false>(a, s);
+        default: return launch_mid<ROWS, 4, 1, 4, false>(a, s);
     }
 }
 
@@ -929,24 +902,23 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     if (!xm && k >= kTileSmall && a.ldx >= (1 << 23)) k = kSmall;
     if (k == kSmall) a.S = 1;
     if (xm) switch (k) {
-        case kMid16x2: return launch_mid<16, 1, 2, 2, 4, true>(a, s);
-        case kMid32: return launch_mid_waves<32, 1, true>(p.wn, a, s);
-        case kMid32x2: return launch_mid<32, 1, 4, 2, 4, true>(a, s);
-        case kMid64: return launch_mid_waves<64, 1, true>(p.wn, a, s);
+        case kMid16x2: return launch_mid<16, 2, 2, 4, true>(a, s);
+        case kMid32: return launch_mid<32, 4, 1, 4, true>(a, s);
+        case kMid32x2: return launch_mid<32, 4, 2, 4, true>(a, s);
+        case kMid64: return launch_mid<64, 4, 1, 4, true>(a, s);
         case kTileSmall: return launch_tile<4, 2, 1, 4, true, true>(a, s);
         case kTileMid: return launch_tile<8, 2, 1, 4, true, true>(a, s);
         case kTile128: return launch_tile<8, 4, 1, 4, true, true>(a, s);
         default: return launch_small<2, 8, 2, true>(a, s);
     }
     switch (k) {
-        case kMid4: return launch_mid<4, 1, 2, 2, 2, false>(a, s);
-        case kMid4Long: return launch_mid<4, 1, 1, 4, 4, false>(a, s);
+        case kMid4: return launch_mid<4, 2, 2, 2, false>(a, s);
+        case kMid4Long: return launch_mid<4, 1, 4, 4, false>(a, s);
         case kMid16:
-            return p.wn == 8 ? launch_mid<16, 1, 8, 1, 4, false>(a, s)
-                             : launch_mid_waves<16, 1, false>(p.wn, a, s);
-        case kMid16x2: return launch_mid<16, 1, 4, 2, 4, false>(a, s);
-        case kMid32: return launch_mid_waves<32, 1, false>(p.wn, a, s);
-        case kMid32R2: return launch_mid_waves<32, 2, false>(p.wn, a, s);
+            return p.wn == 8 ? launch_mid<16, 8, 1, 4, false>(a, s)
+                             : launch_mid_waves<16>(p.wn, a, s);
+        case kMid16x2: return launch_mid<16, 4, 2, 4, false>(a, s);
+        case kMid32: return launch_mid_waves<32>(p.wn, a, s);
         case kTileSmall: return launch_tile<2, 4, 1, 4, false, true>(a, s);
         case kTileMid: return launch_tile<4, 4, 1, 4, false, true>(a, s);
         case kTile128: return launch_tile<8, 4, 1, 4, false, false>(a, s);

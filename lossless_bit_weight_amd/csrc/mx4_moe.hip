@@ -724,8 +724,9 @@ void launch_up_one(const MoeArgs& a, hipStream_t s) {
     constexpr int WN = 1, KW = 4, UG = 4;   // (1, 8, 2): 12.9 against 12.1 us at H = 5120, I = 1280
     using X = Expert<true, 1, 2, WN, KW, UG, UG>;
     const int blocks = (a.I / 16 + WN - 1) / WN;
-    hipLaunchKernelGGL((up_one_kernel<EV, WN, KW, UG>), dim3((unsigned)(a.top_k * blocks), (unsigned)a.T),
-                       dim3(X::kThreads), X::lds(4), s, a, blocks);
+    const dim3 grid((unsigned)(a.top_k * blocks), (unsigned)a.T);
+    hipLaunchKernelGGL((up_one_kernel<EV, WN, KW, UG>), grid, dim3(X::kThreads), X::lds(4), s, a,
+                       blocks);
 }
 
 template <int PARTS, int WN, int KW, int UG>
@@ -748,8 +749,9 @@ void launch_route(const MoeArgs& a, hipStream_t s) {
 
 size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bool y_f32) {
     const int64_t pairs = T * top_k;
-    return up256((size_t)max_slots(T, H, I, E, top_k) * kSlotWords * 4) + 2 * up256((size_t)pairs * 4) +
-           up256((size_t)pairs * H * 4) + (size_t)(y_f32 ? 3 : 2) * pairs * I * 2;
+    const size_t slots = (size_t)max_slots(T, H, I, E, top_k) * kSlotWords * 4;
+    return up256(slots) + 2 * up256((size_t)pairs * 4) + up256((size_t)pairs * H * 4) +
+           (size_t)(y_f32 ? 3 : 2) * pairs * I * 2;
 }
 
 hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
