@@ -136,8 +136,8 @@ constexpr int kMaxTopK = 32;
 
 // Up to 16 of the pairs (token, chosen expert) of one expert: words [0] the
 // expert, [1] their number (0: none, nothing to do), [2] the first pair's place
-// among all, [16 + i] the i-th pair's token (past the last: the first's).  With
-// one token only words 0, 1 and [3], the expert's share (fp32).
+// among all, [16 + i] the i-th pair's token (past the last: the first's).  Where
+// tokens go one by one a slot is a pair: words 0 and [3], the expert's share (fp32).
 constexpr int kSlotWords = 32;
 
 struct MoeArgs {
@@ -150,7 +150,7 @@ struct MoeArgs {
     void* y;
     int64_t ldy;
     int y_f32;
-    int max_slots;          // min(E, pairs) + pairs / 16
+    int max_slots;          // min(E, pairs) + pairs / 16, or pairs
     // workspace: the pairs in the order of (expert, token), cut into slots
     int* slots;             // [max_slots][kSlotWords]
     int* place;             // [T][top_k] place of token t's j-th pair, or -1

@@ -489,7 +489,6 @@ __global__ __launch_bounds__(WN* KW * 64) void up_one_kernel(MoeArgs a, int bloc
         if (threadIdx.x == 0) {
             int* o = a.slots + pair * kSlotWords;
             o[0] = e;
-            o[1] = e >= 0;
             o[3] = __float_as_int(expf(mine - top) / sum);
         }
     }
@@ -664,8 +663,9 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // and the bytes expected: 2 tokens, 2 of 8 experts, H = 5120, I = 1280 17.6 / 24.4 (5 MB);
 // 4 tokens, 8 of 127, H = 2080, I = 736 31.0 / 32.2 (7 MB); 3 tokens, 6 of 64, H = 4096,
 // I = 1408 41.9 / 42.0 (16 MB); 16 tokens, 4 of 64, H = 1024, I = 512 24.6 / 21.6 (25 MB);
-// 4 tokens, 6 of 64, H = 5120, I = 1280 58.2 / 53.8 (35 MB).
-constexpr int kOneByOne = 16;               // tokens
+// 4 tokens, 6 of 64, H = 5120, I = 1280 58.2 / 53.8 (35 MB); 32 tokens, 1 of 22,
+// H = 800, I = 320 16.4 / 18.0 (9 MB), 64, 1 of 64, 26.9 / 20.7 (13 MB).
+constexpr int kOneByOne = 32;               // tokens
 constexpr int64_t kRepeatedBytes = 16 << 20;
 bool one_by_one(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     if (T > kOneByOne) return false;

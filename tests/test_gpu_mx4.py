@@ -245,7 +245,8 @@ MOE_SHAPES = [(1, 64, 32, 1, 1), (1, 256, 96, 8, 2), (2, 160, 64, 5, 5), (7, 416
               # workgroups of the down product; one token on every width of the choice
               (4, 512, 448, 8, 8), (9, 512, 256, 24, 12), (16, 288, 608, 70, 32),
               (6, 96, 4128, 4, 4), (40, 96, 4128, 4, 2), (40, 1056, 64, 64, 4),
-              (1, 160, 96, 100, 3), (2, 96, 64, 250, 32), (1, 96, 64, 1024, 32)]
+              (24, 96, 64, 30, 2), (1, 160, 96, 100, 3), (2, 96, 64, 250, 32),
+              (1, 96, 64, 1024, 32)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
@@ -270,11 +271,12 @@ def test_moe(T, H, I, E, k, renormalize, out):
     assert torch.equal(z, y)
 
 
-@pytest.mark.parametrize("E,H,I", [(6, 128, 64), (200, 128, 64), (6, 512, 1024)])
-def test_moe_routing_edges(E, H, I):
+@pytest.mark.parametrize("T,E,H,I", [(9, 6, 128, 64), (9, 200, 128, 64), (9, 6, 512, 1024),
+                                     (50, 6, 128, 64), (50, 200, 128, 64)])
+def test_moe_routing_edges(T, E, H, I):
     """Ties (also of -0 and +0), masked experts, a token with fewer experts than
     top_k, one with none, and NaN and infinite logits."""
-    T, k = 9, 4
+    k = 4
     xv, logits, w13, w2, q13, q2 = _moe_case(T, H, I, E, 40)
     logits[0] = 0.0
     logits[1] = np.where(np.arange(E) % 2, 0.0, -0.0)
