@@ -172,7 +172,10 @@ hipError_t launch_small(GemmArgs a, hipStream_t s) {
 // itself, the caches deliver as many bytes of x as of weights (gate+up M = 16:
 // 29.2 us there, 27.1 here; with x's reads left out, 18).  LDS row m of a
 // group holds x's 16 pieces of 8 values, piece p at place p ^ (m % 16), so that
-// the rows one read takes a piece from lie in 16 different places.
+// the rows one read takes a piece from lie in 16 different places.  From 16
+// rows on the weights are read through the caches: row blocks share them, and the
+// weights of a small model stay in the last of them (gate+up M = 16 over 190 MB of
+// weights 19.6 us, past the caches 20.8; over 760 MB 24.2 and 23.1).
 template <int ROWS, int WN, int KW, int UG, bool XM>
 struct Mid {
     static constexpr int kThreads = WN * KW * 64;
@@ -760,17 +763,20 @@ struct Plan {
 };
 
 // Waves beside each other that spread nt tiles best over 256 CUs: the CU with the
-// most of them decides.  Gate+up, 2176 tiles, M = 32, us (tiles of that CU): 9 waves
-// 26.4 (9), 12 30.1 (12), 5 33.2 (10), 7 35.4 (14), 8 36.8 (16).  Of equals the most
-// waves, which share x.
-int spread(int64_t nt) {
+// most of them decides; up to 16 rows a CU with one workgroup, whose barriers nothing
+// fills, counts a fifth more.  us (tiles of that CU): gate+up, 2176 tiles, M = 16,
+// 5 waves 24.4 (2 x 5), 9 25.4 (9), 7 26.8 (2 x 7), 12 28.6 (12), 4 27.6 (3 x 4);
+// M = 32, 9 waves 30.1, 5 31.3, 12 32.0, 7 35.0, 4 42.4; 1792 tiles, M = 16, 4 waves
+// 15.5 (2 x 4), 7 17.6 (7).  Of equals the most waves, which share x.
+int spread(int64_t nt, bool few_rows) {
     static const int kWaves[] = {12, 9, 7, 5, 4};
     int best = 4;
     int64_t least = -1;
     for (const int w : kWaves) {
-        const int64_t load = ((nt + w - 1) / w + 255) / 256 * w;
-        if (least < 0 || load < least) {
-            least = load;
+        const int64_t most = ((nt + w - 1) / w + 255) / 256;
+        const int64_t cost = most * w * (few_rows && most == 1 ? 6 : 5);
+        if (least < 0 || cost < least) {
+            least = cost;
             best = w;
         }
     }
@@ -826,13 +832,13 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
         } else {
             p.kernel = kMid16;
             if (many)
-                p.wn = spread(nt);
+                p.wn = spread(nt, true);
             else
                 S = slices(480, blocks(16, 64));
         }
     } else if (many && M <= 32 && (xm || blocks(32, 256) < 200)) {
         p.kernel = kMid32;
-        p.wn = spread(nt);
+        p.wn = spread(nt, false);
     } else if (xm && !many &&
                (M <= (lengthy ? 192 : 256) || (!lengthy && blocks(32, 64) <= 640))) {
         if (lengthy) {
