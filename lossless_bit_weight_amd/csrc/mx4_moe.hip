@@ -696,12 +696,13 @@ void launch_expert(const MoeArgs& a, hipStream_t s) {
 // Waves beside each other share a slot's rows, waves that split K let a few slots fill
 // the GPU.  Up, H = 5120, I = 1280, 12 tokens, 2 of 8 experts (at most 360 workgroups of
 // 2 x 2 waves): whole layer 38.6 us, with 1 x 4 waves 34.2; 48 tokens, 2 of 16 (880):
-// 53.4 and 55.6.
+// 53.4 and 55.6.  Above four rows a slot units of two groups: 128 tokens, 4 of 16, 94
+// with units of one, 88.
 void launch_up(const MoeArgs& a, hipStream_t s) {
     if ((int64_t)a.max_slots * ((a.I + 31) / 32) < 512)
         launch_expert<true, 1, 2, 1, 4, 2, 1>(a, s);
     else
-        launch_expert<true, 1, 2, 2, 2, 2, 1>(a, s);
+        launch_expert<true, 1, 2, 2, 2, 2, 2>(a, s);
 }
 
 // Down, by workgroups of 4 x 1 waves: 16 tokens, 6 of 64 experts (2800) 104.9 us, with

@@ -245,7 +245,8 @@ MOE_SHAPES = [(1, 64, 32, 1, 1), (1, 256, 96, 8, 2), (2, 160, 64, 5, 5), (7, 416
               # workgroups of the down product; one token on every width of the choice
               (4, 512, 448, 8, 8), (9, 512, 256, 24, 12), (16, 288, 608, 70, 32),
               (6, 96, 4128, 4, 4), (40, 96, 4128, 4, 2), (40, 1056, 64, 64, 4),
-              (24, 96, 64, 30, 2), (1, 160, 96, 100, 3), (2, 96, 64, 250, 32),
+              (24, 96, 64, 30, 2), (28, 96, 4128, 4, 2), (128, 160, 96, 3, 3),
+              (70, 1056, 160, 2, 1), (1, 160, 96, 100, 3), (2, 96, 64, 250, 32),
               (1, 96, 64, 1024, 32)]
 
 
