@@ -101,6 +101,12 @@ def mx4_moe_workspace_bytes(T: int, H: int, I: int, E: int, top_k: int,
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=4096)
+def _sizes(R: int, K: int, batch: int) -> tuple:
+    tiles = batch * ((R + 15) // 16)
+    return tiles * ((K + 127) // 128) * 1024, tiles * ((K + 511) // 512) * 256
+
+
 @dataclass
 class MX4Tensor:
     """A container of one [R, K] matrix (batch None) or of `batch` of them: one
@@ -112,9 +118,7 @@ class MX4Tensor:
     batch: int | None = None
 
     def __post_init__(self):
-        tiles = (self.batch or 1) * ((self.R + 15) // 16)
-        self._code_bytes = tiles * ((self.K + 127) // 128) * 1024
-        self._scale_bytes = tiles * ((self.K + 511) // 512) * 256
+        self._code_bytes, self._scale_bytes = _sizes(self.R, self.K, self.batch or 1)
 
     @property
     def shape(self) -> tuple:
@@ -172,16 +176,10 @@ _current = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
     else torch.cuda.current_device
 
 
-def _call(device: int, fn, *args) -> None:
-    """fn(*args, stream) on torch's current stream of `device`, which is made
-    current for the launch."""
-    if _current() == device:
-        status = fn(*args, _raw_stream(device))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(device))
-    if status != 0:
-        raise MX4Error(status, fn.__name__)
+# Every call launches with its tensors' device current: a function that finds another
+# one current calls itself again under it.
+def _away(device: int) -> bool:
+    return _current() != device
 
 
 def _same(device: int, *others: int) -> None:
@@ -215,7 +213,8 @@ def _batched(t: torch.Tensor, what: str) -> tuple:
     """(batch or None, R, K, row stride, matrix stride) of a 2-D or 3-D tensor."""
     shape = t.shape
     if len(shape) == 2:
-        return None, *_rows(t, what), 0
+        R, K, ld = _rows(t, what)
+        return None, R, K, ld, 0
     if len(shape) != 3:
         raise ValueError("%s must be 2-D or 3-D" % what)
     B, R, K = shape
@@ -272,6 +271,9 @@ def _container(R: int, K: int, batch: int | None) -> MX4Tensor:
 def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None) -> MX4Tensor:
     """x [R, K] or [B, R, K] (BF16 or fp32, unit column stride) as MX4."""
     dev = _gpu(x, "x")
+    if _away(dev):
+        with torch.cuda.device(dev):
+            return mx4_quantize(x, out)
     xt = _type_of(x.dtype)
     B, R, K, ld, ldb = _batched(x, "x")
     if out is None:
@@ -284,7 +286,8 @@ def mx4_quantize(x: torch.Tensor, out: MX4Tensor | None = None) -> MX4Tensor:
             raise ValueError("out holds %s, x is %s" % (out.shape, tuple(x.shape)))
         codes, scales, out_dev = out.ptrs("out")
         _same(dev, out_dev)
-    _call(dev, lib().mx4_quantize, x.data_ptr(), xt, B or 1, R, K, ld, ldb, codes, scales)
+    _check(lib().mx4_quantize(x.data_ptr(), xt, B or 1, R, K, ld, ldb, codes, scales,
+                              _raw_stream(dev)), "mx4_quantize")
     return out
 
 
@@ -292,6 +295,9 @@ def mx4_dequantize(q: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """The values a container stands for, [R, K] or [B, R, K]."""
     codes, scales, dev = q.ptrs("q")
+    if _away(dev):
+        with torch.cuda.device(dev):
+            return mx4_dequantize(q, out_dtype, out)
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):
             raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
@@ -304,7 +310,8 @@ def mx4_dequantize(q: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16,
             raise ValueError("out is %s, q holds %s" % (tuple(out.shape), q.shape))
         B, R, K, ld, ldb = _batched(out, "out")
     yt = _type_of(out.dtype)
-    _call(dev, lib().mx4_dequantize, codes, scales, B or 1, R, K, out.data_ptr(), yt, ld, ldb)
+    _check(lib().mx4_dequantize(codes, scales, B or 1, R, K, out.data_ptr(), yt, ld, ldb,
+                                _raw_stream(dev)), "mx4_dequantize")
     return out
 
 
@@ -315,6 +322,9 @@ def mx4_gemm(x, w: MX4Tensor, out_dtype: torch.dtype = torch.float32,
     if w.batch is not None:
         raise ValueError("w must hold one matrix")
     wc, wsc, dev = w.ptrs("w")
+    if _away(dev):
+        with torch.cuda.device(dev):
+            return mx4_gemm(x, w, out_dtype, y, workspace)
     N, K = w.R, w.K
     x_mx4 = isinstance(x, MX4Tensor)
     if x_mx4:
@@ -334,9 +344,12 @@ def mx4_gemm(x, w: MX4Tensor, out_dtype: torch.dtype = torch.float32,
     _same(dev, x_dev)
     y, ldy, yt = _output(y, M, N, out_dtype, dev, w.data)
     keep, wsp, wsb = _workspace(mx4_gemm_workspace_bytes(M, N, K, x_mx4), workspace, w.data)
-    L = lib()
-    _call(dev, L.mx4_gemm_mx4 if x_mx4 else L.mx4_gemm, a0, a1, a2, wc, wsc, N, K, y.data_ptr(),
-          ldy, yt, wsp, wsb)
+    if x_mx4:
+        _check(lib().mx4_gemm_mx4(a0, a1, a2, wc, wsc, N, K, y.data_ptr(), ldy, yt, wsp, wsb,
+                                  _raw_stream(dev)), "mx4_gemm_mx4")
+    else:
+        _check(lib().mx4_gemm(a0, a1, a2, wc, wsc, N, K, y.data_ptr(), ldy, yt, wsp, wsb,
+                              _raw_stream(dev)), "mx4_gemm")
     return y
 
 
@@ -347,6 +360,9 @@ def mx4_moe(x: torch.Tensor, logits: torch.Tensor, w13: MX4Tensor, w2: MX4Tensor
     [T, E], w13 a container of E matrices [2 I, H] (gate rows, then up rows),
     w2 of E matrices [H, I]; T <= 128."""
     dev, logits_dev = _gpu(x, "x"), _gpu(logits, "logits")
+    if _away(dev):
+        with torch.cuda.device(dev):
+            return mx4_moe(x, logits, w13, w2, top_k, renormalize, out_dtype, y, workspace)
     if x.dtype not in _BF16_TYPES:
         raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
     if logits.dtype is not torch.float32:
@@ -363,6 +379,7 @@ def mx4_moe(x: torch.Tensor, logits: torch.Tensor, w13: MX4Tensor, w2: MX4Tensor
     y, ldy, yt = _output(y, T, H, out_dtype, dev, x)
     need = mx4_moe_workspace_bytes(T, H, I, E, int(top_k), y.dtype)
     keep, wsp, wsb = _workspace(need, workspace, x)
-    _call(dev, lib().mx4_moe, x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I,
-          E, int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp, wsb)
+    _check(lib().mx4_moe(x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I, E,
+                         int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp, wsb,
+                         _raw_stream(dev)), "mx4_moe")
     return y
