@@ -228,6 +228,31 @@ def test_gemm_extreme_scales():
             ref.assert_close(_host(mx4.mx4_gemm(x, wq)), want, tol, "f32", "extreme")
 
 
+def test_offsets_past_32_bits():
+    """A container of 4.4 GB that repeats one matrix (read again at stride 0): every
+    repetition decodes to, and multiplies as, the first one, bit for bit."""
+    B, R, K = 130, 1024, 65536
+    w = _dev(_values((R, K), 90, 0.02))
+    one = mx4.mx4_quantize(w)
+    q = mx4.mx4_quantize(w.expand(B, R, K))
+    assert q.codes.numel() > 1 << 32
+    y = mx4.mx4_dequantize(q)
+    first = mx4.mx4_dequantize(one)
+    for b in (0, 64, 65, B - 1):
+        assert torch.equal(y[b], first)
+    del y
+    whole = mx4.MX4Tensor(q.data, B * R, K)             # the same bytes as one [B R, K]
+    for M in (1, 3, 40, 200):
+        xv = _values((M, K), 91 + M)
+        x = _dev(xv)
+        for a, av in ((x, xv), (mx4.mx4_quantize(x), ref.rounded(xv))):
+            y = mx4.mx4_gemm(a, whole).view(M, B, R)
+            assert torch.equal(y, y[:, :1].expand(M, B, R))
+            rows = _host(first[:64])
+            want, tol = ref.matmul(av, rows)
+            ref.assert_close(_host(y[:, B - 1, :64]), want, tol, "f32", "large")
+
+
 # ---- expert layer -------------------------------------------------------------------
 
 def _moe_case(T, H, I, E, seed):
@@ -312,6 +337,23 @@ def test_moe_bad_expert_stays_with_its_tokens():
     assert chose.any() and not chose.all()
     assert np.array_equal(np.isnan(y).any(1), chose)
     assert np.array_equal(np.isnan(y[:, 7]), chose)
+
+
+def test_moe_offsets_past_32_bits():
+    """1024 times the same expert, 4.4 GB of gate and up weights: the last ones give
+    what the first ones give, bit for bit."""
+    H, I, E = 4096, 1056, 1024
+    w13, w2 = _dev(_values((2 * I, H), 95, 0.02)), _dev(_values((H, I), 96, 0.02))
+    q13 = mx4.mx4_quantize(w13.expand(E, 2 * I, H))
+    q2 = mx4.mx4_quantize(w2.expand(E, H, I))
+    assert q13.codes.numel() > 1 << 32
+    for T in (1, 3, 40):
+        x = _dev(_values((T, H), 97 + T))
+        logits = torch.zeros((T, E), device="cuda")
+        logits[:, 0], logits[:, 1] = 3.0, 2.5
+        first = mx4.mx4_moe(x, logits, q13, q2, 2)
+        last = mx4.mx4_moe(x, logits.roll(E - 2, 1), q13, q2, 2)
+        assert first.abs().max() > 0 and torch.equal(first, last)
 
 
 # ---- a run of them together ------------------------------------------------------------
