@@ -228,6 +228,17 @@ def test_gemm_extreme_scales():
             ref.assert_close(_host(mx4.mx4_gemm(x, wq)), want, tol, "f32", "extreme")
 
 
+@pytest.mark.parametrize("ldx", [(1 << 23) - 8, 1 << 23])
+def test_gemm_wide_row_stride(ldx):
+    """Rows of x 16 MB apart, on both sides of what a tile's 24-bit row offsets take."""
+    M, N, K = 96, 16400, 64
+    xv, wv = _values((M, K), 85), _values((N, K), 86)
+    x = torch.empty_strided((M, K), (ldx, 1), dtype=torch.bfloat16, device="cuda")
+    x.copy_(_dev(xv))
+    want, tol = ref.matmul(xv, ref.rounded(wv))
+    ref.assert_close(_host(mx4.mx4_gemm(x, mx4.mx4_quantize(_dev(wv)))), want, tol, "f32", "wide")
+
+
 def test_offsets_past_32_bits():
     """A container of 4.4 GB that repeats one matrix (read again at stride 0): every
     repetition decodes to, and multiplies as, the first one, bit for bit."""
