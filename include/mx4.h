@@ -133,8 +133,8 @@ int mx4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_mx4, size_t 
  *   y[t]    = sum over e in S(t) of p(t, e) * D_e h.
  * An expert with logit -inf is never chosen, so such a token has fewer experts
  * (all of them -inf: y[t] = 0); a NaN logit makes its token's y NaN.  The
- * hidden values h are carried between the two products as sums of BF16 parts
- * that hold 16 bits (BF16 output) or all 24 (fp32 output) of their mantissa.
+ * hidden values h are carried between the two products with all 24 bits of
+ * their mantissa, the sums are fp32.
  *   x      : device BF16 [T, H], as mx4_gemm's.
  *   logits : device fp32 [T, E], row stride ldl >= E elements, 4-byte aligned.
  *   w13_*  : a container of E matrices [2*I, H], rows 0..I-1 of each G_e, rows

@@ -156,7 +156,7 @@ struct MoeArgs {
     int* place;             // [T][top_k] place of token t's j-th pair, or -1
     float* share;           // [T][top_k]
     float* out;             // [pairs][H] an expert's output for a token
-    uint16_t* h;            // [parts][pairs][I], hidden values as sums of BF16 parts
+    void* h;                // hidden values: [pairs][I] fp32, or (y_f32) BF16 parts [3][pairs][I]
 };
 
 size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bool y_f32);

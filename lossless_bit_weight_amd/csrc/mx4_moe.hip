@@ -245,6 +245,58 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
     }
 }
 
+// ---- hidden values --------------------------------------------------------------------
+// h goes to the matrix units as three BF16 numbers whose sum it is: all 24 bits of its
+// mantissa, whatever the output's type (two of them would differ from an fp32 product
+// by 2^-16 of h, which differences of hidden values do not hide).  Up stores it whole,
+// 4 bytes that down splits (BF16 outputs), or as its parts, 6 bytes (fp32 outputs).
+// Whole layer, us, BF16 output, whole / parts: H = 2080, I = 736, 61 tokens, 8 of 127
+// experts 86.9 / 89.6; H = 4096, I = 14336, 128 tokens, 2 of 8 337 / 327.
+enum Hidden { kF32, kParts };
+
+// V values of h (an infinity's rest is 0; a NaN that arithmetic made keeps its quiet bit
+// in the upper half).
+template <int V>
+struct Values {
+    typedef float f32_t __attribute__((ext_vector_type(V)));
+    typedef uint32_t u32_t __attribute__((ext_vector_type(V / 2)));
+    f32_t f;
+    __device__ __forceinline__ void load(const float* p) {
+        f = *reinterpret_cast<const f32_t*>(p);
+    }
+    // Part P of them, in order: the upper half of each number's bits, which are taken off.
+    template <int P>
+    __device__ __forceinline__ void take(uint8_t* to) {
+        u32_t v;
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            uint32_t b[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = f[2 * j + i];
+                b[i] = __float_as_uint(x);
+                if (P < 2) f[2 * j + i] = x - __uint_as_float(b[i] & 0xFFFF0000u);
+                if (P < 1 && __builtin_isinf(x)) f[2 * j + i] = 0.f;
+            }
+            v[j] = __builtin_amdgcn_perm(b[1], b[0], 0x07060302u);
+        }
+        *reinterpret_cast<u32_t*>(to) = v;
+    }
+    // Part p of them (zeros unless `in`) to place(p).
+    template <class Place>
+    __device__ __forceinline__ void split(bool in, Place place) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = in ? f[i] : 0.f;
+        take<0>(place(0));
+        take<1>(place(1));
+        take<2>(place(2));
+    }
+};
+// of a piece of eight that a thread takes where `pieces` of them are for `threads`
+constexpr int values_each(int pieces, int threads) {
+    return pieces >= threads ? 8 : pieces * 2 >= threads ? 4 : 2;
+}
+
 // ---- the experts' products -----------------------------------------------------------
 // A workgroup: one slot by WN waves' weight tiles (up: a gate tile and the up tile
 // beside it a wave; down: R tiles); KW groups of such waves take every KW-th unit
@@ -254,8 +306,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
 // them: slots of up to four rows, the most by far, move a quarter of the bytes, and
 // read weights that no other slot does (16 tokens 106 us past the caches, 116
 // through them; 128 tokens at 16 an expert the reverse, 109 and 102).
-template <bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
+template <bool UP, int R, int WN, int KW, int UG4, int UG16>
 struct Expert {
+    static constexpr int PARTS = UP ? 1 : 3;
+    // four groups of waves on h: one buffer, behind one more barrier a unit, so that two
+    // workgroups fit a CU (12 tokens, 2 of 8 experts, H = 4096, I = 14336 169 -> 147 us)
+    static constexpr int kBuffers = !UP && KW == 4 ? 1 : 2;
     static constexpr int kThreads = WN * KW * 64;
     static constexpr int ug(int rows) { return rows > 4 ? UG16 : UG4; }
     static constexpr int pieces(int rows) { return rows * 16 * ug(rows) * PARTS; }
@@ -263,19 +319,24 @@ struct Expert {
         return (pieces(rows) + WN * 64 - 1) / (WN * 64) * (WN * 64) * 16;
     }
     static constexpr int lds(int rows) {
-        const int x4 = 2 * KW * stage(4), x16 = rows > 4 ? 2 * KW * stage(16) : 0;
+        const int x4 = kBuffers * KW * stage(4), x16 = rows > 4 ? kBuffers * KW * stage(16) : 0;
         const int x = x4 > x16 ? x4 : x16, red = KW * WN * R * 1024;
         return x > red ? x : red;
     }
 };
 
-template <int ROWS, bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
+template <int ROWS, bool UP, Hidden F, int R, int WN, int KW, int UG4, int UG16>
 __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, int e, int count,
                                             int p0, int block, uint8_t* lds) {
-    using X = Expert<UP, PARTS, R, WN, KW, UG4, UG16>;
-    constexpr int UG = X::ug(ROWS);
-    constexpr int kStage = X::stage(ROWS), P = kStage / (WN * 64 * 16);
+    using X = Expert<UP, R, WN, KW, UG4, UG16>;
+    constexpr bool kSplit = !UP && F == kF32;   // h comes whole and is split here
+    constexpr int UG = X::ug(ROWS), PARTS = X::PARTS;
+    constexpr int kStage = X::stage(ROWS);
     constexpr int kPart = ROWS * 16 * UG;       // pieces of one part of a unit
+    constexpr int V = kSplit ? values_each(kPart, WN * 64) : 8;     // values a thread at a time
+    constexpr int P = kSplit ? kPart * 8 / (V * WN * 64) : kStage / (WN * 64 * 16);
+    static_assert(!kSplit || P * V * WN * 64 == kPart * 8, "every thread has as many");
+    using Piece = std::conditional_t<kSplit, Values<V>, u32x4_t>;
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int kw = w / WN, wn = w % WN;
@@ -303,22 +364,28 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
         wp[r] = m.codes + t * G * kCodeBlock;
         sp[r] = m.scales + t * Q * kScaleBlock;
     }
-    const uint16_t* xp[P];
+    using Value = std::conditional_t<kSplit, float, uint16_t>;
+    const Value* xp[P];
     int xk[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int piece = (i * WN + wn) * 64 + lane;
+        const int value = ((i * WN + wn) * 64 + lane) * V, piece = value / 8;
         int part = piece / kPart;
         if (part > PARTS - 1) part = PARTS - 1;
         const int row = piece % kPart / (16 * UG);
         if constexpr (UP)
             xp[i] = a.x + (slot == nullptr ? 0 : slot[16 + row] * a.ldx);
+        else if constexpr (kSplit)
+            xp[i] = static_cast<const float*>(a.h) +
+                    (p0 + (row < count ? row : 0)) * (int64_t)a.I;
         else
-            xp[i] = a.h + (part * pairs + p0 + (row < count ? row : 0)) * (int64_t)a.I;
-        xk[i] = piece % (16 * UG) * 8;
+            xp[i] = static_cast<const uint16_t*>(a.h) +
+                    (part * pairs + p0 + (row < count ? row : 0)) * (int64_t)a.I;
+        xk[i] = value % (128 * UG);
     }
-    uint8_t* mine = lds + kw * 2 * kStage;
-    u32x4_t wb[2][UG][R], xb[P];
+    uint8_t* mine = lds + kw * X::kBuffers * kStage;
+    u32x4_t wb[2][UG][R];
+    Piece xb[P];
     uint32_t ws[2][R];
     bool xin[P];
     // (no branch: a place past the last unit, group or K is a valid one whose x is
@@ -343,28 +410,44 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
         for (int i = 0; i < P; ++i) {
             const int k = u * UG * 128 + xk[i];
             xin[i] = u < U && k < K;
-            xb[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[i] ? k : 0));
+            if constexpr (kSplit)
+                xb[i].load(xp[i] + (xin[i] ? k : 0));
+            else
+                xb[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[i] ? k : 0));
         }
     };
     auto stage = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int piece = (i * WN + wn) * 64 + lane;
-            const int row = piece % kPart / (16 * UG);
-            const int at = (piece & ~15) + x_place(piece & 15, row);
-            u32x4_t v;
+            const int value = ((i * WN + wn) * 64 + lane) * V;
+            const auto place = [&](int p) {
+                const int piece = value / 8 + p * kPart;
+                const int at = (piece & ~15) + x_place(piece & 15, piece / (16 * UG));
+                return mine + (X::kBuffers > 1 ? buf * kStage : 0) + at * 16 + value % 8 * 2;
+            };
+            if constexpr (kSplit) {
+                xb[i].split(xin[i], place);
+            } else {
+                u32x4_t v;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = xin[i] ? xb[i][k] : 0u;
-            *reinterpret_cast<u32x4_t*>(mine + buf * kStage + at * 16) = v;
+                for (int k = 0; k < 4; ++k) v[k] = xin[i] ? xb[i][k] : 0u;
+                *reinterpret_cast<u32x4_t*>(place(0)) = v;
+            }
         }
     };
     f32x4_t acc[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r] = f32x4_t{0, 0, 0, 0};
-    const int row = c & (ROWS - 1);
+    // four rows leave columns of the operand for their parts: column 4 p + m is part p
+    // of row m (the last four are the third part once more, unused), one matrix
+    // instruction instead of three (16 tokens, 6 of 64 experts, H = 5120, I = 1280
+    // 109.0 -> 104.4 us)
+    constexpr bool kColumns = !UP && ROWS == 4;
+    constexpr int kOperands = kColumns ? 1 : PARTS;
+    const int row = kColumns ? (c < 12 ? c : c - 4) : c & (ROWS - 1);
     auto product = [&](auto sc) {
         constexpr int s = decltype(sc)::value;
-        const uint8_t* xl = mine + s * kStage;
+        const uint8_t* xl = mine + (X::kBuffers > 1 ? s * kStage : 0);
 #pragma unroll
         for (int j = 0; j < UG; ++j) {
             float f[R];
@@ -372,16 +455,16 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
             for (int r = 0; r < R; ++r) f[r] = scale_f32((ws[s][r] >> (8 * j)) & 255u);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                bf16x8_t xv[PARTS];
+                bf16x8_t xv[kOperands];
 #pragma unroll
-                for (int p = 0; p < PARTS; ++p)
+                for (int p = 0; p < kOperands; ++p)
                     xv[p] = *reinterpret_cast<const bf16x8_t*>(
                         xl + (p * kPart + row * 16 * UG + 16 * j + x_place(q, b, row)) * 16);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     const bf16x8_t wv = expand8(wb[s][j][r][b], f[r]);
 #pragma unroll
-                    for (int p = 0; p < PARTS; ++p) acc[r] = mfma_bf16(wv, xv[p], acc[r]);
+                    for (int p = 0; p < kOperands; ++p) acc[r] = mfma_bf16(wv, xv[p], acc[r]);
                 }
             }
         }
@@ -395,6 +478,7 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
         __builtin_amdgcn_sched_barrier(0);
         product(sc);
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (X::kBuffers == 1) __syncthreads();
         stage(s ^ 1);
         __syncthreads();
     };
@@ -425,12 +509,15 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
                 u += red[k * WN * R * 256 + 256 + at];
             }
             const float h = g / (1.f + expf(-g)) * u;
-            uint16_t* o = a.h + (int64_t)(p0 + m) * a.I + n;
-            // h = the sum of BF16 numbers, each the rounded rest of those before: two hold
-            // 16 bits of its mantissa, three all 24
-            const int parts = a.y_f32 ? 3 : 2;
+            const int64_t at_h = (int64_t)(p0 + m) * a.I + n;
+            if (!a.y_f32) {
+                static_cast<float*>(a.h)[at_h] = h;
+                continue;
+            }
+            // h = the sum of three BF16 numbers, each the rounded rest of those before
+            uint16_t* o = static_cast<uint16_t*>(a.h) + at_h;
             float rest = h;
-            for (int p = 0; p < parts; ++p) {
+            for (int p = 0; p < 3; ++p) {
                 const uint16_t b = bf16_bits(rest);
                 o[p * pairs * a.I] = b;
                 const float f = __uint_as_float((uint32_t)b << 16);
@@ -440,22 +527,25 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
             const int at = col / 16 * 256 + in;
             float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < KW; ++k) s += red[k * WN * R * 256 + at];
+            for (int k = 0; k < KW; ++k) {
+                const float* v = red + k * WN * R * 256 + at;
+                s += kColumns ? v[0] + (v[16] + v[32]) : v[0];
+            }
             a.out[(int64_t)(p0 + m) * a.H + n] = s;
         }
     }
 }
 
-template <bool MANY, bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
+template <bool MANY, bool UP, Hidden F, int R, int WN, int KW, int UG4, int UG16>
 __global__ __launch_bounds__(WN* KW * 64) void expert_kernel(MoeArgs a, int blocks) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int* slot = a.slots + (blockIdx.x / blocks) * kSlotWords;
     const int e = slot[0], count = slot[1], p0 = slot[2], block = blockIdx.x % blocks;
     if (count == 0) return;
     if (MANY && count > 4)
-        expert_body<16, UP, PARTS, R, WN, KW, UG4, UG16>(a, slot, e, count, p0, block, lds);
+        expert_body<16, UP, F, R, WN, KW, UG4, UG16>(a, slot, e, count, p0, block, lds);
     else
-        expert_body<4, UP, PARTS, R, WN, KW, UG4, UG16>(a, slot, e, count, p0, block, lds);
+        expert_body<4, UP, F, R, WN, KW, UG4, UG16>(a, slot, e, count, p0, block, lds);
 }
 
 // up for few tokens, each by itself (blockIdx.y): the token chooses for itself, slot
@@ -493,29 +583,35 @@ __global__ __launch_bounds__(WN* KW * 64) void up_one_kernel(MoeArgs a, int bloc
         }
     }
     if (e < 0) return;
-    expert_body<4, true, 1, 2, WN, KW, UG, UG>(a, nullptr, e, 1, pair, block, lds);
+    expert_body<4, true, kF32, 2, WN, KW, UG, UG>(a, nullptr, e, 1, pair, block, lds);
 }
 
 // ---- down for few tokens -------------------------------------------------------------
 // A workgroup: WN tiles of 16 outputs of one token (blockIdx.y).  The units (expert,
 // UG groups of its hidden values) are one sequence of which each of the KW groups of
 // waves takes every KW-th; a unit's product is weighted into the sum at once, and no
-// pair's output goes through memory.  All 16 columns of an operand hold the one token.
-template <int PARTS, int WN, int KW, int UG>
+// pair's output goes through memory.
+template <int WN, int KW, int UG>
 struct One {
+    static constexpr int PARTS = 3;
     static constexpr int kThreads = WN * KW * 64;
     static constexpr int kPieces = 16 * UG * PARTS;
     static constexpr int kStage = (kPieces + WN * 64 - 1) / (WN * 64) * (WN * 64) * 16;
     static constexpr int lds() {
-        const int x = 2 * KW * kStage, red = KW * WN * 64;
+        const int x = 2 * KW * kStage, red = KW * WN * PARTS * 64;
         return x > red ? x : red;
     }
 };
 
-template <int PARTS, int WN, int KW, int UG>
+template <Hidden F, int WN, int KW, int UG>
 __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
-    using X = One<PARTS, WN, KW, UG>;
-    constexpr int P = X::kStage / (WN * 64 * 16), kPart = 16 * UG;
+    using X = One<WN, KW, UG>;
+    constexpr bool kSplit = F == kF32;
+    constexpr int PARTS = X::PARTS, kPart = 16 * UG;
+    constexpr int V = kSplit ? values_each(kPart, WN * 64) : 8;
+    constexpr int P = kSplit ? kPart * 8 / (V * WN * 64) : X::kStage / (WN * 64 * 16);
+    static_assert(!kSplit || P * V * WN * 64 == kPart * 8, "every thread has as many");
+    using Piece = std::conditional_t<kSplit, Values<V>, u32x4_t>;
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -538,7 +634,8 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
     const int its = (units + KW - 1) / KW;
 
     uint8_t* mine = lds + kw * 2 * X::kStage;
-    u32x4_t wb[2][UG], xb[P];
+    u32x4_t wb[2][UG];
+    Piece xb[P];
     uint32_t ws[2];
     bool xin[P];
     auto load = [&](int s, int it) {
@@ -557,24 +654,40 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int piece = (i * WN + wn) * 64 + lane;
+            const int value = ((i * WN + wn) * 64 + lane) * V, piece = value / 8;
             const int part = piece / kPart < PARTS ? piece / kPart : PARTS - 1;
-            const int k = ui * UG * 128 + piece % kPart * 8;
+            const int k = ui * UG * 128 + value % (128 * UG);
             xin[i] = u < units && k < a.I;
-            xb[i] = *reinterpret_cast<const u32x4_t*>(
-                a.h + ((int64_t)part * a.T * a.top_k + first + sl) * a.I + (k < a.I ? k : 0));
+            using Value = std::conditional_t<kSplit, float, uint16_t>;
+            const int64_t row = (kSplit ? 0 : (int64_t)part * a.T * a.top_k) + first + sl;
+            const Value* p = static_cast<const Value*>(a.h) + row * a.I + (k < a.I ? k : 0);
+            if constexpr (kSplit)
+                xb[i].load(p);
+            else
+                xb[i] = *reinterpret_cast<const u32x4_t*>(p);
         }
     };
     auto stage = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int piece = (i * WN + wn) * 64 + lane;
-            u32x4_t v;
+            const int value = ((i * WN + wn) * 64 + lane) * V;
+            const auto place = [&](int p) {
+                const int piece = value / 8 + p * kPart;
+                const int at = (piece & ~15) + x_place(piece & 15, piece / kPart * 4);
+                return mine + buf * X::kStage + at * 16 + value % 8 * 2;
+            };
+            if constexpr (kSplit) {
+                xb[i].split(xin[i], place);
+            } else {
+                u32x4_t v;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = xin[i] ? xb[i][k] : 0u;
-            *reinterpret_cast<u32x4_t*>(mine + buf * X::kStage + piece * 16) = v;
+                for (int k = 0; k < 4; ++k) v[k] = xin[i] ? xb[i][k] : 0u;
+                *reinterpret_cast<u32x4_t*>(place(0)) = v;
+            }
         }
     };
+    // the first three columns of the operand hold the parts, the others the third again
+    const int column = (lane & 15) < PARTS ? lane & 15 : PARTS - 1;
     f32x4_t sum = {0, 0, 0, 0};
     auto product = [&](auto sc, int it) {
         constexpr int s = decltype(sc)::value;
@@ -586,10 +699,8 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const bf16x8_t wv = expand8(wb[s][j][b], f);
-#pragma unroll
-                for (int p = 0; p < PARTS; ++p)
-                    acc = mfma_bf16(wv, *reinterpret_cast<const bf16x8_t*>(
-                                            xl + (p * kPart + 16 * j + 4 * q + b) * 16), acc);
+                const int at = column * kPart + 16 * j + x_place(q, b, column * 4);
+                acc = mfma_bf16(wv, *reinterpret_cast<const bf16x8_t*>(xl + at * 16), acc);
             }
         }
         const int u = it * KW + kw;
@@ -618,14 +729,18 @@ __global__ __launch_bounds__(WN* KW * 64) void down_one_kernel(MoeArgs a) {
         }
     }
     __syncthreads();
-    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][16]
-    if ((lane & 15) == 0) *reinterpret_cast<f32x4_t*>(red + w * 16 + 4 * q) = sum;
+    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][PARTS][16]
+    if ((lane & 15) < PARTS)
+        *reinterpret_cast<f32x4_t*>(red + (w * PARTS + column) * 16 + 4 * q) = sum;
     __syncthreads();
     const int n = blockIdx.x * 16 * WN + tid;
     if (tid < 16 * WN && n < a.H) {
         float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < KW; ++k) v += red[k * WN * 16 + tid];
+        for (int k = 0; k < KW; ++k) {
+            const float* r = red + ((k * WN + tid / 16) * PARTS) * 16 + tid % 16;
+            v += r[0] + (r[16] + r[32]);
+        }
         const int64_t at = blockIdx.y * a.ldy + n;
         if (a.y_f32)
             static_cast<float*>(a.y)[at] = v;
@@ -678,18 +793,18 @@ int64_t max_slots(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     return one_by_one(T, H, I, E, top_k) ? pairs : (E < pairs ? E : pairs) + pairs / 16;
 }
 
-template <bool UP, int PARTS, int R, int WN, int KW, int UG4, int UG16>
+template <bool UP, Hidden F, int R, int WN, int KW, int UG4, int UG16>
 void launch_expert(const MoeArgs& a, hipStream_t s) {
-    using X = Expert<UP, PARTS, R, WN, KW, UG4, UG16>;
+    using X = Expert<UP, R, WN, KW, UG4, UG16>;
     static_assert(X::lds(16) <= 65536, "more LDS than a launch gets without asking");
     const int nt = (UP ? a.I : a.H) / 16, per = UP ? WN : WN * R;
     const int blocks = (nt + per - 1) / per;
     const dim3 grid((unsigned)((int64_t)a.max_slots * blocks)), block(X::kThreads);
     if (a.T <= 4)
-        hipLaunchKernelGGL((expert_kernel<false, UP, PARTS, R, WN, KW, UG4, UG16>), grid, block,
+        hipLaunchKernelGGL((expert_kernel<false, UP, F, R, WN, KW, UG4, UG16>), grid, block,
                            X::lds(4), s, a, blocks);
     else
-        hipLaunchKernelGGL((expert_kernel<true, UP, PARTS, R, WN, KW, UG4, UG16>), grid, block,
+        hipLaunchKernelGGL((expert_kernel<true, UP, F, R, WN, KW, UG4, UG16>), grid, block,
                            X::lds(16), s, a, blocks);
 }
 
@@ -700,41 +815,42 @@ void launch_expert(const MoeArgs& a, hipStream_t s) {
 // with units of one, 88.
 void launch_up(const MoeArgs& a, hipStream_t s) {
     if ((int64_t)a.max_slots * ((a.I + 31) / 32) < 512)
-        launch_expert<true, 1, 2, 1, 4, 2, 1>(a, s);
+        launch_expert<true, kF32, 2, 1, 4, 2, 1>(a, s);
     else
-        launch_expert<true, 1, 2, 2, 2, 2, 2>(a, s);
+        launch_expert<true, kF32, 2, 2, 2, 2, 2>(a, s);
 }
 
-// Down, by workgroups of 4 x 1 waves: 16 tokens, 6 of 64 experts (2800) 104.9 us, with
-// 2 x 2 waves 106.5; 16 tokens, 4 of 32, H = 2048, I = 768 (576) 31.6 and 29.6; 2 of 8
-// experts, H = 4096, I = 14336: 128 tokens (768) 304, with 2 x 4 waves 319, 80 tokens
-// (576) 259 and 249, 12 tokens (288) 193 and 139, with 2 x 2 waves 154 (three parts of h
-// for 16 rows leave no LDS for 2 x 4).
-template <int PARTS>
+// Down, by workgroups of 4 x 1 waves, 2 x 2 and 2 x 4, whole layer, us.  16 tokens, 6 of 64
+// experts, H = 5120, I = 1280 (2800 of 4 x 1): 104.4 by the first, 106.5 by the second.
+// 2 of 8 experts, H = 4096, I = 14336: 128 tokens (768) 337 by the first; 80 tokens (576)
+// 293 by the second, 274 by the third; 12 tokens (288) 169 and 147.  H = 1024: 24 tokens,
+// 2 of 8, I = 1024 24.5 and 23.4; 16 tokens, 4 of 64, I = 512 23.5 and 25.1; H = 2048,
+// 16 tokens, 4 of 32, I = 768 32.6 and 33.5.
+template <Hidden F>
 void launch_down(const MoeArgs& a, hipStream_t s) {
     if ((int64_t)a.max_slots * ((a.H + 127) / 128) >= 640)
-        launch_expert<false, PARTS, 2, 4, 1, 1, 1>(a, s);
-    else if (PARTS == 2 && a.I >= 4096)
-        launch_expert<false, 2, 2, 2, 4, 1, 1>(a, s);
+        launch_expert<false, F, 2, 4, 1, 1, 1>(a, s);
+    else if (a.I >= 1024)
+        launch_expert<false, F, 2, 2, 4, 1, 1>(a, s);
     else
-        launch_expert<false, PARTS, 2, 2, 2, 1, 1>(a, s);
+        launch_expert<false, F, 2, 2, 2, 1, 1>(a, s);
 }
 
 template <int EV>
 void launch_up_one(const MoeArgs& a, hipStream_t s) {
     constexpr int WN = 1, KW = 4, UG = 4;   // (1, 8, 2): 12.9 against 12.1 us at H = 5120, I = 1280
-    using X = Expert<true, 1, 2, WN, KW, UG, UG>;
+    using X = Expert<true, 2, WN, KW, UG, UG>;
     const int blocks = (a.I / 16 + WN - 1) / WN;
     const dim3 grid((unsigned)(a.top_k * blocks), (unsigned)a.T);
     hipLaunchKernelGGL((up_one_kernel<EV, WN, KW, UG>), grid, dim3(X::kThreads), X::lds(4), s, a,
                        blocks);
 }
 
-template <int PARTS, int WN, int KW, int UG>
+template <Hidden F, int WN, int KW, int UG>
 void launch_down_one(const MoeArgs& a, hipStream_t s) {
-    using X = One<PARTS, WN, KW, UG>;
+    using X = One<WN, KW, UG>;
     static_assert(X::lds() <= 65536, "more LDS than a launch gets without asking");
-    hipLaunchKernelGGL((down_one_kernel<PARTS, WN, KW, UG>),
+    hipLaunchKernelGGL((down_one_kernel<F, WN, KW, UG>),
                        dim3((unsigned)((a.H / 16 + WN - 1) / WN), (unsigned)a.T),
                        dim3(X::kThreads), X::lds(), s, a);
 }
@@ -752,7 +868,7 @@ size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t t
     const int64_t pairs = T * top_k;
     const size_t slots = (size_t)max_slots(T, H, I, E, top_k) * kSlotWords * 4;
     return up256(slots) + 2 * up256((size_t)pairs * 4) + up256((size_t)pairs * H * 4) +
-           (size_t)(y_f32 ? 3 : 2) * pairs * I * 2;
+           (size_t)pairs * I * (y_f32 ? 6 : 4);
 }
 
 hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
@@ -767,7 +883,7 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     p += up256((size_t)pairs * 4);
     a.out = reinterpret_cast<float*>(p);
     p += up256((size_t)pairs * a.H * 4);
-    a.h = reinterpret_cast<uint16_t*>(p);
+    a.h = p;
 
     const int ev = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : 16;
     if (one_by_one(a.T, a.H, a.I, a.E, a.top_k)) {
@@ -778,9 +894,9 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
             default: launch_up_one<16>(a, s);
         }
         if (a.y_f32)
-            launch_down_one<3, 1, 8, 2>(a, s);
+            launch_down_one<kParts, 1, 8, 2>(a, s);
         else
-            launch_down_one<2, 1, 8, 2>(a, s);
+            launch_down_one<kF32, 1, 8, 2>(a, s);
         return hipGetLastError();
     }
     switch (ev) {
@@ -791,9 +907,9 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     }
     launch_up(a, s);
     if (a.y_f32)
-        launch_down<3>(a, s);
+        launch_down<kParts>(a, s);
     else
-        launch_down<2>(a, s);
+        launch_down<kF32>(a, s);
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)((a.H + 1023) / 1024), (unsigned)a.T), dim3(256),
                        0, s, a);
     return hipGetLastError();
