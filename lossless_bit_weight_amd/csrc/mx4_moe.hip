@@ -514,14 +514,15 @@ __device__ __forceinline__ void expert_body(const MoeArgs& a, const int* slot, i
                 static_cast<float*>(a.h)[at_h] = h;
                 continue;
             }
-            // h = the sum of three BF16 numbers, each the rounded rest of those before
+            // the parts as Values::take has them (rounded to nearest, the first of the
+            // largest finite numbers would be infinite)
             uint16_t* o = static_cast<uint16_t*>(a.h) + at_h;
             float rest = h;
+#pragma unroll
             for (int p = 0; p < 3; ++p) {
-                const uint16_t b = bf16_bits(rest);
-                o[p * pairs * a.I] = b;
-                const float f = __uint_as_float((uint32_t)b << 16);
-                rest = __builtin_isfinite(f) ? rest - f : 0.f;
+                const uint32_t b = __float_as_uint(rest);
+                o[p * pairs * a.I] = (uint16_t)(b >> 16);
+                rest = __builtin_isinf(rest) ? 0.f : rest - __uint_as_float(b & 0xFFFF0000u);
             }
         } else {
             const int at = col / 16 * 256 + in;

@@ -80,3 +80,53 @@ def test_hidden_values_keep_24_bits(T, H, I, E, out):
     y = mx4.mx4_moe(_dev(x), torch.from_numpy(logits).cuda(), mx4.mx4_quantize(_dev(w13)),
                     mx4.mx4_quantize(_dev(w2)), 1, out_dtype=TYPES[out])
     _assert_equal(y, want, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,I,E", [(1, 64, 96, 2), (40, 64, 96, 24), (40, 96, 1056, 2)])
+def test_hidden_values_at_the_top_of_fp32(T, H, I, E, out):
+    """Hidden values within 2^-9 of the largest fp32 number, which no BF16 holds: finite,
+    so their products with small weights are too."""
+    digits = np.array(np.meshgrid(*[[1, 2, 3, 4, 6]] * 4)).reshape(4, -1).T
+    value = digits @ 8 ** np.arange(4)
+    product = np.outer(value, value)
+    pairs = np.argwhere((product >= (1 << 22) - (1 << 13)) & (product < 1 << 22))
+    rng = np.random.default_rng(T)
+    pick = pairs[rng.integers(0, len(pairs), (E, I))]
+    w13 = np.zeros((E, 2 * I, H))
+    sign = rng.choice([-1.0, 1.0], (E, I))
+    w13[:, :I, :4], w13[:, I:, :4] = digits[pick[..., 0]], sign[..., None] * digits[pick[..., 1]]
+    x = np.zeros((T, H))
+    x[:, :4] = 8.0 ** np.arange(4) * 2.0 ** 53
+    w2 = np.zeros((E, H, I))
+    at = rng.integers(0, I, (E, H))
+    np.put_along_axis(w2, at[..., None], 2.0 ** -100, axis=2)
+    for w in (w13, w2):
+        assert np.array_equal(ref.rounded(w), w)
+    expert = rng.integers(0, E, T)
+    logits = np.zeros((T, E), np.float32)
+    logits[np.arange(T), expert] = 9.0
+    h = sign * product[pick[..., 0], pick[..., 1]] * 2.0 ** 106
+    assert np.abs(h).max() <= np.finfo(np.float32).max
+    want = (np.take_along_axis(h, at, 1) * 2.0 ** -100)[expert]
+    y = mx4.mx4_moe(_dev(x), torch.from_numpy(logits).cuda(), mx4.mx4_quantize(_dev(w13)),
+                    mx4.mx4_quantize(_dev(w2)), 1, out_dtype=TYPES[out])
+    _assert_equal(y, want, out)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("T,I,E", [(1, 96, 2), (40, 96, 24), (40, 1056, 2)])
+def test_infinite_hidden_value(T, I, E, out):
+    """g u past fp32's range: its products are infinite, with the weight's sign."""
+    H = 64
+    w13 = np.zeros((E, 2 * I, H))
+    w13[:, 5, 0] = w13[:, I + 5, 0] = 4.0
+    x = np.zeros((T, H))
+    x[:, 0] = 2.0 ** 70
+    w2 = np.random.default_rng(T).choice([-2.0, 1.0], (E, H, I))
+    expert = np.arange(T) % E
+    logits = np.zeros((T, E), np.float32)
+    logits[np.arange(T), expert] = 9.0
+    y = mx4.mx4_moe(_dev(x), torch.from_numpy(logits).cuda(), mx4.mx4_quantize(_dev(w13)),
+                    mx4.mx4_quantize(_dev(w2)), 1, out_dtype=TYPES[out])
+    assert np.array_equal(y.float().cpu().numpy(), w2[expert][:, :, 5] * np.inf)
