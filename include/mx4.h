@@ -85,7 +85,9 @@ int mx4_quantize(const void *x, int x_type, int64_t B, int64_t R, int64_t K,
  * mx4_dequantize -- container -> y [B, R, K], the values it stands for: exact
  * in fp32 and in BF16 for every scale that mx4_quantize writes.
  *   y : device output, BF16 bits or fp32 as y_type says; strides and alignment
- *       as mx4_quantize's x.
+ *       as mx4_quantize's x.  Its matrices share no value: they lie one behind
+ *       the other (ldb >= (R - 1) * ldy + K) or between each other's rows
+ *       (ldb >= K, ldy >= (B - 1) * ldb + K).
  * Errors as mx4_quantize.
  */
 int mx4_dequantize(const void *codes, const void *scales, int64_t B, int64_t R, int64_t K,

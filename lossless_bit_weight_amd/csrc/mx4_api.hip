@@ -42,6 +42,13 @@ int check_rows(const void* p, int type, int64_t B, int64_t K, int64_t ld, int64_
     return W12_OK;
 }
 
+// B matrices of R rows that share no value: one behind the other, or all of them
+// between two rows of one (matrices that overlap would be written twice)
+bool apart(int64_t B, int64_t R, int64_t K, int64_t ld, int64_t ldb) {
+    if (ldb < K) return false;
+    return (ldb - K) / ld >= R - 1 || (ld - K) / ldb >= B - 1;      // ld >= K >= 1
+}
+
 int check_y(const void* y, int64_t N, int64_t ldy, int y_type) {
     if (type_bytes(y_type) == 0) return W12_ERR_DTYPE;
     if (ldy < N || ldy >= kMaxElems) return W12_ERR_SHAPE;
@@ -99,7 +106,7 @@ const char* mx4_status_string(int status) {
         case W12_ERR_NULL: return "a required pointer is NULL";
         case W12_ERR_SHAPE:
             return "bad shape (K and I are positive multiples of 32 below 2^24, N >= 1, row "
-                   "strides cover their rows, 1 <= top_k <= E)";
+                   "strides cover their rows, an output's matrices lie apart, 1 <= top_k <= E)";
         case W12_ERR_ALIGN:
             return "misaligned pointer or stride (16-byte rows of x, containers and decoded rows)";
         case W12_ERR_DTYPE: return "unknown element type";
@@ -142,9 +149,8 @@ int mx4_dequantize(const void* codes, const void* scales, int64_t B, int64_t R, 
     if (R > 0 && (!y || !codes || !scales)) return W12_ERR_NULL;
     if (int rc = check_rows(y, y_type, B, K, ldy, ldb)) return rc;
     if (!aligned(codes, 16) || !aligned(scales, 16)) return W12_ERR_ALIGN;
-    // matrices of y that overlap would be written twice
-    if (B > 1 && ldb < (R - 1) * ldy + K) return W12_ERR_SHAPE;
     if (R == 0) return W12_OK;
+    if (B > 1 && !apart(B, R, K, ldy, ldb)) return W12_ERR_SHAPE;
     return status_of(mx4::launch_dequantize(mat(codes, scales), B, R, K, y, y_type == W12_OUT_F32,
                                             ldy, ldb, static_cast<hipStream_t>(stream)));
 }

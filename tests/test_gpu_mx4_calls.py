@@ -1,0 +1,44 @@
+"""Calls of the MX4 operators that the documentation allows: views as outputs, one
+container in several calls at once."""
+import numpy as np
+import pytest
+import torch
+
+from lossless_bit_weight_amd import mx4
+from tests import mx4_ref as ref
+from tests.gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _values(shape, seed, sigma=1.0):
+    """BF16-exact normal values in float64."""
+    v = np.random.default_rng(seed).standard_normal(shape) * sigma
+    return ref.bf16_to_f64(ref.f64_to_bf16_bits(v))
+
+
+def _dev(v, dtype=torch.bfloat16):
+    return torch.from_numpy(np.ascontiguousarray(v).astype(np.float32)).cuda().to(dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,R,K", [(2, 1, 32), (3, 20, 160), (5, 33, 544), (1, 17, 64)])
+def test_codec_interleaved_matrices(B, R, K, dtype):
+    """Matrices whose rows lie between each other's: [R, B, K] memory seen as [B, R, K]."""
+    v = _values((R, B, K + 8), B + R + K)
+    rows = _dev(v, TYPES[dtype])
+    x = rows[:, :, :K].transpose(0, 1)
+    q = mx4.mx4_quantize(x)
+    want = ref.rounded(v[:, :, :K])
+    rows.fill_(7.0)
+    assert mx4.mx4_dequantize(q, out=x) is x
+    full = np.full(v.shape, 7.0)
+    full[:, :, :K] = want
+    assert np.array_equal(rows.float().cpu().numpy().astype(np.float64), full)

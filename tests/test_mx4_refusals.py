@@ -1,0 +1,21 @@
+"""What the MX4 calls refuse at the edges of their limits, without a GPU."""
+import ctypes
+
+import pytest
+
+from lossless_bit_weight_amd import mx4
+
+A = ctypes.c_void_p(4096)       # never dereferenced: every call here fails validation
+
+
+@pytest.mark.parametrize("B,R,K,ldy,ldb", [
+    (2, 16, 64, 64, 512),           # the second starts inside the first
+    (3, 4, 64, 128, 64),            # room between rows for one more matrix, not for two
+    (2, 4, 64, 96, 64), (2, 4, 64, 128, 32),
+    (2, 1 << 30, 64, 1 << 39, 32)])  # rows times stride past 2^63
+def test_dequantize_refuses_matrices_that_overlap(B, R, K, ldy, ldb):
+    assert mx4.lib().mx4_dequantize(A, A, B, R, K, A, 0, ldy, ldb, None) == -2
+
+
+def test_dequantize_of_zero_rows_needs_no_strides():
+    assert mx4.lib().mx4_dequantize(None, None, 3, 0, 64, None, 0, 64, 0, None) == 0
