@@ -98,13 +98,15 @@ int mx4_dequantize(const void *codes, const void *scales, int64_t B, int64_t R, 
  * x BF16; any M.  The weights are expanded to BF16 (exactly) in registers, the
  * sums are fp32.
  *   x  : device BF16 [M, K], row stride ldx elements (ldx >= K, ldx % 8 == 0),
- *        16-byte aligned.
+ *        16-byte aligned.  With ldx >= 2^23 and many rows the weights are
+ *        read once for every 16 of them (copy such rows together first).
  *   y  : device output [M, N], row stride ldy >= N, BF16 bits (2-byte aligned)
  *        or fp32 (4-byte aligned) as y_type says.
  *   workspace : mx4_gemm_workspace_bytes(M, N, K, 0) bytes; NULL if that is 0.
- * Errors: W12_ERR_NULL, W12_ERR_SHAPE (N < 1, N > 2^27, M < 0, M > 2^24 or
- *         M*N > 2^37 beside those of the sizes), W12_ERR_ALIGN, W12_ERR_DTYPE,
- *         W12_ERR_WORKSPACE, W12_ERR_HIP.
+ * Errors: W12_ERR_NULL, W12_ERR_SHAPE (N < 1, N > 2^27, M < 0, M > 2^24,
+ *         M*N > 2^37 or ldx >= 2^23 with M > 16 * 65535, beside those of the
+ *         sizes), W12_ERR_ALIGN, W12_ERR_DTYPE, W12_ERR_WORKSPACE,
+ *         W12_ERR_HIP.
  */
 int mx4_gemm(const uint16_t *x, int64_t M, int64_t ldx, const void *w_codes,
              const void *w_scales, int64_t N, int64_t K, void *y, int64_t ldy, int y_type,

@@ -169,6 +169,7 @@ int mx4_gemm(const uint16_t* x, int64_t M, int64_t ldx, const void* w_codes, con
     if (!w_codes || !w_scales || (M > 0 && (!x || !y))) return W12_ERR_NULL;
     if (int rc = check_gemm_shape(M, N, K)) return rc;
     if (int rc = check_rows(x, W12_OUT_BF16, 1, K, ldx, 0)) return rc;
+    if (ldx >= mx4::kFarRows && M > mx4::kMaxFarRows) return W12_ERR_SHAPE;
     return gemm(x, ldx, mx4::Mat{}, M, mat(w_codes, w_scales), N, K, y, ldy, y_type, workspace,
                 workspace_bytes, stream);
 }

@@ -142,25 +142,12 @@ __global__ __launch_bounds__(KW * 64) void small_kernel(GemmArgs a) {
 }
 
 template <int R, int KW, int D, bool XM>
-hipError_t launch_small(GemmArgs a, hipStream_t s) {
-    const unsigned nb = (unsigned)((tiles(a.N) + R - 1) / R);
-    const int M = a.M;
-    const int most = 65535 * 16;            // rows one grid covers
-    for (int m = 0; m < M; m += most) {
-        a.M = M - m < most ? M - m : most;
-        const dim3 grid(nb, (unsigned)tiles(a.M)), block(KW * 64);
-        if (!XM && a.K % kGroup != 0)
-            hipLaunchKernelGGL((small_kernel<R, KW, D, XM, !XM>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((small_kernel<R, KW, D, XM, false>), grid, block, 0, s, a);
-        if (XM) {
-            a.xm.codes += (int64_t)65535 * a.G * kCodeBlock;
-            a.xm.scales += (int64_t)65535 * a.Q * kScaleBlock;
-        } else {
-            a.x += (int64_t)most * a.ldx;
-        }
-        a.y = static_cast<uint8_t*>(a.y) + (int64_t)most * a.ldy * (a.y_f32 ? 4 : 2);
-    }
+hipError_t launch_small(const GemmArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)((tiles(a.N) + R - 1) / R), (unsigned)tiles(a.M)), block(KW * 64);
+    if (!XM && a.K % kGroup != 0)
+        hipLaunchKernelGGL((small_kernel<R, KW, D, XM, !XM>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((small_kernel<R, KW, D, XM, false>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
@@ -904,8 +891,7 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     a.gs = p.gs;
     a.part = static_cast<float*>(ws);
     Kernel k = p.kernel;
-    // the tile kernel's row offsets are products of 24-bit numbers
-    if (!xm && k >= kTileSmall && a.ldx >= (1 << 23)) k = kSmall;
+    if (!xm && k >= kTileSmall && a.ldx >= kFarRows) k = kSmall;
     if (k == kSmall) a.S = 1;
     if (xm) switch (k) {
         case kMid16x2: return launch_mid<16, 2, 2, 4, true>(a, s);

@@ -126,6 +126,10 @@ hipError_t launch_quantize(const void* x, int x_f32, int64_t B, int64_t R, int64
                            int64_t ldb, uint8_t* codes, uint8_t* scales, hipStream_t s);
 hipError_t launch_dequantize(Mat m, int64_t B, int64_t R, int64_t K, void* y, int y_f32,
                              int64_t ldy, int64_t ldb, hipStream_t s);
+// Rows of x this far apart are past the tile kernel's row offsets, which are products of
+// 24-bit numbers: the few-row kernel takes them, up to kMaxFarRows (its grid's y).
+constexpr int64_t kFarRows = (int64_t)1 << 23;
+constexpr int64_t kMaxFarRows = 65535 * 16;
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, bool x_mx4);
 hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s);
 

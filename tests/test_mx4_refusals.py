@@ -19,3 +19,9 @@ def test_dequantize_refuses_matrices_that_overlap(B, R, K, ldy, ldb):
 
 def test_dequantize_of_zero_rows_needs_no_strides():
     assert mx4.lib().mx4_dequantize(None, None, 3, 0, 64, None, 0, 64, 0, None) == 0
+
+
+@pytest.mark.parametrize("M,ldx,status", [(1 << 20, 1 << 23, -2), (1 << 24, 1 << 23, -2)])
+def test_gemm_refuses_many_rows_far_apart(M, ldx, status):
+    """Rows 2^23 elements apart and more go to the few-row kernel, up to 16 * 65535 of them."""
+    assert mx4.lib().mx4_gemm(A, M, ldx, A, A, 32, 64, A, 32, 0, None, 0, None) == status
