@@ -155,7 +155,8 @@ struct MoeArgs {
     int64_t ldy;
     int y_f32;
     int max_slots;          // min(E, pairs) + pairs / 16, or pairs
-    // workspace: the pairs in the order of (expert, token), cut into slots
+    // workspace: the pairs in the order of (expert, token), cut into slots (tokens one by
+    // one: slots and h only)
     int* slots;             // [max_slots][kSlotWords]
     int* place;             // [T][top_k] place of token t's j-th pair, or -1
     float* share;           // [T][top_k]

@@ -867,9 +867,10 @@ void launch_route(const MoeArgs& a, hipStream_t s) {
 
 size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bool y_f32) {
     const int64_t pairs = T * top_k;
-    const size_t slots = (size_t)max_slots(T, H, I, E, top_k) * kSlotWords * 4;
-    return up256(slots) + 2 * up256((size_t)pairs * 4) + up256((size_t)pairs * H * 4) +
-           (size_t)pairs * I * (y_f32 ? 6 : 4);
+    const size_t slots = up256((size_t)max_slots(T, H, I, E, top_k) * kSlotWords * 4);
+    const size_t h = (size_t)pairs * I * (y_f32 ? 6 : 4);
+    if (one_by_one(T, H, I, E, top_k)) return slots + h;
+    return slots + 2 * up256((size_t)pairs * 4) + up256((size_t)pairs * H * 4) + h;
 }
 
 hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
@@ -878,12 +879,6 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     uint8_t* p = static_cast<uint8_t*>(ws);
     a.slots = reinterpret_cast<int*>(p);
     p += up256((size_t)a.max_slots * kSlotWords * 4);
-    a.place = reinterpret_cast<int*>(p);
-    p += up256((size_t)pairs * 4);
-    a.share = reinterpret_cast<float*>(p);
-    p += up256((size_t)pairs * 4);
-    a.out = reinterpret_cast<float*>(p);
-    p += up256((size_t)pairs * a.H * 4);
     a.h = p;
 
     const int ev = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : 16;
@@ -900,6 +895,13 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
             launch_down_one<kF32, 1, 8, 2>(a, s);
         return hipGetLastError();
     }
+    a.place = reinterpret_cast<int*>(p);
+    p += up256((size_t)pairs * 4);
+    a.share = reinterpret_cast<float*>(p);
+    p += up256((size_t)pairs * 4);
+    a.out = reinterpret_cast<float*>(p);
+    p += up256((size_t)pairs * a.H * 4);
+    a.h = p;
     switch (ev) {
         case 1: launch_route<1>(a, s); break;
         case 2: launch_route<2>(a, s); break;

@@ -42,3 +42,23 @@ def test_codec_interleaved_matrices(B, R, K, dtype):
     full = np.full(v.shape, 7.0)
     full[:, :, :K] = want
     assert np.array_equal(rows.float().cpu().numpy().astype(np.float64), full)
+
+
+def _moe(T, H, I, E, seed):
+    logits = torch.from_numpy(np.random.default_rng(seed).standard_normal((T, E))
+                              .astype(np.float32)).cuda()
+    return (_dev(_values((T, H), seed + 1)), logits,
+            mx4.mx4_quantize(_dev(_values((E, 2 * I, H), seed + 2, 0.05))),
+            mx4.mx4_quantize(_dev(_values((E, H, I), seed + 3, 0.05))))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 160, 96, 9, 4), (32, 64, 32, 20, 3), (40, 96, 64, 12, 5),
+                                       (128, 64, 96, 5, 5)])
+def test_moe_stays_within_its_workspace(T, H, I, E, k, out):
+    x, logits, w13, w2 = _moe(T, H, I, E, 7)
+    need = mx4.mx4_moe_workspace_bytes(T, H, I, E, k, TYPES[out])
+    room = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    y = mx4.mx4_moe(x, logits, w13, w2, k, out_dtype=TYPES[out], workspace=room[:need])
+    assert bool((room[need:] == 0xA5).all())
+    assert torch.equal(y, mx4.mx4_moe(x, logits, w13, w2, k, out_dtype=TYPES[out]))

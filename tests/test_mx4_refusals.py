@@ -1,7 +1,8 @@
-"""What the MX4 calls refuse at the edges of their limits, without a GPU."""
+"""What the MX4 calls ask for, and refuse at the edges of their limits, without a GPU."""
 import ctypes
 
 import pytest
+import torch
 
 from lossless_bit_weight_amd import mx4
 
@@ -25,3 +26,12 @@ def test_dequantize_of_zero_rows_needs_no_strides():
 def test_gemm_refuses_many_rows_far_apart(M, ldx, status):
     """Rows 2^23 elements apart and more go to the few-row kernel, up to 16 * 65535 of them."""
     assert mx4.lib().mx4_gemm(A, M, ldx, A, A, 32, 64, A, 32, 0, None, 0, None) == status
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(1, 5120, 1280, 64, 6), (2, 2048, 768, 128, 8)])
+def test_moe_workspace_of_tokens_one_by_one(T, H, I, E, k):
+    """Tokens that go one by one need their pairs' words and hidden values, no outputs of
+    pairs and no places."""
+    for dtype, size in ((torch.bfloat16, 4), (torch.float32, 6)):
+        need = mx4.mx4_moe_workspace_bytes(T, H, I, E, k, dtype)
+        assert T * k * (I * size + 16) <= need <= T * k * (I * size + 128) + 256
