@@ -8,6 +8,7 @@ import torch
 from lossless_bit_weight_amd import mx4
 from tests import mx4_ref as ref
 from tests.gpu_util import require_gpu
+from tests.test_gpu_mx4 import GEMM_KERNELS, GEMM_SHAPES
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +131,35 @@ def test_infinite_hidden_value(T, I, E, out):
     y = mx4.mx4_moe(_dev(x), torch.from_numpy(logits).cuda(), mx4.mx4_quantize(_dev(w13)),
                     mx4.mx4_quantize(_dev(w2)), 1, out_dtype=TYPES[out])
     assert np.array_equal(y.float().cpu().numpy(), w2[expert][:, :, 5] * np.inf)
+
+
+# ---- products ------------------------------------------------------------------------
+
+def _whole(shape, seed):
+    """Whole numbers from -2 to 2: MX4 holds them, and a sum of fewer than 2^22 products
+    of two is exact in fp32 in any order."""
+    return np.random.default_rng(seed).integers(-2, 3, shape).astype(np.float64)
+
+
+# past the lengths that one slice, one wave or one unit of a kernel takes
+LONG = [(M, N, 65536) for M in (1, 3, 11, 16) for N in (70, 2600)] + [
+    (27, 300, 65536), (40, 300, 65536), (64, 2600, 65536), (100, 300, 65536), (200, 520, 65536),
+    (2, 16400, 20000), (13, 16400, 20000), (27, 16400, 20000), (50, 16400, 20000),
+    (300, 1000, 20000)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMM_SHAPES + GEMM_KERNELS + LONG)
+def test_products_of_whole_numbers(M, N, K):
+    """Every kernel, every cut of K: no group of K may be left out, taken twice or met by
+    another one's scale."""
+    K -= K % 32
+    x, w = _whole((M, K), M + K), _whole((N, K), N + K + 1)
+    for k in range(0, K, 32):                  # scales of their own for every block of K
+        s = 2.0 ** (k // 32 % 3)
+        x[:, k:k + 32] *= s
+        w[:, k:k + 32] /= s
+    want = (torch.from_numpy(x).cuda() @ torch.from_numpy(w).cuda().T).cpu().numpy()
+    xd, wq = _dev(x), mx4.mx4_quantize(_dev(w))
+    for a in (xd, mx4.mx4_quantize(xd)):
+        for out in TYPES:
+            _assert_equal(mx4.mx4_gemm(a, wq, out_dtype=TYPES[out]), want, out)
