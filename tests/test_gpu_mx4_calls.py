@@ -62,3 +62,40 @@ def test_moe_stays_within_its_workspace(T, H, I, E, k, out):
     y = mx4.mx4_moe(x, logits, w13, w2, k, out_dtype=TYPES[out], workspace=room[:need])
     assert bool((room[need:] == 0xA5).all())
     assert torch.equal(y, mx4.mx4_moe(x, logits, w13, w2, k, out_dtype=TYPES[out]))
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1000, 512), (40, 300, 17408), (200, 3000, 160)])
+def test_one_weight_in_two_products_at_once(M, N, K):
+    """Two streams, one container, workspaces of their own: every result is the eager one."""
+    wq = mx4.mx4_quantize(_dev(_values((N, K), 1, 0.02)))
+    xs = [_dev(_values((M, K), 2 + i)) for i in range(2)]
+    want = [(mx4.mx4_gemm(x, wq), mx4.mx4_gemm(mx4.mx4_quantize(x), wq)) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((mx4.mx4_gemm(xs[i], wq),
+                               mx4.mx4_gemm(mx4.mx4_quantize(xs[i]), wq)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y in got[i]:
+            assert torch.equal(y[0], want[i][0]) and torch.equal(y[1], want[i][1])
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(2, 160, 96, 9, 4), (40, 96, 1056, 12, 5)])
+def test_one_expert_weight_in_two_layers_at_once(T, H, I, E, k):
+    _, _, w13, w2 = _moe(T, H, I, E, 20)
+    xs = [_moe(T, H, I, E, 30 + i)[:2] for i in range(2)]
+    want = [mx4.mx4_moe(x, l, w13, w2, k) for x, l in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mx4.mx4_moe(*xs[i], w13, w2, k))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
