@@ -35,3 +35,17 @@ def test_moe_workspace_of_tokens_one_by_one(T, H, I, E, k):
     for dtype, size in ((torch.bfloat16, 4), (torch.float32, 6)):
         need = mx4.mx4_moe_workspace_bytes(T, H, I, E, k, dtype)
         assert T * k * (I * size + 16) <= need <= T * k * (I * size + 128) + 256
+
+
+@pytest.mark.parametrize("x_mx4", [False, True])
+def test_gemm_that_splits_k_refuses_a_bad_workspace(x_mx4):
+    M, N, K = 33, 512, 17408
+    need = mx4.mx4_gemm_workspace_bytes(M, N, K, x_mx4)
+    assert need >= 2 * M * N * 4                # two slices' sums at least
+    L = mx4.lib()
+    for ws, n in ((None, need), (A, need - 1), (A, 0), (ctypes.c_void_p(4096 + 16), need)):
+        if x_mx4:
+            rc = L.mx4_gemm_mx4(A, A, M, A, A, N, K, A, N, 0, ws, n, None)
+        else:
+            rc = L.mx4_gemm(A, M, K, A, A, N, K, A, N, 0, ws, n, None)
+        assert rc == -8
