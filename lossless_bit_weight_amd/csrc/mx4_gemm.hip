@@ -158,8 +158,8 @@ hipError_t launch_small(const GemmArgs& a, hipStream_t s) {
 // double-buffered, where the WN waves share it: with every wave reading x for
 // itself, the caches deliver as many bytes of x as of weights (gate+up M = 16:
 // 29.2 us there, 27.1 here; with x's reads left out, 18).  LDS row m of a
-// group holds x's 16 pieces of 8 values, piece p at place p ^ (m % 16), so that
-// the rows one read takes a piece from lie in 16 different places.  From 16
+// group holds x's 16 pieces of 8 values, piece p at x_place(p, m), so that
+// the rows one read takes a piece from lie in different places.  From 16
 // rows on the weights are read through the caches: row blocks share them, and the
 // weights of a small model stay in the last of them (gate+up M = 16 over 190 MB of
 // weights 19.6 us, past the caches 20.8; over 760 MB 24.2 and 23.1).
@@ -380,8 +380,8 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
 // ahead, or two (DEEP) where the sums leave the registers for it.  64 x 128 tiles,
 // us, one group ahead / two: gate+up M = 128 71 / 58, MX4 x 37.4 / 30.5; 128 x 256
 // tiles of MX4 x, QKV M = 4096, 90.9 / 87.9.
-// BF16 x: LDS row m holds 16 pieces of 8 values, piece p at place p ^ (m % 16),
-// so that the 16 rows a read takes one piece from lie in 16 different places.
+// BF16 x: LDS row m holds 16 pieces of 8 values, piece p at x_place(p, m), so that
+// the rows a read takes one piece from lie in different places.
 // MX4 x: its own blocks, in lane order.
 // Steps run over whole quads of groups, as the scales do: a group past the last
 // has zeros for x in LDS, the last weight block and its padding scale.
@@ -788,6 +788,9 @@ int spread(int64_t nt, bool few_rows) {
 //   17 to 32 and many tiles: 32 rows, waves as spread() says (MX4 x: four), unless BF16
 //     tiles of 32 x 256 nearly fill the GPU (gate+up M = 32, 136 of them, 37.2, by waves
 //     29.8; N = 65536 on K = 2048, 256 of them, 20.0 and 26.8).
+//   33 to 64 and many tiles: the tiles below, BF16 x 64 x 256 from about one a CU on, else
+//     32 x 256 (K = 5120, M = 64: N = 65536 53.5, 32 rows by two tiles a wave 72.1; N = 50000
+//     51.4 and 65.0, N = 34816 42.3 and 41.7, N = 20480 31.4 and 35.7).
 //   above: 128 x 256 if that gives 440 workgroups (QKV M = 2048 115, 64 x 256 125.5);
 //     else, BF16 x, 64 x 256 if that gives 440 (QKV M = 1024 64.9, 128 x 256 75.5) or
 //     nearly one a CU (QKV M = 512 39.2, 128 x 256 51.7), then 32 x 256 (QKV M = 256

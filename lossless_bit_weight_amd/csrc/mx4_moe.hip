@@ -1,11 +1,11 @@
 // mx4_moe.hip -- a mixture-of-experts layer for a few tokens on MX4 weights
 // (../../include/mx4.h states the operation).
 //
-// Four launches.  route: each token's experts and their shares, and the pairs
-// (token, expert) sorted by expert and cut into slots of at most 16.  up: per
-// slot the products with the gate and up rows and h = silu(g) * u.  down: per
+// Up to 16 tokens four launches.  route: each token's experts and their shares, and
+// the pairs (token, expert) sorted by expert and cut into slots of at most 16.  up:
+// per slot the products with the gate and up rows and h = silu(g) * u.  down: per
 // slot the products of h with the down rows.  join: each token's weighted sum.
-// Above 16 tokens a launch before route chooses the experts.  One token, and few
+// Above, a fifth before them (choose): the experts of each token.  One token, and few
 // that would seldom share an expert, take two launches: up, where a token chooses
 // for itself, and down over all its experts, which writes y.
 // The chosen experts' weights are read once (an expert with more than 16 tokens:
@@ -304,8 +304,8 @@ constexpr int values_each(int pieces, int threads) {
 // the slot's rows (of x, gathered by token, or of h in PARTS parts) go through
 // LDS, double-buffered, in the layout of mx4_gemm.hip's few-row kernel, ROWS of
 // them: slots of up to four rows, the most by far, move a quarter of the bytes, and
-// read weights that no other slot does (16 tokens 106 us past the caches, 116
-// through them; 128 tokens at 16 an expert the reverse, 109 and 102).
+// read weights that no other slot does (H = 5120, I = 1280: 16 tokens, 6 of 64 experts
+// 105 us past the caches, 117 through them; 128 tokens, 8 of 64 the reverse, 209 and 199).
 template <bool UP, int R, int WN, int KW, int UG4, int UG16>
 struct Expert {
     static constexpr int PARTS = UP ? 1 : 3;
@@ -776,11 +776,11 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Each token by itself, weights that several of them chose read again: two launches
 // instead of four, at the cost of the repeated bytes.  Whole layer, us, so / by slots,
-// and the bytes expected: 2 tokens, 2 of 8 experts, H = 5120, I = 1280 17.6 / 24.4 (5 MB);
-// 4 tokens, 8 of 127, H = 2080, I = 736 31.0 / 32.2 (7 MB); 3 tokens, 6 of 64, H = 4096,
-// I = 1408 41.9 / 42.0 (16 MB); 16 tokens, 4 of 64, H = 1024, I = 512 24.6 / 21.6 (25 MB);
-// 4 tokens, 6 of 64, H = 5120, I = 1280 58.2 / 53.8 (35 MB); 32 tokens, 1 of 22,
-// H = 800, I = 320 16.4 / 18.0 (9 MB), 64, 1 of 64, 26.9 / 20.7 (13 MB).
+// and the bytes expected: 2 tokens, 2 of 8 experts, H = 5120, I = 1280 18.7 / 23.7 (5 MB);
+// 4 tokens, 8 of 127, H = 2080, I = 736 31.3 / 31.6 (7 MB); 3 tokens, 6 of 64, H = 4096,
+// I = 1408 42.0 / 46.8 (16 MB); 16 tokens, 4 of 64, H = 1024, I = 512 26.4 / 23.7 (25 MB);
+// 4 tokens, 6 of 64, H = 5120, I = 1280 58.7 / 55.1 (35 MB); 32 tokens, 1 of 22,
+// H = 800, I = 320 18.4 / 18.8 (9 MB), 64, 1 of 64, 31.1 / 21.8 (13 MB).
 constexpr int kOneByOne = 32;               // tokens
 constexpr int64_t kRepeatedBytes = 16 << 20;
 bool one_by_one(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
@@ -811,9 +811,9 @@ void launch_expert(const MoeArgs& a, hipStream_t s) {
 
 // Waves beside each other share a slot's rows, waves that split K let a few slots fill
 // the GPU.  Up, H = 5120, I = 1280, 12 tokens, 2 of 8 experts (at most 360 workgroups of
-// 2 x 2 waves): whole layer 38.6 us, with 1 x 4 waves 34.2; 48 tokens, 2 of 16 (880):
-// 53.4 and 55.6.  Above four rows a slot units of two groups: 128 tokens, 4 of 16, 94
-// with units of one, 88.
+// 2 x 2 waves): whole layer 38.0 us, with 1 x 4 waves 37.3; 48 tokens, 2 of 16 (880):
+// 57.3 and 61.7.  Above four rows a slot units of two groups: 128 tokens, 4 of 16, 103
+// with units of one, 96.
 void launch_up(const MoeArgs& a, hipStream_t s) {
     if ((int64_t)a.max_slots * ((a.I + 31) / 32) < 512)
         launch_expert<true, kF32, 2, 1, 4, 2, 1>(a, s);
