@@ -249,9 +249,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
 // h goes to the matrix units as three BF16 numbers whose sum it is: all 24 bits of its
 // mantissa, whatever the output's type (two of them would differ from an fp32 product
 // by 2^-16 of h, which differences of hidden values do not hide).  Up stores it whole,
-// 4 bytes that down splits (BF16 outputs), or as its parts, 6 bytes (fp32 outputs).
-// Whole layer, us, BF16 output, whole / parts: H = 2080, I = 736, 61 tokens, 8 of 127
-// experts 86.9 / 89.6; H = 4096, I = 14336, 128 tokens, 2 of 8 337 / 327.
+// 4 bytes that down splits (BF16 outputs, whose workspace stays as small), or as its
+// parts, 6 bytes (fp32 outputs).  Neither is always the faster; whole layer, us, fp32
+// output, whole / parts: 16 tokens, 6 of 64 experts, H = 5120, I = 1280 103.9 / 104.7;
+// 61 tokens, 8 of 127, H = 2080, I = 736 86.2 / 89.2; 128 tokens, 2 of 8, H = 4096,
+// I = 14336 337 / 328.
 enum Hidden { kF32, kParts };
 
 // V values of h (an infinity's rest is 0; a NaN that arithmetic made keeps its quiet bit
