@@ -8,7 +8,7 @@ A case names its operator in "op":
 
   norm     s = x + residual, rounded to the residual's type;
            y = s / sqrt(mean(s^2) + eps) * weight, in BF16, fp32 or MX8 (blocks
-           of 32 along K: E4M3 values under a shared power of two)
+           of 32 along K under a shared power of two: E4M3 values, multiples of 1/4)
   linear8  y = x W^T, W [N, K] in MX4, x [M, K] BF16 quantised to MX8 within the
            pass
   route    a token's experts (the top_k of its scores plus a bias, from the kept
@@ -199,11 +199,11 @@ def _whole(packed):
 def _mx8(x):
     """The values that MX8 holds for x [..., K], in 32 bits: per block of 32 the
     exponent e of its unit, and per value the nearest multiple (ties to even) of
-    its binade's step, an eighth of the binade and at least 2^-9; 448 at most."""
+    its binade's step, an eighth of the binade and at least 1/4; 448 at most."""
     blocks = x.float().unflatten(-1, (-1, BLOCK))
     e = _exponents(blocks, 8)
     t = torch.ldexp(blocks.abs(), -e)
-    step = (torch.frexp(t).exponent - 4).clamp(min=-9)
+    step = (torch.frexp(t).exponent - 4).clamp(min=-2)
     q = torch.ldexp(torch.round(torch.ldexp(t, -step)), step).clamp(max=448.0)
     return torch.copysign(torch.ldexp(q, e), blocks).flatten(-2)
 
@@ -460,7 +460,7 @@ def _held(x, top, steps):
     format's largest binade, `steps` its steps a binade; the smallest binade
     that has its own step starts at 2^low, and what lies past the largest value
     becomes it."""
-    low, most = {2: (0, 6.0), 8: (-6, 448.0)}[top]
+    low, most = {2: (0, 6.0), 8: (1, 448.0)}[top]
     b = x.double().unflatten(-1, (-1, BLOCK))
     big = b.abs().amax(-1, keepdim=True)
     whole = torch.floor(torch.log2(torch.where(big > 0, big, torch.full_like(big, 2.0 ** -126))))
