@@ -25,7 +25,10 @@ SOURCES = [("w12_api.hip", "w12_api", []), ("w12_pack.hip", "w12_pack", []),
            ("w12_exc.hip", "w12_exc", []), ("w12_gemm.hip", "w12_gemm", []),
            ("w12_probe.hip", "w12_probe", []), ("mx4_api.hip", "mx4_api", []),
            ("mx4_codec.hip", "mx4_codec", []), ("mx4_gemm.hip", "mx4_gemm", []),
-           ("mx4_moe.hip", "mx4_moe", [])]
+           ("mx4_moe.hip", "mx4_moe", []), ("mx4_route.hip", "mx4_route", []),
+           ("mx8_api.hip", "mx8_api", []), ("mx8_codec.hip", "mx8_codec", []),
+           ("mx8_norm.hip", "mx8_norm", []), ("mx8_gemm.hip", "mx8_gemm", []),
+           ("draft_api.hip", "draft_api", []), ("draft.hip", "draft", [])]
 SOURCES += [("w12_gemm_inst.hip", "w12_gemv_m%d" % m, ["-DW12_INST_M=%d" % m]) for m in range(1, 9)]
 SOURCES += [("w12_gemm_inst.hip", "w12_mfma", ["-DW12_INST_MFMA"]),
             ("w12_gemm_inst.hip", "w12_mfma8", ["-DW12_INST_MFMA8"]),

@@ -1,0 +1,42 @@
+// draft_internal.hpp -- arguments and launcher of the verification of drafted
+// tokens (../../include/draft.h states the operation).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace draft {
+
+// A chunk of a row: its largest logit (NaN: the chunk holds a NaN or +inf), that
+// one's first word, and the sum of 2^((logit - largest) log2(e) / tau).
+struct Part {
+    double sum;
+    float top;
+    int word;
+};
+
+struct Args {
+    const void* logits;
+    int f32;
+    int B, D, V;
+    int64_t ldb, ldd;
+    const void* drafts;
+    int drafts_i64;
+    const float* uniforms;
+    const void* probs;
+    int probs_f32;
+    int64_t pdb, pdd;
+    const int* lengths;
+    const float* temperature;
+    int* tokens;
+    int* accepted;
+    int size, chunks;       // words of a chunk, chunks a row
+    // workspace
+    Part* parts;            // [B (D + 1)][chunks]
+    double* rest;           // [B][chunks] with probs: sums of max(0, p - q)
+};
+
+size_t workspace_bytes(int64_t B, int64_t D, int64_t V);
+hipError_t launch_verify(Args a, void* ws, hipStream_t s);
+
+}  // namespace draft

@@ -1,0 +1,26 @@
+// exp64.hpp -- 2^t in 64 bits on the device.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+// t = n + f with n the nearest whole number, and 2^f = sum of (f ln 2)^k / k! up to
+// k = 11, whose remainder at |f| = 1/2 is 6.3e-15 relative.  Below -1100 it is 0, above
+// 1100 infinite; a NaN counts as -1100.
+__device__ __forceinline__ double exp2_64(double t) {
+    t = __builtin_fmin(__builtin_fmax(t, -1100.0), 1100.0);
+    const double n = __builtin_rint(t), f = t - n;
+    double p = 4.4455382718708116e-10;
+    p = __builtin_fma(p, f, 7.054911620801123e-09);
+    p = __builtin_fma(p, f, 1.01780860092397e-07);
+    p = __builtin_fma(p, f, 1.321548679014431e-06);
+    p = __builtin_fma(p, f, 1.5252733804059841e-05);
+    p = __builtin_fma(p, f, 0.0001540353039338161);
+    p = __builtin_fma(p, f, 0.0013333558146428443);
+    p = __builtin_fma(p, f, 0.009618129107628477);
+    p = __builtin_fma(p, f, 0.05550410866482158);
+    p = __builtin_fma(p, f, 0.24022650695910072);
+    p = __builtin_fma(p, f, 0.6931471805599453);
+    p = __builtin_fma(p, f, 1.0);
+    return __builtin_ldexp(p, (int)n);
+}
+constexpr double kLog2E = 1.4426950408889634;

@@ -1,77 +1,17 @@
-// mx4_api.hip -- the C ABI declared in include/mx4.h: host-side argument checks
-// and launches on the caller's stream.  Nothing here allocates, synchronises or
-// keeps state.
+// mx4_api.hip -- the C ABI declared in include/mx4.h and include/mx4_route.h:
+// host-side argument checks and launches on the caller's stream.  Nothing here
+// allocates, synchronises or keeps state.
 #include <stdint.h>
 
-#include "../../include/mx4.h"
-#include "mx4_internal.hpp"
+#include "../../include/mx4_route.h"
+#include "mx4_checks.hpp"
+
+using namespace mx4;
 
 namespace {
 
-// Padded values of a container: keeps every grid far below 2^31 blocks and
-// every byte offset inside int64.  K below 2^24 keeps group indices and the
-// kernels' in-row offsets in 32 bits.
-constexpr int64_t kMaxElems = (int64_t)1 << 40;
-constexpr int64_t kMaxK = (int64_t)1 << 24;
-constexpr int64_t kMaxM = (int64_t)1 << 24;
-// A launch counts its work items along x in 32 bits: N and M * N up to these keep
-// every product's grid within (2^27 / 32 workgroups of 512 in the few-row kernel).
-constexpr int64_t kMaxN = (int64_t)1 << 27;
-constexpr int64_t kMaxMN = (int64_t)1 << 37;
-// The same for the expert layer: slots times tiles of its outputs.
+// Slots times tiles of the expert layer's outputs, for the same reason as kMaxMN.
 constexpr int64_t kMaxMoeBlocks = (int64_t)1 << 24;
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-int check_container(int64_t B, int64_t R, int64_t K) {
-    if (B < 1 || R < 0 || K < MX4_BLOCK || K % MX4_BLOCK != 0 || K >= kMaxK) return W12_ERR_SHAPE;
-    if (R >= kMaxElems || B >= kMaxElems) return W12_ERR_SHAPE;
-    const int64_t per = mx4::quads(K) * 8192;       // padded values of one tile
-    if (mx4::tiles(R) > kMaxElems / per) return W12_ERR_SHAPE;
-    if (mx4::tiles(R) > 0 && B > kMaxElems / per / mx4::tiles(R)) return W12_ERR_SHAPE;
-    return W12_OK;
-}
-
-int type_bytes(int t) { return t == W12_OUT_F32 ? 4 : t == W12_OUT_BF16 ? 2 : 0; }
-
-// rows of K values with strides ldx, ldb that start on 16 bytes
-int check_rows(const void* p, int type, int64_t B, int64_t K, int64_t ld, int64_t ldb) {
-    const int64_t n = 16 / type_bytes(type);
-    if (ld < K || ld >= kMaxElems || (B > 1 && (ldb < 0 || ldb >= kMaxElems))) return W12_ERR_SHAPE;
-    if (!aligned(p, 16) || ld % n != 0 || (B > 1 && ldb % n != 0)) return W12_ERR_ALIGN;
-    return W12_OK;
-}
-
-// B matrices of R rows that share no value: one behind the other, or all of them
-// between two rows of one (matrices that overlap would be written twice)
-bool apart(int64_t B, int64_t R, int64_t K, int64_t ld, int64_t ldb) {
-    if (ldb < K) return false;
-    return (ldb - K) / ld >= R - 1 || (ld - K) / ldb >= B - 1;      // ld >= K >= 1
-}
-
-int check_y(const void* y, int64_t N, int64_t ldy, int y_type) {
-    if (type_bytes(y_type) == 0) return W12_ERR_DTYPE;
-    if (ldy < N || ldy >= kMaxElems) return W12_ERR_SHAPE;
-    if (!aligned(y, (uintptr_t)type_bytes(y_type))) return W12_ERR_ALIGN;
-    return W12_OK;
-}
-
-int check_ws(const void* ws, size_t have, size_t need) {
-    if (need == 0) return W12_OK;
-    return ws == nullptr || have < need || !aligned(ws, 256) ? W12_ERR_WORKSPACE : W12_OK;
-}
-
-int status_of(hipError_t e) { return e == hipSuccess ? W12_OK : W12_ERR_HIP; }
-
-int check_gemm_shape(int64_t M, int64_t N, int64_t K) {
-    if (N < 1 || M < 0 || M > kMaxM || N > kMaxN) return W12_ERR_SHAPE;
-    if (M > 0 && N > kMaxMN / M) return W12_ERR_SHAPE;
-    return check_container(1, N, K);
-}
-
-mx4::Mat mat(const void* codes, const void* scales) {
-    return mx4::Mat{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales)};
-}
 
 int gemm(const uint16_t* x, int64_t ldx, mx4::Mat xm, int64_t M, mx4::Mat w, int64_t N, int64_t K,
          void* y, int64_t ldy, int y_type, void* ws, size_t ws_bytes, void* stream) {
@@ -205,19 +145,20 @@ int mx4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t 
     return W12_OK;
 }
 
-int mx4_moe(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int64_t ldl,
-            const void* w13_codes, const void* w13_scales, const void* w2_codes,
-            const void* w2_scales, int64_t H, int64_t I, int64_t E, int64_t top_k, int renormalize,
-            void* y, int64_t ldy, int y_type, void* workspace, size_t workspace_bytes,
-            void* stream) {
-    if (!w13_codes || !w13_scales || !w2_codes || !w2_scales) return W12_ERR_NULL;
-    if (T > 0 && (!x || !logits || !y)) return W12_ERR_NULL;
+// The layer on logits, or (chosen) on a given choice.
+static int moe(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int64_t ldl,
+               const int32_t* chosen, const float* given, mx4::Mat w13, mx4::Mat w2, int64_t H,
+               int64_t I, int64_t E, int64_t top_k, int renormalize, void* y, int64_t ldy,
+               int y_type, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!w13.codes || !w13.scales || !w2.codes || !w2.scales) return W12_ERR_NULL;
+    if (T > 0 && (!x || !y || !(logits || (chosen && given)))) return W12_ERR_NULL;
     if (int rc = check_moe_shape(T, H, I, E, top_k)) return rc;
     if (int rc = check_rows(x, W12_OUT_BF16, 1, H, ldx, 0)) return rc;
     if (int rc = check_y(y, H, ldy, y_type)) return rc;
     if (ldl < E || ldl >= kMaxElems) return W12_ERR_SHAPE;
-    if (!aligned(logits, 4) || !aligned(w13_codes, 16) || !aligned(w13_scales, 16) ||
-        !aligned(w2_codes, 16) || !aligned(w2_scales, 16))
+    if (!aligned(logits, 4) || !aligned(chosen, 4) || !aligned(given, 4) ||
+        !aligned(w13.codes, 16) || !aligned(w13.scales, 16) || !aligned(w2.codes, 16) ||
+        !aligned(w2.scales, 16))
         return W12_ERR_ALIGN;
     size_t need = 0;
     if (T > 0) need = mx4::moe_workspace_bytes(T, H, I, E, top_k, y_type == W12_OUT_F32);
@@ -228,8 +169,10 @@ int mx4_moe(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int6
     a.ldx = ldx;
     a.logits = logits;
     a.ldl = ldl;
-    a.w13 = mat(w13_codes, w13_scales);
-    a.w2 = mat(w2_codes, w2_scales);
+    a.chosen = chosen;
+    a.given = given;
+    a.w13 = w13;
+    a.w2 = w2;
     a.T = (int)T;
     a.H = (int)H;
     a.I = (int)I;
@@ -240,6 +183,62 @@ int mx4_moe(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int6
     a.ldy = ldy;
     a.y_f32 = y_type == W12_OUT_F32;
     return status_of(mx4::launch_moe(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int mx4_moe(const uint16_t* x, int64_t T, int64_t ldx, const float* logits, int64_t ldl,
+            const void* w13_codes, const void* w13_scales, const void* w2_codes,
+            const void* w2_scales, int64_t H, int64_t I, int64_t E, int64_t top_k, int renormalize,
+            void* y, int64_t ldy, int y_type, void* workspace, size_t workspace_bytes,
+            void* stream) {
+    return moe(x, T, ldx, logits, ldl, nullptr, nullptr, mat(w13_codes, w13_scales),
+               mat(w2_codes, w2_scales), H, I, E, top_k, renormalize, y, ldy, y_type, workspace,
+               workspace_bytes, stream);
+}
+
+int mx4_moe_routed(const uint16_t* x, int64_t T, int64_t ldx, const int32_t* experts,
+                   const float* shares, const void* w13_codes, const void* w13_scales,
+                   const void* w2_codes, const void* w2_scales, int64_t H, int64_t I, int64_t E,
+                   int64_t top_k, void* y, int64_t ldy, int y_type, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    return moe(x, T, ldx, nullptr, E, experts, shares, mat(w13_codes, w13_scales),
+               mat(w2_codes, w2_scales), H, I, E, top_k, 0, y, ldy, y_type, workspace,
+               workspace_bytes, stream);
+}
+
+int mx4_route(const void* logits, int logits_type, int64_t T, int64_t E, int64_t ldl,
+              const float* bias, int score, int64_t groups, int64_t kept_groups, int group_terms,
+              int64_t top_k, int renormalize, float scale, int32_t* experts, float* shares,
+              void* stream) {
+    if (T < 0 || E < 1 || top_k < 1 || top_k > E || groups < 1 || E % groups != 0 ||
+        kept_groups < 1 || kept_groups > groups || group_terms < 1 || group_terms > 2)
+        return W12_ERR_SHAPE;
+    if (T > MX4_MAX_ROUTE_T || E > MX4_MAX_E || top_k > MX4_MAX_TOP_K || groups > MX4_MAX_GROUPS)
+        return W12_ERR_UNSUPPORTED;
+    if (type_bytes(logits_type) == 0) return W12_ERR_DTYPE;
+    if (score != MX4_SCORE_SOFTMAX && score != MX4_SCORE_SIGMOID) return W12_ERR_DTYPE;
+    if (T > 0 && (!logits || !experts || !shares)) return W12_ERR_NULL;
+    if (ldl < E || ldl >= kMaxElems) return W12_ERR_SHAPE;
+    if (!aligned(logits, (uintptr_t)type_bytes(logits_type)) || !aligned(bias, 4) ||
+        !aligned(experts, 4) || !aligned(shares, 4))
+        return W12_ERR_ALIGN;
+    if (T == 0) return W12_OK;
+    mx4::RouteArgs a{};
+    a.logits = logits;
+    a.f32 = logits_type == W12_OUT_F32;
+    a.T = T;
+    a.ldl = ldl;
+    a.E = (int)E;
+    a.top_k = (int)top_k;
+    a.bias = bias;
+    a.sigmoid = score == MX4_SCORE_SIGMOID;
+    a.groups = (int)groups;
+    a.kept = (int)kept_groups;
+    a.terms = group_terms;
+    a.renormalize = renormalize != 0;
+    a.scale = scale;
+    a.experts = experts;
+    a.shares = shares;
+    return status_of(mx4::launch_pick(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

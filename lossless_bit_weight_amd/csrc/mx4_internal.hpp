@@ -149,6 +149,8 @@ struct MoeArgs {
     int64_t ldx;
     const float* logits;
     int64_t ldl;
+    const int* chosen;      // or, without logits, each token's experts [T][top_k] and
+    const float* given;     // their shares
     Mat w13, w2;
     int T, H, I, E, top_k, renormalize;
     void* y;
@@ -167,5 +169,19 @@ struct MoeArgs {
 size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k, bool y_f32);
 // Point the workspace fields of `a` at `ws` (moe_workspace_bytes) and launch.
 hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s);
+
+// ---- routing (../../include/mx4_route.h) ----------------------------------------
+struct RouteArgs {
+    const void* logits;
+    int f32;
+    int64_t T, ldl;
+    int E, top_k;
+    const float* bias;
+    int sigmoid, groups, kept, terms, renormalize;
+    float scale;
+    int* experts;
+    float* shares;
+};
+hipError_t launch_pick(const RouteArgs& a, hipStream_t s);
 
 }  // namespace mx4

@@ -53,6 +53,9 @@ __device__ __forceinline__ float wave_sum(float v) {
     return v;
 }
 
+// A given choice: an entry that names no expert is -1, no pair.
+__device__ __forceinline__ int valid(int e, int E) { return (unsigned)e < (unsigned)E ? e : -1; }
+
 // A token's logits over a wave: lane l holds the experts EV l .. EV l + EV - 1, so
 // that the lowest lane of a tie has the lowest expert.
 template <int EV>
@@ -157,7 +160,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(MoeArgs a) {
     for (int i = tid; i < a.E * 4; i += kRouteThreads) (&set[0][0])[i] = 0;
     __syncthreads();
 
-    if (a.T > kRouteTokens) {
+    if (a.chosen != nullptr) {
+        for (int i = tid; i < a.T * a.top_k; i += kRouteThreads) {
+            const int e = valid(a.chosen[i], a.E), t = i / a.top_k;
+            chosen[i] = (int16_t)e;
+            a.share[i] = a.given[i];
+            if (e >= 0) atomicOr(&set[e][t >> 5], 1u << (t & 31));
+        }
+    } else if (a.T > kRouteTokens) {
         for (int i = tid; i < a.T * a.top_k; i += kRouteThreads) {
             const int e = a.place[i], t = i / a.top_k;
             chosen[i] = (int16_t)e;
@@ -553,36 +563,55 @@ __global__ __launch_bounds__(WN* KW * 64) void expert_kernel(MoeArgs a, int bloc
 
 // up for few tokens, each by itself (blockIdx.y): the token chooses for itself, slot
 // s is its expert with the s-th largest logit, found by every wave; the slot's first
-// workgroup writes its words for down.
+// workgroup writes its words for down.  EV = 0: the choice is given, and slot s is its
+// s-th entry that names an expert (down takes the used ones first).
 template <int EV, int WN, int KW, int UG>
 __global__ __launch_bounds__(WN* KW * 64) void up_one_kernel(MoeArgs a, int blocks) {
     extern __shared__ __align__(16) uint8_t lds[];
     const int s = blockIdx.x / blocks, block = blockIdx.x % blocks, lane = threadIdx.x & 63;
     const int t = blockIdx.y, pair = t * a.top_k + s;
     a.x += t * a.ldx;
-    Logits<EV> g;
-    g.load(a.logits + t * a.ldl, a.E, lane);
-    g.rank(a.E, lane);
-    float top = 0.f, mine = 0.f, sum = 0.f;
     int e = -1;
-    const int rounds = block == 0 ? a.top_k : s + 1;
-    for (int j = 0; j < rounds; ++j) {
-        float v = 0.f;
-        const int found = g.take(lane, v);
-        if (found < 0) break;
-        if (j == 0) top = v;
-        if (j == s) {
-            e = found;
-            mine = v;
+    if constexpr (EV == 0) {
+        const int first = t * a.top_k;
+        const int named = lane < a.top_k ? valid(a.chosen[first + lane], a.E) : -1;
+        uint64_t used = __ballot(named >= 0);
+        for (int j = 0; j < s; ++j) used &= used - 1;
+        float p = 0.f;
+        if (used != 0) {
+            const int at = __builtin_ctzll(used);
+            e = __builtin_amdgcn_readlane(named, at);
+            p = a.given[first + at];
         }
-        sum += expf(v - top);
-    }
-    if (block == 0) {
-        if (!a.renormalize) sum = g.total(top);
-        if (threadIdx.x == 0) {
+        if (block == 0 && threadIdx.x == 0) {
             int* o = a.slots + pair * kSlotWords;
             o[0] = e;
-            o[3] = __float_as_int(expf(mine - top) / sum);
+            o[3] = __float_as_int(p);
+        }
+    } else {
+        Logits<EV> g;
+        g.load(a.logits + t * a.ldl, a.E, lane);
+        g.rank(a.E, lane);
+        float top = 0.f, mine = 0.f, sum = 0.f;
+        const int rounds = block == 0 ? a.top_k : s + 1;
+        for (int j = 0; j < rounds; ++j) {
+            float v = 0.f;
+            const int found = g.take(lane, v);
+            if (found < 0) break;
+            if (j == 0) top = v;
+            if (j == s) {
+                e = found;
+                mine = v;
+            }
+            sum += expf(v - top);
+        }
+        if (block == 0) {
+            if (!a.renormalize) sum = g.total(top);
+            if (threadIdx.x == 0) {
+                int* o = a.slots + pair * kSlotWords;
+                o[0] = e;
+                o[3] = __float_as_int(expf(mine - top) / sum);
+            }
         }
     }
     if (e < 0) return;
@@ -860,7 +889,7 @@ void launch_down_one(const MoeArgs& a, hipStream_t s) {
 
 template <int EV>
 void launch_route(const MoeArgs& a, hipStream_t s) {
-    if (a.T > kRouteTokens)
+    if (a.chosen == nullptr && a.T > kRouteTokens)
         hipLaunchKernelGGL(choose_kernel<EV>, dim3((unsigned)((a.T + 3) / 4)), dim3(256), 0, s, a);
     hipLaunchKernelGGL(route_kernel<EV>, dim3(1), dim3(kRouteThreads), 0, s, a);
 }
@@ -885,7 +914,8 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
 
     const int ev = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : 16;
     if (one_by_one(a.T, a.H, a.I, a.E, a.top_k)) {
-        switch (ev) {
+        switch (a.chosen != nullptr ? 0 : ev) {
+            case 0: launch_up_one<0>(a, s); break;
             case 1: launch_up_one<1>(a, s); break;
             case 2: launch_up_one<2>(a, s); break;
             case 4: launch_up_one<4>(a, s); break;
@@ -904,7 +934,7 @@ hipError_t launch_moe(MoeArgs a, void* ws, hipStream_t s) {
     a.out = reinterpret_cast<float*>(p);
     p += up256((size_t)pairs * a.H * 4);
     a.h = p;
-    switch (ev) {
+    switch (a.chosen != nullptr ? 1 : ev) {
         case 1: launch_route<1>(a, s); break;
         case 2: launch_route<2>(a, s); break;
         case 4: launch_route<4>(a, s); break;

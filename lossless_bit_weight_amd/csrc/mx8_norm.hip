@@ -1,0 +1,159 @@
+// mx8_norm.hip -- residual addition, root-mean-square norm and its output in BF16,
+// fp32 or MX8 (../../include/mx8.h states the operation).
+//
+// s = x + residual is read once and stays in registers: TPR threads hold a row, C
+// chunks of eight values each, thread t the chunks t + TPR i.  The sum of squares is
+// held in 64 bits (two instructions a value beside the memory's time), so that no
+// square overflows that s itself does not.  Then y = s * r * weight from the
+// registers; in MX8 the four lanes of a quad hold one block.  One pass over the
+// data, bound by memory.
+#include "mx8_internal.hpp"
+
+namespace mx8 {
+namespace {
+
+template <int TPR>
+__device__ __forceinline__ double row_sum(double v, double* part) {
+    constexpr int kLanes = TPR < 64 ? TPR : 64;
+#pragma unroll
+    for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    if constexpr (TPR > 64) {
+        const int w = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) part[w] = v;
+        __syncthreads();
+        v = 0.0;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) v += part[i];
+    }
+    return v;
+}
+
+constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+// RES: 0 none, 1 BF16, 2 fp32
+template <int TPR, int C, bool XF32, int RES>
+__global__ __launch_bounds__(threads_of(TPR)) void norm_kernel(NormArgs a) {
+    __shared__ double part[TPR > 64 ? TPR / 64 : 1];
+    constexpr int kRows = threads_of(TPR) / TPR;
+    const int t = threadIdx.x % TPR;
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    const bool live = row < a.M;
+    if (!live) row = a.M - 1;           // (a row of its own wave or lanes: nothing is stored)
+
+    // (the weights of long rows are read behind the sum: there are no registers for them)
+    constexpr bool kEarly = C <= 2;
+    Eight v[C], w[kEarly ? C : 1];
+    auto weights = [&](Eight& e, int at) {
+        if (a.w_f32)
+            e.load<true>(a.w, at);
+        else
+            e.load<false>(a.w, at);
+    };
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int k = 8 * (t + TPR * i), at = k < a.K ? k : 0;
+        v[i].template load<XF32>(a.x, row * a.ldx + at);
+        if constexpr (RES != 0) {
+            Eight r;
+            r.load<RES == 2>(a.res, row * a.ldr + at);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i].f[j] += r.f[j];
+        }
+        if constexpr (kEarly) weights(w[i], at);
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int k = 8 * (t + TPR * i);
+        if constexpr (RES == 1) {
+            // the norm is of what the residual keeps
+            const u32x4_t b = v[i].bf16();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[i].f[2 * j] = __uint_as_float(b[j] << 16);
+                v[i].f[2 * j + 1] = __uint_as_float(b[j] & 0xFFFF0000u);
+            }
+        }
+        if constexpr (RES != 0) {
+            if (live && k < a.K) v[i].template store<RES == 2>(a.res_out, row * a.ldo + k);
+        }
+        if (k < a.K) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const double d = v[i].f[j];
+                sum = __builtin_fma(d, d, sum);
+            }
+        }
+    }
+    sum = row_sum<TPR>(sum, part);
+    double r64 = 1.0 / __builtin_sqrt(sum / a.K + (double)a.eps);
+    // a factor outside fp32's normal range: a power of two (exact) goes to the values first
+    if (r64 < 0x1p-100 || r64 > 0x1p100) {
+        const float p = r64 > 1.0 ? 0x1p64f : 0x1p-64f;
+        r64 *= r64 > 1.0 ? 0x1p-64 : 0x1p64;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i].f[j] *= p;
+    }
+    const float r = (float)r64;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int k = 8 * (t + TPR * i);
+        Eight& wi = w[kEarly ? i : 0];
+        if constexpr (!kEarly) weights(wi, k < a.K ? k : 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i].f[j] = v[i].f[j] * r * wi.f[j];
+        const bool in = live && k < a.K;
+        if (a.y_type == 2) {
+            uint32_t e;
+            const u32x2_t d = v[i].encode(e);
+            uint8_t* y = static_cast<uint8_t*>(a.y);
+            if (in) *reinterpret_cast<u32x2_t*>(y + row * a.ldy + k) = d;
+            if ((t & 3) == 0 && live && k < a.K)
+                a.ys[row * a.lds + scale_place(k)] = (uint8_t)e;
+        } else if (in) {
+            if (a.y_type == 1)
+                v[i].template store<true>(a.y, row * a.ldy + k);
+            else
+                v[i].template store<false>(a.y, row * a.ldy + k);
+        }
+    }
+    // the scales past K
+    if (a.y_type == 2 && live) {
+        const int first = a.K / 32, n = (int)mx4::quads(a.K) * 16 - first;
+        for (int i = t; i < n; i += TPR)
+            a.ys[row * a.lds + scale_place((first + i) * 32)] = 127;
+    }
+}
+
+template <int TPR, int C>
+hipError_t launch(const NormArgs& a, hipStream_t s) {
+    constexpr int kRows = threads_of(TPR) / TPR;
+    const dim3 grid((unsigned)((a.M + kRows - 1) / kRows)), block(threads_of(TPR));
+    const int res = a.res == nullptr ? 0 : a.res_f32 ? 2 : 1;
+    switch (res * 2 + a.x_f32) {
+        case 0: hipLaunchKernelGGL((norm_kernel<TPR, C, false, 0>), grid, block, 0, s, a); break;
+        case 1: hipLaunchKernelGGL((norm_kernel<TPR, C, true, 0>), grid, block, 0, s, a); break;
+        case 2: hipLaunchKernelGGL((norm_kernel<TPR, C, false, 1>), grid, block, 0, s, a); break;
+        case 3: hipLaunchKernelGGL((norm_kernel<TPR, C, true, 1>), grid, block, 0, s, a); break;
+        case 4: hipLaunchKernelGGL((norm_kernel<TPR, C, false, 2>), grid, block, 0, s, a); break;
+        default: hipLaunchKernelGGL((norm_kernel<TPR, C, true, 2>), grid, block, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+    const int chunks = a.K / 8;
+    if (chunks <= 16) return launch<16, 1>(a, s);
+    if (chunks <= 64) return launch<64, 1>(a, s);
+    if (chunks <= 256) return launch<256, 1>(a, s);
+    if (chunks <= 512) return launch<512, 1>(a, s);
+    if (chunks <= 1024) return launch<1024, 1>(a, s);
+    if (chunks <= 2048) return launch<1024, 2>(a, s);
+    return launch<1024, 4>(a, s);
+}
+
+}  // namespace mx8

@@ -1,6 +1,7 @@
-"""Python binding of libw12.so's MX4 calls (include/mx4.h): 4-bit floating
-point under a shared scale per 32 values, the products with weights stored
-that way, and an expert layer on them.
+"""Python binding of libw12.so's MX4 calls (include/mx4.h, include/mx4_route.h):
+4-bit floating point under a shared scale per 32 values, the products with
+weights stored that way, an expert layer on them, and the routing of tokens to
+experts.
 
 As w12.py this marshals arguments only: every function hands torch tensors'
 device pointers and torch's current HIP stream of the tensors' device to the
@@ -12,6 +13,8 @@ call, so calls on different streams, and captured graphs, share nothing.
     y = mx4_gemm(x, wq)                     # x BF16 [M, K], any M
     y = mx4_gemm(mx4_quantize(x), wq)       # both sides in 4 bits
     y = mx4_moe(x, logits, w13q, w2q, 6)    # an expert layer, up to 128 tokens
+    experts, shares = mx4_route(logits, 8, scores="sigmoid", bias=b, groups=8, kept_groups=4)
+    y = mx4_moe_routed(x, experts, shares, w13q, w2q)
 """
 from __future__ import annotations
 
@@ -28,6 +31,8 @@ BLOCK = 32
 MAX_T = 128
 MAX_E = 1024
 MAX_TOP_K = 32
+MAX_GROUPS = 64
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 _BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)
 _u8 = torch.uint8
@@ -64,8 +69,13 @@ def lib() -> ctypes.CDLL:
     L.mx4_moe_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i32, psz]
     L.mx4_moe.argtypes = [p, i64, i64, p, i64, p, p, p, p, i64, i64, i64, i64, i32, p, i64, i32,
                           p, sz, p]
+    L.mx4_route.argtypes = [p, i32, i64, i64, i64, p, i32, i64, i64, i32, i64, i32, ctypes.c_float,
+                            p, p, p]
+    L.mx4_moe_routed.argtypes = [p, i64, i64, p, p, p, p, p, p, i64, i64, i64, i64, p, i64, i32, p,
+                                 sz, p]
     for name in ("mx4_quantize", "mx4_dequantize", "mx4_gemm_workspace_bytes", "mx4_gemm",
-                 "mx4_gemm_mx4", "mx4_moe_workspace_bytes", "mx4_moe"):
+                 "mx4_gemm_mx4", "mx4_moe_workspace_bytes", "mx4_moe", "mx4_route",
+                 "mx4_moe_routed"):
         getattr(L, name).restype = i32
     _lib = L
     return L
@@ -382,4 +392,86 @@ def mx4_moe(x: torch.Tensor, logits: torch.Tensor, w13: MX4Tensor, w2: MX4Tensor
     _check(lib().mx4_moe(x.data_ptr(), T, ldx, logits.data_ptr(), ldl, c13, s13, c2, s2, H, I, E,
                          int(top_k), int(bool(renormalize)), y.data_ptr(), ldy, yt, wsp, wsb,
                          _raw_stream(dev)), "mx4_moe")
+    return y
+
+
+def _pairs(t: torch.Tensor, what: str, T: int, k: int, dtype: torch.dtype, dev: int) -> int:
+    """The pointer of a contiguous [T, k] tensor."""
+    _same(dev, _gpu(t, what))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if tuple(t.shape) != (T, k) or not t.is_contiguous():
+        raise ValueError("%s must be contiguous (%d, %d), got %s" % (what, T, k, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def mx4_route(logits: torch.Tensor, top_k: int, scores: str = "softmax",
+              bias: torch.Tensor | None = None, groups: int = 1, kept_groups: int = 1,
+              group_terms: int = 1, renormalize: bool = True, scale: float = 1.0,
+              experts: torch.Tensor | None = None, shares: torch.Tensor | None = None) -> tuple:
+    """(experts int32 [T, top_k], shares fp32 [T, top_k]) of include/mx4_route.h's
+    mx4_route: router logits [T, E] BF16 or fp32, scores "softmax" or "sigmoid",
+    bias fp32 [E] added to the scores for the choice alone, the choice limited to
+    kept_groups of `groups` groups of experts by their group_terms (1 or 2)
+    largest."""
+    dev = _gpu(logits, "logits")
+    if _away(dev):
+        with torch.cuda.device(dev):
+            return mx4_route(logits, top_k, scores, bias, groups, kept_groups, group_terms,
+                             renormalize, scale, experts, shares)
+    T, E, ldl = _rows(logits, "logits")
+    kind = SCORES.get(scores)
+    if kind is None:
+        raise ValueError("scores must be one of %s, got %r" % (tuple(SCORES), scores))
+    bp = None
+    if bias is not None:
+        _same(dev, _gpu(bias, "bias"))
+        if bias.dtype is not torch.float32:
+            raise TypeError("bias must be float32, got %s" % bias.dtype)
+        if tuple(bias.shape) != (E,) or not bias.is_contiguous():
+            raise ValueError("bias must be %d contiguous values" % E)
+        bp = bias.data_ptr()
+    top_k = int(top_k)
+    if experts is None:
+        experts = logits.new_empty((T, max(top_k, 0)), dtype=torch.int32)
+    if shares is None:
+        shares = logits.new_empty((T, max(top_k, 0)), dtype=torch.float32)
+    ep = _pairs(experts, "experts", T, max(top_k, 0), torch.int32, dev)
+    sp = _pairs(shares, "shares", T, max(top_k, 0), torch.float32, dev)
+    _check(lib().mx4_route(logits.data_ptr(), _type_of(logits.dtype), T, E, ldl, bp, kind,
+                           int(groups), int(kept_groups), int(group_terms), top_k,
+                           int(bool(renormalize)), float(scale), ep, sp, _raw_stream(dev)),
+           "mx4_route")
+    return experts, shares
+
+
+def mx4_moe_routed(x: torch.Tensor, experts: torch.Tensor, shares: torch.Tensor, w13: MX4Tensor,
+                   w2: MX4Tensor, out_dtype: torch.dtype = torch.bfloat16,
+                   y: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """mx4_moe on a given routing: experts int32 and shares fp32 [T, top_k], as
+    mx4_route gives them (an entry outside 0 .. E-1 counts for nothing)."""
+    dev = _gpu(x, "x")
+    if _away(dev):
+        with torch.cuda.device(dev):
+            return mx4_moe_routed(x, experts, shares, w13, w2, out_dtype, y, workspace)
+    if x.dtype not in _BF16_TYPES:
+        raise TypeError("x must hold BF16 bits (bfloat16/int16/uint16), got %s" % x.dtype)
+    T, H, ldx = _rows(x, "x")
+    if experts.dim() != 2:
+        raise ValueError("experts must be 2-D")
+    k, E, I = experts.shape[1], w13.batch, w2.K
+    if E is None or w13.shape != (E, 2 * I, H) or w2.shape != (E, H, I):
+        raise ValueError("x %s, w13 %s and w2 %s do not fit together"
+                         % (tuple(x.shape), w13.shape, w2.shape))
+    ep = _pairs(experts, "experts", T, k, torch.int32, dev)
+    sp = _pairs(shares, "shares", T, k, torch.float32, dev)
+    c13, s13, d13 = w13.ptrs("w13")
+    c2, s2, d2 = w2.ptrs("w2")
+    _same(dev, d13, d2)
+    y, ldy, yt = _output(y, T, H, out_dtype, dev, x)
+    keep, wsp, wsb = _workspace(mx4_moe_workspace_bytes(T, H, I, E, k, y.dtype), workspace, x)
+    _check(lib().mx4_moe_routed(x.data_ptr(), T, ldx, ep, sp, c13, s13, c2, s2, H, I, E, k,
+                                y.data_ptr(), ldy, yt, wsp, wsb, _raw_stream(dev)),
+           "mx4_moe_routed")
     return y
