@@ -1,178 +1,287 @@
 // mx4_route.hip -- each token's experts and their shares (../../include/mx4_route.h
 // states the operation).
 //
-// A wave takes one token: lane l holds the experts EV l .. EV l + EV - 1, so that the
-// lowest lane of a tie has the lowest expert.  Scores and ranks are fp64 (a choice
-// between two that differ in the last of fp32's bits is then the same for every way of
-// computing them); a rank becomes a 64-bit number of the same order, and the chosen
-// ones are taken by repeated maxima over the wave.
+// A wave takes one token.  Where groups are limited a group has L neighbouring lanes, the
+// largest power of two that 64 lanes have for each, else all 64 are one group; lane r of
+// a group holds its experts r, r + L, r + 2 L ..: what a group is worth is then found for
+// all groups at once, by exchanges between neighbours.
+// A rank is a 64-bit number of the same order (fp64 scores plus bias: a choice between two
+// that differ in the last of fp32's bits is then the same for every way of computing
+// them; or the fp32 logit in the upper half).  The chosen ones are taken by maxima over
+// the wave of the upper halves, and of the lower ones and the indices only where several
+// share the largest: seven instructions a maximum, no LDS.  The scores of the chosen are
+// computed again from their logits, a lane each, so that softmax with renormalised shares
+// and no bias needs no exponential of the others.
+// Bound by instructions: 8191 tokens, 256 experts in 8 groups, sigmoid and bias: see
+// launch_pick.
+#include <type_traits>
+
 #include "exp64.hpp"
 #include "mx4_internal.hpp"
 
 namespace mx4 {
 namespace {
 
-// Order of ranks as unsigned numbers: NaN above all, -0 as +0; 0 is no rank's.
-__device__ __forceinline__ uint64_t order_key(double v) {
+// Order as unsigned numbers: NaN above all, -0 as +0; 0 is no rank's.
+__device__ __forceinline__ uint32_t order32(float l) {
+    if (l != l) return ~0u;
+    const uint32_t u = __float_as_uint(l + 0.0f);
+    return u >> 31 ? ~u : u | 1u << 31;
+}
+__device__ __forceinline__ uint64_t order64(double v) {
     if (v != v) return ~0ull;
     const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
     return u >> 63 ? ~u : u | 1ull << 63;
 }
 
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const uint64_t o = (uint64_t)__shfl_xor((long long)v, d);
-        v = o > v ? o : v;
+// Two copies of v between which the lanes D apart (in the order of mirrored rows below 16)
+// have changed places: every lane finds its own value in one of them and the other lane's
+// in the other.
+template <int D>
+__device__ __forceinline__ void exchange(uint32_t v, uint32_t& a, uint32_t& b) {
+    a = b = v;
+    if constexpr (D == 1) {
+        b = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);   // 1 0 3 2
+    } else if constexpr (D == 2) {
+        b = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);   // 2 3 0 1
+    } else if constexpr (D == 4) {
+        b = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true);  // half mirror
+    } else if constexpr (D == 8) {
+        b = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true);  // mirror
+    } else if constexpr (D == 16) {
+        swap16(a, b);
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+        a = r[0];
+        b = r[1];
     }
-    return v;
+}
+template <int D, class T>
+__device__ __forceinline__ void exchange64(T v, T& a, T& b) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    uint32_t a0, a1, b0, b1;
+    exchange<D>((uint32_t)u, a0, b0);
+    exchange<D>((uint32_t)(u >> 32), a1, b1);
+    a = __builtin_bit_cast(T, (uint64_t)a1 << 32 | a0);
+    b = __builtin_bit_cast(T, (uint64_t)b1 << 32 | b0);
+}
+// f(D) for the distances within runs of L lanes, L a power of two that is the same in all.
+template <class F>
+__device__ __forceinline__ void within(int L, F f) {
+    if (L > 1) f(std::integral_constant<int, 1>{});
+    if (L > 2) f(std::integral_constant<int, 2>{});
+    if (L > 4) f(std::integral_constant<int, 4>{});
+    if (L > 8) f(std::integral_constant<int, 8>{});
+    if (L > 16) f(std::integral_constant<int, 16>{});
+    if (L > 32) f(std::integral_constant<int, 32>{});
 }
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    within(64, [&](auto d) {
+        double a, b;
+        exchange64<decltype(d)::value>(v, a, b);
+        v = a + b;
+    });
     return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    within(64, [&](auto d) {
+        uint32_t a, b;
+        exchange<decltype(d)::value>(v, a, b);
+        v = a > b ? a : b;
+    });
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+template <bool F32>
+__device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
+    if constexpr (F32) return static_cast<const float*>(a.logits)[t * a.ldl + e];
+    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[t * a.ldl + e] << 16);
+}
+__device__ __forceinline__ double sigmoid(float l) {
+    const double d = l;
+    return d != d ? d : 1.0 / (1.0 + exp2_64(-d * kLog2E));
+}
+// exp(l - top), whose sum is softmax's denominator
+__device__ __forceinline__ double power(float l, float top) {
+    return l == -__builtin_inff() ? 0.0 : exp2_64(((double)l - (double)top) * kLog2E);
 }
 
 template <int EV, bool F32>
-__global__ __launch_bounds__(256) void pick_kernel(RouteArgs a) {
+__global__ __launch_bounds__(256) void pick_kernel(RouteArgs a, int groups, int log_lanes) {
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= a.T) return;
     const int lane = threadIdx.x & 63;
+    const int L = 1 << log_lanes, per = a.E / groups;
+    const int g = lane >> log_lanes, r = lane & (L - 1);
+    const int first = g * per + r;              // the expert of slot i is first + i L
+    const bool any_bias = a.bias != nullptr, limited = groups > 1;
 
-    double score[EV];
-    uint64_t key[EV];               // 0: not to be chosen
     float l[EV];
 #pragma unroll
     for (int i = 0; i < EV; ++i) {
-        const int e = EV * lane + i;
-        l[i] = -__builtin_inff();
-        if (e < a.E) {
-            if constexpr (F32)
-                l[i] = static_cast<const float*>(a.logits)[t * a.ldl + e];
-            else
-                l[i] = __uint_as_float(
-                    (uint32_t)static_cast<const uint16_t*>(a.logits)[t * a.ldl + e] << 16);
+        const bool in = g < groups && i * L + r < per;
+        l[i] = logit<F32>(a, t, in ? first + i * L : 0);
+        l[i] = in ? l[i] : -__builtin_inff();
+    }
+    // softmax: the largest logit; without a distribution (a NaN, +inf) all scores are NaN
+    float top = 0.f;
+    bool bad = false;
+    if (!a.sigmoid) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < EV; ++i) {
+            const uint32_t o = order32(l[i]);
+            m = o > m ? o : m;
+        }
+        m = wave_max(m);
+        bad = m >= order32(__builtin_inff());
+        top = __uint_as_float(m >> 31 ? m & 0x7FFFFFFFu : ~m);
+    }
+    double score[EV], sum = 1.0;
+    const bool all = any_bias || (limited && a.terms == 2) || (!a.sigmoid && !a.renormalize);
+    if (all) {
+        if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < EV; ++i) score[i] = sigmoid(l[i]);
+        } else {
+            sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < EV; ++i) {
+                score[i] = power(l[i], top);
+                sum += score[i];
+            }
+            sum = wave_sum(sum);
+#pragma unroll
+            for (int i = 0; i < EV; ++i) score[i] = bad ? __builtin_nan("") : score[i] / sum;
         }
     }
-    if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < EV; ++i) {
-            const double d = l[i];
-            score[i] = d != d ? d : 1.0 / (1.0 + exp2_64(-d * kLog2E));
-        }
-    } else {
-        float top = -__builtin_inff();
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < EV; ++i) {
-            top = l[i] > top ? l[i] : top;
-            bad = bad || l[i] != l[i] || l[i] == __builtin_inff();
-        }
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-        bad = __ballot(bad) != 0;
-        double sum = 0.0;
-#pragma unroll
-        for (int i = 0; i < EV; ++i) {
-            score[i] = l[i] == -__builtin_inff()
-                           ? 0.0
-                           : exp2_64(((double)l[i] - (double)top) * kLog2E);
-            sum += score[i];
-        }
-        sum = wave_sum(sum);
-#pragma unroll
-        for (int i = 0; i < EV; ++i) score[i] = bad ? __builtin_nan("") : score[i] / sum;
-    }
-    double biased[EV];
-    bool any[EV];
+    uint32_t hi[EV], lo[EV];            // ranks; 0: not to be chosen
+    double value[EV];                   // s + bias, -inf for those
 #pragma unroll
     for (int i = 0; i < EV; ++i) {
-        const int e = EV * lane + i;
-        const float b = a.bias != nullptr && e < a.E ? a.bias[e] : 0.f;
-        biased[i] = score[i] + (double)b;
-        any[i] = e < a.E && l[i] != -__builtin_inff() && b != -__builtin_inff();
-        key[i] = any[i] ? order_key(a.bias != nullptr ? biased[i] : (double)l[i]) : 0;
-        if (a.bias != nullptr && l[i] != l[i] && any[i]) key[i] = ~0ull;
+        const bool in = g < groups && i * L + r < per;
+        bool may = l[i] != -__builtin_inff();
+        if (any_bias) {
+            const float b = a.bias[in ? first + i * L : 0];
+            may = may && b != -__builtin_inff();
+            value[i] = score[i] + (double)b;
+            const uint64_t o = order64(l[i] != l[i] ? (double)l[i] : value[i]);
+            hi[i] = (uint32_t)(o >> 32);
+            lo[i] = (uint32_t)o;
+        } else {
+            value[i] = all ? score[i] : 0.0;
+            hi[i] = order32(l[i]);
+            lo[i] = 0;
+        }
+        hi[i] = may ? hi[i] : 0u;
+        lo[i] = may ? lo[i] : 0u;
+        value[i] = may ? value[i] : -__builtin_inf();
     }
 
-    // the groups that count: lane g holds the value of group g
-    if (a.kept < a.groups) {
-        const int per = a.E / a.groups;
-        uint64_t mine = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            uint64_t v = 0;
+    if (limited) {
+        uint64_t worth = 0;
+        if (a.terms == 1) {
 #pragma unroll
-            for (int i = 0; i < EV; ++i)
-                if ((EV * lane + i) / per == g && key[i] > v) v = key[i];
-            v = wave_max(v);
-            if (a.terms == 2 && v != 0) {
-                double one = -__builtin_inf(), two = -__builtin_inf();
-                bool nan = false;
-#pragma unroll
-                for (int i = 0; i < EV; ++i) {
-                    if ((EV * lane + i) / per != g || !any[i]) continue;
-                    const double s = biased[i];
-                    nan = nan || s != s;
-                    two = fmax(two, s < one ? s : one);
-                    one = fmax(one, s);
-                }
-#pragma unroll
-                for (int d = 32; d > 0; d >>= 1) {
-                    const double o1 = __shfl_xor(one, d), o2 = __shfl_xor(two, d);
-                    two = fmax(fmax(two, o2), one < o1 ? one : o1);
-                    one = fmax(one, o1);
-                }
-                v = __ballot(nan)                ? ~0ull
-                    : two == -__builtin_inf() ? order_key(one)
-                                              : order_key(one + two);
+            for (int i = 0; i < EV; ++i) {
+                const uint64_t k = (uint64_t)hi[i] << 32 | lo[i];
+                worth = k > worth ? k : worth;
             }
-            if (lane == g) mine = v;
+            within(L, [&](auto d) {
+                uint64_t x, y;
+                exchange64<decltype(d)::value>(worth, x, y);
+                worth = x > y ? x : y;
+            });
+        } else {
+            // the two largest values; a NaN makes the sum one
+            double one = -__builtin_inf(), two = one;
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < EV; ++i) {
+                nan = nan || value[i] != value[i];
+                two = fmax(two, fmin(one, value[i]));
+                one = fmax(one, value[i]);
+            }
+            uint32_t nans = nan;
+            within(L, [&](auto d) {
+                constexpr int D = decltype(d)::value;
+                double x1, y1, x2, y2;
+                uint32_t xn, yn;
+                exchange64<D>(one, x1, y1);
+                exchange64<D>(two, x2, y2);
+                exchange<D>(nans, xn, yn);
+                two = fmax(fmax(x2, y2), fmin(x1, y1));
+                one = fmax(x1, y1);
+                nans = xn | yn;
+            });
+            if (nans)
+                worth = ~0ull;
+            else if (one != -__builtin_inf())
+                worth = order64(two == -__builtin_inf() ? one : one + two);
         }
-        // those above a group, and those equal before it
+        // those worth more than this lane's group, and those equal before it
         int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const uint64_t o = (uint64_t)__shfl((long long)mine, g);
-            before += o > mine || (o == mine && g < lane);
+        for (int o = 0; o < groups; ++o) {
+            const uint32_t o0 =
+                (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)worth, o << log_lanes);
+            const uint32_t o1 =
+                (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(worth >> 32), o << log_lanes);
+            const uint64_t other = (uint64_t)o1 << 32 | o0;
+            before += other > worth || (other == worth && o < g);
         }
-        const uint64_t keep = __ballot(before < a.kept && lane < a.groups);
 #pragma unroll
         for (int i = 0; i < EV; ++i) {
-            const int g = (EV * lane + i) / per;
-            if (g > 63 || !(keep >> g & 1)) key[i] = 0;
+            hi[i] = before < a.kept ? hi[i] : 0u;
+            lo[i] = before < a.kept ? lo[i] : 0u;
         }
     }
 
     int found = -1;
-    double share = 0.0;
     for (int j = 0; j < a.top_k; ++j) {
-        uint64_t best = 0;
-        int at = 0;
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < EV; ++i) best = hi[i] > best ? hi[i] : best;
+        best = wave_max(best);
+        if (best == 0) break;
+        int e = 0, n = 0;
 #pragma unroll
         for (int i = 0; i < EV; ++i) {
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
+            const uint64_t hits = __ballot(hi[i] == best);
+            n += __popcll(hits);
+            if (hits != 0) {
+                const int src = __builtin_ctzll(hits);
+                e = (src >> log_lanes) * per + (src & (L - 1)) + i * L;
             }
         }
-        const uint64_t m = wave_max(best);
-        if (m == 0) break;
-        const int src = __builtin_ctzll(__ballot(best == m));
-        double s = 0.0;
+        if (n > 1) {            // the largest lower half, and of its experts the lowest
+            uint32_t low = 0, at = 0;
 #pragma unroll
-        for (int i = 0; i < EV; ++i) {
-            if (i == at) s = score[i];
-            if (lane == src && i == at) key[i] = 0;
+            for (int i = 0; i < EV; ++i)
+                if (hi[i] == best && lo[i] > low) low = lo[i];
+            low = wave_max(low);
+#pragma unroll
+            for (int i = 0; i < EV; ++i)
+                if (hi[i] == best && lo[i] == low && ~(uint32_t)(first + i * L) > at)
+                    at = ~(uint32_t)(first + i * L);
+            e = (int)~wave_max(at);
         }
-        const int e = EV * src + __shfl(at, src);
-        s = __shfl(s, src);
-        if (lane == j) {
-            found = e;
-            share = s;
-        }
+#pragma unroll
+        for (int i = 0; i < EV; ++i) hi[i] = first + i * L == e ? 0u : hi[i];
+        found = lane == j ? e : found;
+    }
+
+    double share = 0.0;
+    if (found >= 0) {
+        const float chosen = logit<F32>(a, t, found);
+        if (a.sigmoid)
+            share = sigmoid(chosen);
+        else
+            share = bad ? __builtin_nan("") : power(chosen, top);
     }
     if (a.renormalize) {
-        const double sum = wave_sum(share);
-        share = sum == 0.0 ? 0.0 : share / sum;
+        const double whole = wave_sum(share);
+        share = whole == 0.0 ? 0.0 : share / whole;
+    } else if (!a.sigmoid) {
+        share /= sum;
     }
     if (lane < a.top_k) {
         a.experts[t * a.top_k + lane] = found;
@@ -181,27 +290,34 @@ __global__ __launch_bounds__(256) void pick_kernel(RouteArgs a) {
 }
 
 template <int EV>
-void launch(const RouteArgs& a, hipStream_t s) {
+void launch(const RouteArgs& a, int groups, int log_lanes, hipStream_t s) {
     const dim3 grid((unsigned)((a.T + 3) / 4)), block(256);
     if (a.f32)
-        hipLaunchKernelGGL((pick_kernel<EV, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((pick_kernel<EV, true>), grid, block, 0, s, a, groups, log_lanes);
     else
-        hipLaunchKernelGGL((pick_kernel<EV, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((pick_kernel<EV, false>), grid, block, 0, s, a, groups, log_lanes);
 }
 
 }  // namespace
 
 hipError_t launch_pick(const RouteArgs& a, hipStream_t s) {
-    if (a.E <= 64)
-        launch<1>(a, s);
-    else if (a.E <= 128)
-        launch<2>(a, s);
-    else if (a.E <= 256)
-        launch<4>(a, s);
-    else if (a.E <= 512)
-        launch<8>(a, s);
+    // groups that all count are as good as one
+    const int groups = a.kept < a.groups ? a.groups : 1;
+    int log_lanes = 6;
+    while (groups > 64 >> log_lanes) --log_lanes;
+    const int slots = (a.E / groups + (1 << log_lanes) - 1) >> log_lanes;
+    if (slots <= 1)
+        launch<1>(a, groups, log_lanes, s);
+    else if (slots <= 2)
+        launch<2>(a, groups, log_lanes, s);
+    else if (slots <= 4)
+        launch<4>(a, groups, log_lanes, s);
+    else if (slots <= 8)
+        launch<8>(a, groups, log_lanes, s);
+    else if (slots <= 16)
+        launch<16>(a, groups, log_lanes, s);
     else
-        launch<16>(a, s);
+        launch<32>(a, groups, log_lanes, s);
     return hipGetLastError();
 }
 

@@ -432,12 +432,17 @@ def mx4_route(logits: torch.Tensor, top_k: int, scores: str = "softmax",
             raise ValueError("bias must be %d contiguous values" % E)
         bp = bias.data_ptr()
     top_k = int(top_k)
+    k = top_k if top_k > 0 else 0
     if experts is None:
-        experts = logits.new_empty((T, max(top_k, 0)), dtype=torch.int32)
+        experts = logits.new_empty((T, k), dtype=torch.int32)
+        ep = experts.data_ptr()
+    else:
+        ep = _pairs(experts, "experts", T, k, torch.int32, dev)
     if shares is None:
-        shares = logits.new_empty((T, max(top_k, 0)), dtype=torch.float32)
-    ep = _pairs(experts, "experts", T, max(top_k, 0), torch.int32, dev)
-    sp = _pairs(shares, "shares", T, max(top_k, 0), torch.float32, dev)
+        shares = logits.new_empty((T, k), dtype=torch.float32)
+        sp = shares.data_ptr()
+    else:
+        sp = _pairs(shares, "shares", T, k, torch.float32, dev)
     _check(lib().mx4_route(logits.data_ptr(), _type_of(logits.dtype), T, E, ldl, bp, kind,
                            int(groups), int(kept_groups), int(group_terms), top_k,
                            int(bool(renormalize)), float(scale), ep, sp, _raw_stream(dev)),
