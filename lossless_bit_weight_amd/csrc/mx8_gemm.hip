@@ -19,8 +19,31 @@ namespace {
 
 using mx4::kCodeBlock;
 using mx4::kScaleBlock;
-using mx4::scalar;
 using mx4::tiles;
+
+// A uniform pointer to global memory that the compiler keeps in scalar registers (folded
+// with the lane's offset it would hold two vector registers through the loop), and 16, 8 or 4
+// bytes at a lane's offset from it.  In the generic address space these would be flat loads,
+// which every wait for LDS waits for too.
+typedef const __attribute__((address_space(1))) uint8_t* global_t;
+__device__ __forceinline__ global_t scalar(const uint8_t* p) {
+    global_t g = (global_t)p;
+    asm volatile("" : "+s"(g));
+    return g;
+}
+__device__ __forceinline__ u32x4_t load16(global_t p, uint32_t at) {
+    return *reinterpret_cast<const __attribute__((address_space(1))) u32x4_t*>(p + at);
+}
+__device__ __forceinline__ u32x4_t load16_nt(global_t p, uint32_t at) {
+    return __builtin_nontemporal_load(
+        reinterpret_cast<const __attribute__((address_space(1))) u32x4_t*>(p + at));
+}
+__device__ __forceinline__ u32x2_t load8(global_t p, uint32_t at) {
+    return *reinterpret_cast<const __attribute__((address_space(1))) u32x2_t*>(p + at);
+}
+__device__ __forceinline__ uint32_t load4(global_t p, uint32_t at) {
+    return *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(p + at);
+}
 
 __device__ __forceinline__ void store_y(const GemmArgs& a, int64_t m, int64_t n, float v) {
     if (a.y_f32)
@@ -136,10 +159,527 @@ hipError_t launch_small(const GemmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// ---- a few rows of x, shared through LDS ------------------------------------------
+// A workgroup: 16 MT rows of x by 16 WN weight rows; KW groups of WN waves take every
+// KW-th unit of four groups of K.  A unit's weights come to registers one unit ahead of
+// their products; its x goes through LDS, double-buffered, where the WN waves share it:
+// row m of a unit is 32 pieces of 16 bytes, piece p at place (p & 16) | ((p ^ m) & 15).
+// A read takes one piece from 16 rows for each q; the LDS serves it 16 lanes at a time,
+// rows 0-3 and 12-15 of one q with rows 4-11 of the next, which lie in 16 different
+// places then, and so do the 16 pieces that 16 lanes write.
+template <int MT, int WN, int KW>
+struct Mid {
+    static constexpr int kThreads = WN * KW * 64;
+    static constexpr int kAllPieces = 16 * MT * 32;                         // of x a unit
+    static constexpr int kPieces = (kAllPieces + WN * 64 - 1) / (WN * 64);  // a thread
+    static constexpr int kStage = kAllPieces * 16;
+    static constexpr int lds() {
+        const int x = 2 * KW * kStage, red = KW * WN * MT * 1024;
+        return x > red ? x : red;
+    }
+};
+
+template <int MT, int WN, int KW>
+__global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, int nb) {
+    using T = Mid<MT, WN, KW>;
+    constexpr int P = T::kPieces;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kw = w / WN, wn = w % WN;
+    const int c = lane & 15, q = lane >> 4;
+    // the row blocks of one weight block run side by side on one XCD (consecutive
+    // workgroups go to the 8 XCDs in turn), so that its L2 serves the weights again
+    int bm = 0, bn = blockIdx.x;
+    if (mb > 1) {
+        const int band = 8 * mb, b = blockIdx.x / band, i = blockIdx.x % band;
+        const int width = nb - 8 * b < 8 ? nb - 8 * b : 8;
+        bn = 8 * b + i % width;
+        bm = i / width;
+    }
+    const int m0 = bm * 16 * MT;
+    const int u0 = blockIdx.y * (a.gs / 4);
+    const int u1 = u0 + a.gs / 4 < a.Q ? u0 + a.gs / 4 : a.Q;
+    const int its = (u1 - u0 + KW - 1) / KW;
+    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+
+    const int64_t last_tile = tiles(a.N) - 1;
+    int64_t tile = (int64_t)bn * WN + wn;
+    if (tile > last_tile) tile = last_tile;
+    const uint8_t* wp = a.w.codes + tile * a.G * kCodeBlock;
+    const uint8_t* sp = a.w.scales + tile * a.Q * kScaleBlock;
+    uint8_t* mine = lds + kw * 2 * T::kStage;
+    // this thread's pieces of x (past the last: the last once more), and the rows of its
+    // lane's scales
+    int at[P];
+    const uint8_t* xp[P];
+    int xk[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        int piece = (i * WN + wn) * 64 + lane;
+        if (T::kAllPieces % (WN * 64) != 0 && piece > T::kAllPieces - 64 + lane)
+            piece = T::kAllPieces - 64 + lane;
+        const int row = piece / 32, p = piece % 32;
+        at[i] = (row * 32 + ((p & 16) | ((p ^ row) & 15))) * 16;
+        const int m = m0 + row < a.M ? m0 + row : a.M - 1;
+        xp[i] = a.x + (int64_t)m * a.ldv;
+        xk[i] = 16 * p;
+    }
+    const uint8_t* xs[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int m = m0 + 16 * t + c < a.M ? m0 + 16 * t + c : a.M - 1;
+        xs[t] = a.xs + (int64_t)m * a.lds + 4 * q;
+    }
+    u32x4_t wb[2][4], xb[P];
+    uint32_t ws[2], xsc[2][MT];
+    bool xin[P];
+    // (no branch: a place past the last unit, group or K is a valid one whose x is
+    // replaced by zeros)
+    auto load = [&](int slot, int it) {
+        const int u = u0 + it * KW + kw;
+        const int uc = u < u1 ? u : u1 - 1;
+        ws[slot] = load4(scalar(sp + (int64_t)uc * kScaleBlock), lane4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int g = uc * 4 + j < a.G ? uc * 4 + j : a.G - 1;
+            const global_t from = scalar(wp + (int64_t)g * kCodeBlock);
+            wb[slot][j] = MT == 1 ? load16_nt(from, lane16) : load16(from, lane16);
+        }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int k = u * 512 + xk[i];
+            xin[i] = u < u1 && k < a.K;
+            xb[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[i] ? k : 0));
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            xsc[slot][t] = *reinterpret_cast<const uint32_t*>(xs[t] + 16 * uc);
+    };
+    auto stage = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            u32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = xin[i] ? xb[i][e] : 0u;
+            *reinterpret_cast<u32x4_t*>(mine + buf * T::kStage + at[i]) = v;
+        }
+    };
+    f32x4_t acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0, 0, 0, 0};
+    auto product = [&](auto sc) {
+        constexpr int slot = decltype(sc)::value;
+        const uint8_t* xl = mine + slot * T::kStage;
+        auto group = [&](auto jc) {
+            constexpr int J = decltype(jc)::value;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                u32x4_t xv[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int p = 8 * J + 4 * h + q;
+                    xv[h] = *reinterpret_cast<const u32x4_t*>(
+                        xl + ((16 * t + c) * 32 + ((p & 16) | ((p ^ c) & 15))) * 16);
+                }
+                acc[t] = mfma<J>(wb[slot][J], xv[0], xv[1], acc[t], ws[slot], xsc[slot][t]);
+            }
+        };
+        group(std::integral_constant<int, 0>{});
+        group(std::integral_constant<int, 1>{});
+        group(std::integral_constant<int, 2>{});
+        group(std::integral_constant<int, 3>{});
+    };
+    load(0, 0);
+    stage(0);
+    __syncthreads();
+    auto step = [&](auto sc, int it) {
+        constexpr int slot = decltype(sc)::value;
+        load(slot ^ 1, it + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        product(sc);
+        __builtin_amdgcn_sched_barrier(0);
+        stage(slot ^ 1);
+        __syncthreads();
+    };
+    for (int it = 0; it < its; it += 2) {
+        step(std::integral_constant<int, 0>{}, it);
+        if (it + 1 >= its) break;
+        step(std::integral_constant<int, 1>{}, it + 1);
+    }
+
+    // the k groups' sums in their order
+    float* red = reinterpret_cast<float*>(lds);         // [KW][WN][MT][256]
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+        *reinterpret_cast<f32x4_t*>(red + (w * MT + t) * 256 + lane * 4) = acc[t];
+    __syncthreads();
+    constexpr int kCols = 16 * WN;
+    for (int i = tid; i < 16 * MT * kCols; i += T::kThreads) {
+        const int m = i / kCols, col = i % kCols;
+        const int64_t nn = (int64_t)bn * kCols + col;
+        if (m0 + m >= a.M || nn >= a.N) continue;
+        const int wr = col & 15, in = ((wr >> 2) * 16 + (m & 15)) * 4 + (wr & 3);
+        const int from = ((col >> 4) * MT + (m >> 4)) * 256 + in;
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) s += red[k * WN * MT * 256 + from];
+        if (a.S > 1)
+            a.part[((int64_t)blockIdx.y * a.M + m0 + m) * a.N + nn] = s;
+        else
+            store_y(a, m0 + m, nn, s);
+    }
+}
+
+// ---- many rows of x -------------------------------------------------------------
+// A workgroup of WN waves computes 16 MT rows of x by 16 R WN weight rows; a wave all
+// the rows by 16 R, its sums in registers.  Weight pieces go from memory to registers
+// in the layout the matrix instructions take them, AHEAD groups ahead; x through LDS,
+// double-buffered, where the waves share it, asked for one group ahead: row m of a group
+// is 8 pieces of 16 bytes, piece p at place p ^ (m / 2 & 7), so that two rows fill the
+// 16 places that are served at once (a read's rows as in mid_kernel).  x's scales go
+// through LDS too, by quads of groups.
+template <int MT, int R, int WN>
+struct Tile {
+    static constexpr int kThreads = WN * 64;
+    static constexpr int BM = 16 * MT, BN = 16 * R * WN;
+    static constexpr int kAllPieces = BM * 8;                               // of x a group
+    static constexpr int kPieces = (kAllPieces + kThreads - 1) / kThreads;  // a thread
+    static constexpr int kStage = kPieces * kThreads * 16;
+};
+
+template <int MT, int R, int WN, int AHEAD, int WGS>
+__global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, int nb) {
+    using T = Tile<MT, R, WN>;
+    constexpr int P = T::kPieces;
+    // x comes in kRuns runs of H pieces a step, each asked for when the one before is
+    // stored: no more in flight than the registers that 8 x 4 sums leave
+    constexpr int kRuns = P >= 4 ? 4 : 1, H = P / kRuns;
+    static_assert(P % kRuns == 0 && MT % kRuns == 0, "whole runs");
+    __shared__ __align__(16) uint8_t xs[2][T::kStage];
+    __shared__ __align__(16) uint8_t ss[2][T::kThreads * 8];      // (BM rows are read)
+
+    // Consecutive workgroups go to the 8 XCDs in turn: give each XCD a run of
+    // neighbouring tiles, rows of x fastest, so that its L2 serves their x and W.
+    const int total = mb * nb;
+    int id = blockIdx.x;
+    {
+        const int per = total / 8, extra = total % 8, xcd = id % 8;
+        id = xcd * per + (xcd < extra ? xcd : extra) + id / 8;
+    }
+    const int group_n = 8;                      // tiles of W beside each other
+    const int band = group_n * mb;
+    const int n_first = id / band * group_n;
+    const int width = nb - n_first < group_n ? nb - n_first : group_n;
+    const int bn = n_first + id % band % width;
+    const int bm = id % band / width;
+    const int slice = blockIdx.y;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int m0 = bm * T::BM;
+    const int gb = slice * a.gs;                // first group, a multiple of 4
+    const int ge = gb + a.gs < a.G ? gb + a.gs : a.G;
+
+    const int64_t last_tile = tiles(a.N) - 1;
+    const uint8_t* wp[R];
+    const uint8_t* sp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        int64_t t = (int64_t)bn * (T::BN / 16) + w * R + r;
+        if (t > last_tile) t = last_tile;
+        wp[r] = a.w.codes + t * a.G * kCodeBlock;
+        sp[r] = a.w.scales + t * a.Q * kScaleBlock;
+    }
+    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+    // x: thread t holds piece t % 8 of rows t / 8 + 8 WN i (past the last row: the last)
+    const int p = tid & 7;
+    const uint8_t* xbase = a.x + (int64_t)m0 * a.ldv;
+    const int row_last = a.M - 1 - m0;
+    // (offsets of 128 rows less than 2^24 apart)
+    const uint32_t xfirst = (uint32_t)(tid >> 3) * (uint32_t)a.ldv;
+    const uint32_t xstride = (uint32_t)(T::kThreads / 8) * (uint32_t)a.ldv;
+    const uint32_t xlast =
+        (uint32_t)(row_last < T::BM - 1 ? row_last : T::BM - 1) * (uint32_t)a.ldv;
+    const uint8_t* sbase = a.xs + (int64_t)m0 * a.lds;
+    const int srow = (tid >> 1) % T::BM;        // its scales: half of a row's
+    const uint32_t soff =
+        (uint32_t)(srow < row_last ? srow : row_last) * (uint32_t)a.lds + 8 * (tid & 1);
+
+    u32x4_t wreg[AHEAD == 1 ? 2 : 4][R], xreg[H];
+    u32x2_t sreg;
+    bool xin = false;
+    uint32_t ws[2][R];
+    auto load_w = [&](int slot, int g) {
+        const int gg = g < ge ? g : ge - 1;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            wreg[slot][r] = load16(scalar(wp[r] + (int64_t)gg * kCodeBlock), lane16);
+    };
+    auto load_scales = [&](int slot, int g) {
+        const int o = (g < ge ? g : ge - 1) >> 2;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            ws[slot][r] = load4(scalar(sp[r] + (int64_t)o * kScaleBlock), lane4);
+        sreg = load8(scalar(sbase + 16 * (int64_t)o), soff);
+    };
+    // (no branch: a load past the last group, row or K reads a valid place and is
+    // replaced by zeros or, past the last step, never used)
+    auto load_x = [&](int run, int g) {
+        const int k = 128 * (g < ge ? g : ge - 1);
+        const bool k_in = k + 16 * p < a.K;
+        xin = g < ge && k_in;
+        const uint32_t piece = k_in ? 16u * p : 0u;
+        // (computed anew in every step: kept, the rows' offsets would cost more registers
+        // than there are)
+        uint32_t first = xfirst;
+        asm volatile("" : "+v"(first));
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const uint32_t off = first + (run * H + i) * xstride;
+            xreg[i] = load16(scalar(xbase + k), (off < xlast ? off : xlast) + piece);
+        }
+    };
+    auto store_x = [&](int run, int buf) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const int r = (tid >> 3) + (run * H + i) * (T::kThreads / 8);
+            u32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = xin ? xreg[i][e] : 0u;
+            *reinterpret_cast<u32x4_t*>(&xs[buf][r * 128 + ((p ^ (r >> 1 & 7)) << 4)]) = v;
+        }
+    };
+    auto store_scales = [&](int buf) {
+        *reinterpret_cast<u32x2_t*>(&ss[buf][tid * 8]) = sreg;
+    };
+    static_assert(T::kThreads >= 2 * T::BM, "two threads for each row's scales");
+
+    f32x4_t acc[MT][R];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[i][r] = f32x4_t{0, 0, 0, 0};
+
+    load_scales(0, gb);
+    load_w(0, gb);
+    if constexpr (AHEAD == 2) load_w(1, gb + 1);
+#pragma unroll
+    for (int run = 0; run < kRuns; ++run) {
+        load_x(run, gb);
+        store_x(run, 0);
+    }
+    store_scales(0);
+    __syncthreads();
+
+    auto step = [&](auto jc, int g, int quad) {
+        constexpr int J = decltype(jc)::value;
+        constexpr int cur = J & 1, kSlots = AHEAD == 1 ? 2 : 4;
+        load_w((J + AHEAD) % kSlots, g + AHEAD);
+        load_x(0, g + 1);
+        if constexpr (J == 2) load_scales(1, g + 2);
+        // x operands are read one tile (of 16 rows) ahead of the products on them
+        u32x4_t xv[2][2];
+        uint32_t xsc[2];
+        auto read = [&](int slot, int i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                xv[slot][h] = *reinterpret_cast<const u32x4_t*>(
+                    &xs[cur][(16 * i + c) * 128 + (((4 * h + q) ^ (c >> 1)) << 4)]);
+            xsc[slot] =
+                *reinterpret_cast<const uint32_t*>(&ss[quad & 1][(16 * i + c) * 16 + 4 * q]);
+        };
+        read(0, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            if (i + 1 < MT) read((i + 1) & 1, i + 1);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                acc[i][r] = mfma<J>(wreg[J % kSlots][r], xv[i & 1][0], xv[i & 1][1], acc[i][r],
+                                    ws[0][r], xsc[i & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            if ((i + 1) % (MT / kRuns) == 0) {
+                const int run = i / (MT / kRuns);
+                store_x(run, cur ^ 1);
+                if (run + 1 < kRuns) load_x(run + 1, g + 1);
+            }
+        }
+        if constexpr (J == 3) store_scales((quad & 1) ^ 1);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // steps run over whole quads: a group past the last has zeros for x
+    int quad = 0;
+    for (int g = gb; g < ge; g += 4, ++quad) {
+        step(std::integral_constant<int, 0>{}, g, quad);
+        step(std::integral_constant<int, 1>{}, g + 1, quad);
+        step(std::integral_constant<int, 2>{}, g + 2, quad);
+        step(std::integral_constant<int, 3>{}, g + 3, quad);
+#pragma unroll
+        for (int r = 0; r < R; ++r) ws[0][r] = ws[1][r];
+    }
+
+    // lane (c, q): row c of a 16-row tile of x, weight rows 4 q .. 4 q + 3 (both computed
+    // anew: kept, they would cost registers in the loop)
+    int again = threadIdx.x;
+    asm volatile("" : "+v"(again));
+    const int ce = again & 15, qe = again >> 4 & 3;
+    const int64_t n0 = (int64_t)bn * T::BN + w * R * 16;
+    const bool f32 = a.S > 1 || a.y_f32;
+    const int64_t ld = a.S > 1 ? a.N : a.ldy;
+    uint8_t* out = a.S > 1 ? reinterpret_cast<uint8_t*>(a.part + (int64_t)slice * a.M * a.N)
+                           : static_cast<uint8_t*>(a.y);
+    const int size = f32 ? 4 : 2;
+    // 16 bytes at a time where every row of y starts on such a boundary
+    const bool wide = ld % (16 / size) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t m = m0 + 16 * i + ce;
+        uint8_t* o = out + (m * ld + n0) * size;
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+            if (!f32 && wide && n0 + 16 * (r + 2) <= a.N) {
+                // BF16: lanes q and q ^ 1 trade halves of two tiles, and hold eight outputs
+                // in a row each (64 bytes of a row a store instead of 32)
+                const f32x4_t v = acc[i][r], v2 = acc[i][r + 1];
+                uint32_t p0 = mx4::bf16_bits(v[0]) | (uint32_t)mx4::bf16_bits(v[1]) << 16;
+                uint32_t p1 = mx4::bf16_bits(v[2]) | (uint32_t)mx4::bf16_bits(v[3]) << 16;
+                uint32_t p2 = mx4::bf16_bits(v2[0]) | (uint32_t)mx4::bf16_bits(v2[1]) << 16;
+                uint32_t p3 = mx4::bf16_bits(v2[2]) | (uint32_t)mx4::bf16_bits(v2[3]) << 16;
+                mx4::swap16(p0, p2);
+                mx4::swap16(p1, p3);
+                if (m < a.M)
+                    *reinterpret_cast<u32x4_t*>(o + 2 * (16 * (r + (qe & 1)) + 8 * (qe >> 1))) =
+                        u32x4_t{p0, p1, p2, p3};
+                continue;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int n = 16 * (r + h) + 4 * qe;
+                const f32x4_t v = acc[i][r + h];
+                const int64_t left = m < a.M ? a.N - n0 - n : 0;
+                if (f32 && wide && left >= 4) {
+                    *reinterpret_cast<f32x4_t*>(o + 4 * n) = v;
+                    continue;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (e >= left) continue;
+                    if (f32)
+                        reinterpret_cast<float*>(o)[n + e] = v[e];
+                    else
+                        reinterpret_cast<uint16_t*>(o)[n + e] = mx4::bf16_bits(v[e]);
+                }
+            }
+        }
+    }
+}
+
+// y = the slices' partial sums in slice order.
+__global__ __launch_bounds__(256) void join_kernel(GemmArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t MN = (int64_t)a.M * a.N;
+    if (i >= MN) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int v = 0; v < a.S; ++v) s += a.part[v * MN + i];
+    store_y(a, i / a.N, i % a.N, s);
+}
+
+hipError_t launch_join(const GemmArgs& a, hipStream_t s) {
+    if (a.S > 1) {
+        const int64_t MN = (int64_t)a.M * a.N;
+        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((MN + 255) / 256)), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+template <int MT, int R, int WN, int AHEAD, int WGS>
+hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
+    using T = Tile<MT, R, WN>;
+    const int mb = (a.M + T::BM - 1) / T::BM;
+    const int nb = (int)((a.N + T::BN - 1) / T::BN);
+    hipLaunchKernelGGL((tile_kernel<MT, R, WN, AHEAD, WGS>),
+                       dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S), dim3(T::kThreads), 0, s,
+                       a, mb, nb);
+    return launch_join(a, s);
+}
+
+template <int MT, int WN, int KW>
+hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
+    using T = Mid<MT, WN, KW>;
+    static_assert(T::lds() <= 65536, "more LDS than a launch gets without asking");
+    const int mb = (a.M + 16 * MT - 1) / (16 * MT);
+    const int nb = (int)((tiles(a.N) + WN - 1) / WN);
+    hipLaunchKernelGGL((mid_kernel<MT, WN, KW>), dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S),
+                       dim3(T::kThreads), T::lds(), s, a, mb, nb);
+    return launch_join(a, s);
+}
+
+// Rows of x this far apart are past the tile kernel's 32-bit offsets: the few-row kernel
+// takes them.
+constexpr int64_t kFarRows = (int64_t)1 << 24;
+
+// Kernel and split of a product.
+enum Kernel { kSmall, kMid16, kMid32, kMid48, kMid64, kTile64, kTile128 };
+struct Plan {
+    Kernel kernel;
+    int S, gs;              // K slices, groups a slice (a multiple of 4)
+};
+
+Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
+    const int Q = (int)mx4::quads(K);
+    const auto blocks = [&](int64_t bm, int64_t bn) {
+        return (M + bm - 1) / bm * ((N + bn - 1) / bn);
+    };
+    const auto slices = [](int64_t want, int64_t have) { return (want + have / 2) / have; };
+    Plan p{kSmall, 1, 4 * Q};
+    int64_t S = 1;
+    if (M <= 16) {
+        p.kernel = kSmall;
+    } else if (M <= 64) {
+        p.kernel = M <= 32 ? kMid32 : M <= 48 ? kMid48 : kMid64;
+        if (K >= 4096) S = slices(512, blocks(64, 64));
+    } else if (blocks(128, 256) >= 440) {
+        p.kernel = kTile128;
+    } else {
+        p.kernel = kTile64;
+        if (K >= 4096) S = slices(640, blocks(64, 128));
+    }
+    if (S > Q) S = Q;
+    if (S < 1) S = 1;
+    const int qs = (int)((Q + S - 1) / S);      // quads a slice
+    p.S = (Q + qs - 1) / qs;
+    p.gs = 4 * qs;
+    return p;
+}
+
 }  // namespace
 
-size_t gemm_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M == 0) return 0;
+    const Plan p = plan_gemm(M, N, K);
+    return p.S > 1 ? (size_t)p.S * M * N * 4 : 0;
+}
 
-hipError_t launch_gemm(GemmArgs a, void*, hipStream_t s) { return launch_small<2, 4>(a, s); }
+hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
+    const Plan p = plan_gemm(a.M, a.N, a.K);
+    a.S = p.S;
+    a.gs = p.gs;
+    a.part = static_cast<float*>(ws);
+    Kernel k = p.kernel;
+    if (k >= kTile64 && (a.ldv >= kFarRows || a.lds >= kFarRows)) k = kSmall;
+    if (k == kSmall) a.S = 1;
+    switch (k) {
+        case kMid16: return launch_mid<1, 4, 2>(a, s);
+        case kMid32: return launch_mid<2, 4, 1>(a, s);
+        case kMid48: return launch_mid<3, 4, 1>(a, s);
+        case kMid64: return launch_mid<4, 4, 1>(a, s);
+        case kTile64: return launch_tile<4, 2, 4, 2, 2>(a, s);
+        case kTile128: return launch_tile<8, 4, 4, 1, 2>(a, s);
+        default: return launch_small<2, 4>(a, s);
+    }
+}
 
 }  // namespace mx8
