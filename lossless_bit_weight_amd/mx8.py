@@ -13,7 +13,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-from dataclasses import dataclass
 
 import torch
 
@@ -89,22 +88,41 @@ def _scale_bytes(K: int) -> int:
     return 16 * ((K + 511) // 512)
 
 
-@dataclass
 class MX8Tensor:
     """Rows of MX8: values [R, K] (float8_e4m3fn, unit column stride) and scales
     [R, 16 * ceil(K / 512)] (uint8, in include/mx8.h's order).  Rows may be cut
-    out of both together: t[3:7]."""
-    values: torch.Tensor
-    scales: torch.Tensor
+    out of both together: t[3:7].
+
+    Made from two tensors, or by this module's calls in one allocation, the
+    scales behind the values, whose views are built when they are asked for."""
+    __slots__ = ("_data", "_parts", "_values", "_scales")
+
+    def __init__(self, values: torch.Tensor, scales: torch.Tensor):
+        self._data = self._parts = None
+        self._values, self._scales = values, scales
+
+    @property
+    def values(self) -> torch.Tensor:
+        if self._values is None:
+            R, K = self._parts[:2]
+            self._values = self._data[:R * K].view(VALUES).view(R, K)
+        return self._values
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            R, K = self._parts[:2]
+            self._scales = self._data[R * K:].view(R, _scale_bytes(K))
+        return self._scales
 
     @property
     def shape(self) -> tuple:
-        return tuple(self.values.shape)
+        return tuple(self._values.shape) if self._parts is None else self._parts[:2]
 
     @property
     def block_scales(self) -> torch.Tensor:
         """The scales [R, K / 32] in the order of their blocks."""
-        R, K = self.values.shape
+        R, K = self.shape
         s = self.scales[:, :_scale_bytes(K)].unflatten(1, (-1, 4, 4)).transpose(2, 3)
         return s.flatten(1)[:, :K // BLOCK]
 
@@ -113,9 +131,14 @@ class MX8Tensor:
             raise TypeError("an MX8Tensor is cut by a slice of rows")
         return MX8Tensor(self.values[rows], self.scales[rows])
 
+    def __repr__(self) -> str:
+        return "MX8Tensor(%d, %d)" % self.shape
+
     def parts(self, what: str) -> tuple:
         """(R, K, values pointer, stride, scales pointer, stride, device)."""
-        v, s = self.values, self.scales
+        if self._parts is not None:
+            return self._parts
+        v, s = self._values, self._scales
         dev = _gpu(v, what)
         if v.dtype is not VALUES or s.dtype is not _u8:
             raise TypeError("%s must hold float8_e4m3fn values and uint8 scales, got %s and %s"
@@ -129,27 +152,30 @@ class MX8Tensor:
         return R, K, v.data_ptr(), ldv, s.data_ptr(), lds, dev
 
 
-# values and scales from one allocation, the scales behind the values
 def _new(R: int, K: int, like: torch.Tensor) -> MX8Tensor:
+    if K < BLOCK or K % BLOCK:
+        raise MX8Error(-2, "rows of (%d, %d)" % (R, K))
     n = _scale_bytes(K)
-    split = R * K
-    data = like.new_empty(split + R * n, dtype=_u8)
-    return MX8Tensor(data[:split].view(VALUES).view(R, K), data[split:].view(R, n))
+    t = MX8Tensor(None, None)
+    t._data = data = like.new_empty(R * (K + n), dtype=_u8)
+    p = data.data_ptr()
+    t._parts = (R, K, p, K, p + R * K, n, data.get_device())
+    return t
 
 
 def empty_mx8(R: int, K: int, device="cuda") -> MX8Tensor:
     """Rows of the given shape, contents undefined."""
-    if R < 0 or K < BLOCK or K % BLOCK:
+    if R < 0:
         raise MX8Error(-2, "rows of (%d, %d)" % (R, K))
     return _new(R, K, torch.empty(0, dtype=_u8, device=device))
 
 
 def _target(out, R: int, K: int, dev: int, like: torch.Tensor) -> tuple:
+    """(out or new rows, their parts)."""
     if out is None:
-        if K < BLOCK or K % BLOCK:
-            raise MX8Error(-2, "rows of (%d, %d)" % (R, K))
         out = _new(R, K, like)
-    elif out.shape != (R, K):
+        return out, out._parts
+    if out.shape != (R, K):
         raise ValueError("out holds %s, this call writes %s" % (out.shape, (R, K)))
     parts = out.parts("out")
     _same(dev, parts[-1])
@@ -177,7 +203,7 @@ def mx8_dequantize(q: MX8Tensor, out_dtype: torch.dtype = torch.bfloat16,
     if _away(dev):
         with torch.cuda.device(dev):
             return mx8_dequantize(q, out_dtype, out)
-    out, ld, yt = _output(out, R, K, out_dtype, dev, q.values)
+    out, ld, yt = _output(out, R, K, out_dtype, dev, q._values if q._data is None else q._data)
     _check(lib().mx8_dequantize(vp, ldv, sp, lds, R, K, out.data_ptr(), yt, ld, _raw_stream(dev)),
            "mx8_dequantize")
     return out
@@ -203,16 +229,16 @@ def mx8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if residual is not None:
         _same(dev, _gpu(residual, "residual"))
         rt = _type_of(residual.dtype)
-        if tuple(residual.shape) != (M, K):
+        Mr, Kr, ldr = _rows(residual, "residual")
+        if Mr != M or Kr != K:
             raise ValueError("residual is %s, x %s" % (tuple(residual.shape), (M, K)))
-        _, _, ldr = _rows(residual, "residual")
         if residual_out is None:
-            residual_out = residual.new_empty((M, K))
+            residual_out, ldo = residual.new_empty((M, K)), K
         elif residual_out.dtype != residual.dtype or tuple(residual_out.shape) != (M, K):
             raise ValueError("residual_out must be %s of the residual's type" % ((M, K),))
         else:
             _same(dev, _gpu(residual_out, "residual_out"))
-        _, _, ldo = _rows(residual_out, "residual_out")
+            _, _, ldo = _rows(residual_out, "residual_out")
         rp, op = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
