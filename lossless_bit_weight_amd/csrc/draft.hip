@@ -1,15 +1,18 @@
 // draft.hip -- verification of drafted tokens (../../include/draft.h states the
 // operation).
 //
-// Three launches.  parts: every row of logits is read once, in chunks over the GPU;
-// a chunk leaves its largest logit and its sum of powers.  rest (with the drafter's
-// probabilities): every workgroup of a sequence finds from the parts where it stops,
-// and sums max(0, p - q) over its chunk of that row.  pick: one workgroup a sequence
-// finds the chunk that the random number falls into, reads it again and finds the word.
+// Two launches, three with the drafter's probabilities.  parts: every row of logits is
+// read once, in chunks over the GPU, into registers; a chunk leaves its largest logit and
+// its sum of powers (greedy: that logit's word).  rest (with probabilities): every
+// workgroup of a sequence finds from the parts where it stops, and sums max(0, p - q) over
+// its chunk of that row.  pick: one workgroup a sequence finds the chunk that the random
+// number falls into, reads it again and finds the word.
 // Powers, probabilities and sums are fp64: a word's border in the running sum of
 // 10^5 words is then off by less than a random number of 24 bits can tell, so that
-// the word does not depend on the order of summation.  The exponential costs 19 fp64
+// the word does not depend on the order of summation.  The exponential costs 18 fp64
 // instructions a word, which run at the rate of fp32's here, beside 2 or 4 bytes read.
+#include <type_traits>
+
 #include "draft_internal.hpp"
 #include "exp64.hpp"
 
@@ -20,6 +23,8 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kMaxRowsOf = 1024;            // of a sequence: DRAFT_MAX_D + 1
 
 template <bool F32>
 struct Row {
@@ -35,19 +40,23 @@ struct Row {
         if constexpr (F32) return reinterpret_cast<const float*>(p)[v];
         return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[v] << 16);
     }
-    // Words v .. v + VEC - 1, v on a 16-byte boundary; those outside 0 .. V-1 are `none`.
+    // Words v .. v + VEC - 1, v on a 16-byte boundary.
+    __device__ __forceinline__ void whole(int v, float* f) const {
+        const u32x4_t d = *reinterpret_cast<const u32x4_t*>(p + (int64_t)v * (F32 ? 4 : 2));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (F32) {
+                f[j] = __uint_as_float(d[j]);
+            } else {
+                f[2 * j] = __uint_as_float(d[j] << 16);
+                f[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
+            }
+        }
+    }
+    // The same, those outside 0 .. V-1 as `none`.
     __device__ __forceinline__ void load(int v, int V, float none, float* f) const {
         if (v >= 0 && v + VEC <= V) {
-            const u32x4_t d = *reinterpret_cast<const u32x4_t*>(p + (int64_t)v * (F32 ? 4 : 2));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (F32) {
-                    f[j] = __uint_as_float(d[j]);
-                } else {
-                    f[2 * j] = __uint_as_float(d[j] << 16);
-                    f[2 * j + 1] = __uint_as_float(d[j] & 0xFFFF0000u);
-                }
-            }
+            whole(v, f);
         } else {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) f[j] = v + j >= 0 && v + j < V ? one(v + j) : none;
@@ -95,7 +104,31 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return a != a || b != b ? __builtin_nanf("") : a > b ? a : b;
 }
 
-template <bool F32>
+// Chunk `chunk` of a row in registers: NV vectors a thread, vector i of thread t at
+// (NEAR: NV t + i; else t + kThreads i) vectors behind the chunk's first.
+template <bool F32, int NV, bool NEAR>
+struct Chunk {
+    static constexpr int VEC = Row<F32>::VEC;
+    static constexpr int kWords = kThreads * VEC * NV;
+    float f[NV][VEC];
+
+    __device__ __forceinline__ static int word(const Row<F32>& r, int chunk, int i) {
+        return chunk * kWords - r.head +
+               (NEAR ? (int)threadIdx.x * NV + i : i * kThreads + (int)threadIdx.x) * VEC;
+    }
+    __device__ __forceinline__ void load(const Row<F32>& r, int chunk, int V) {
+        const int first = chunk * kWords - r.head;
+        if (first >= 0 && first + kWords <= V) {    // (the same for all: loads side by side)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) r.whole(word(r, chunk, i), f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) r.load(word(r, chunk, i), V, -__builtin_inff(), f[i]);
+        }
+    }
+};
+
+template <bool F32, int NV>
 __global__ __launch_bounds__(kThreads) void parts_kernel(Args a) {
     __shared__ double sums[kWaves];
     __shared__ float tops[kWaves];
@@ -106,53 +139,60 @@ __global__ __launch_bounds__(kThreads) void parts_kernel(Args a) {
     if (row >= a.B * (a.D + 1) || i > length_of(a, b)) return;
     const double rate = rate_of(a, b);
     const Row<F32> r(a.logits, b * a.ldb + i * a.ldd);
-    constexpr int VEC = Row<F32>::VEC;
-    const int first = chunk * a.size - r.head, last = first + a.size;
+    using C = Chunk<F32, NV, false>;
+    constexpr int VEC = C::VEC;
+    C c;
+    c.load(r, chunk, a.V);
 
+    // the largest as a number, and as signed and unsigned bits: +inf and a positive NaN are
+    // above all other signed numbers, a negative NaN above all other unsigned ones
     float top = -__builtin_inff();
-    int word = 0x7FFFFFFF;
-    for (int v = first + (int)threadIdx.x * VEC; v < last && v < a.V; v += kThreads * VEC) {
-        float f[VEC];
-        r.load(v, a.V, -__builtin_inff(), f);
+    int sbits = (int)0x80000000;
+    uint32_t ubits = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            if (f[j] != f[j] || f[j] == __builtin_inff()) {
-                top = __builtin_nanf("");
-            } else if (f[j] > top) {
-                top = f[j];
-                word = v + j;
-            }
+            const float f = c.f[k][j];
+            top = __builtin_fmaxf(top, f);
+            sbits = __float_as_int(f) > sbits ? __float_as_int(f) : sbits;
+            ubits = __float_as_uint(f) > ubits ? __float_as_uint(f) : ubits;
         }
-    }
+    if (sbits >= 0x7F800000 || ubits > 0xFF800000u) top = __builtin_nanf("");
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const float ot = __shfl_xor(top, d);
-        const int ow = __shfl_xor(word, d);
-        if (ot > top || (ot == top && ow < word)) word = ow;
-        top = max_nan(top, ot);
-    }
-    if ((threadIdx.x & 63) == 0) {
-        tops[threadIdx.x >> 6] = top;
-        words[threadIdx.x >> 6] = word;
-    }
+    for (int d = 32; d > 0; d >>= 1) top = max_nan(top, __shfl_xor(top, d));
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
     __syncthreads();
     top = tops[0];
-    word = words[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-        if (tops[w] > top || (tops[w] == top && words[w] < word)) word = words[w];
-        top = max_nan(top, tops[w]);
-    }
+    for (int w = 1; w < kWaves; ++w) top = max_nan(top, tops[w]);
+
     double sum = 0.0;
-    if (rate != 0.0 && top == top && top != -__builtin_inff()) {
-        for (int v = first + (int)threadIdx.x * VEC; v < last && v < a.V; v += kThreads * VEC) {
-            float f[VEC];
-            r.load(v, a.V, -__builtin_inff(), f);
+    int word = 0x7FFFFFFF;
+    if (rate == 0.0) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sum += power(f[j], top, rate);
+        for (int k = NV - 1; k >= 0; --k)
+#pragma unroll
+            for (int j = VEC - 1; j >= 0; --j)
+                word = c.f[k][j] == top ? C::word(r, chunk, k) + j : word;
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            const int o = __shfl_xor(word, d);
+            word = o < word ? o : word;
         }
+        if ((threadIdx.x & 63) == 0) words[threadIdx.x >> 6] = word;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) word = words[w] < word ? words[w] : word;
+    } else if (top > -__builtin_inff()) {
+        const double from = top, least = -1000.0 / rate;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                sum += exp2_64_low((double)c.f[k][j] - from, rate, least);
+        sum = block_sum(sum, sums);
     }
-    sum = block_sum(sum, sums);
     if (threadIdx.x == 0) a.parts[(int64_t)row * a.chunks + chunk] = Part{sum, top, word};
 }
 
@@ -164,26 +204,27 @@ struct Whole {
     __device__ __forceinline__ bool good() const { return top > -__builtin_inff(); }
 };
 
-// The wave's: from the row's chunks, in every lane.
+// From the row's chunks, by 16 lanes of a row (`lane` 0 .. 15 of them), in every one.
 __device__ __forceinline__ Whole whole(const Args& a, int64_t row, double rate, int lane) {
     const Part* p = a.parts + row * a.chunks;
     Whole w{0.0, -__builtin_inff(), 0x7FFFFFFF};
-    for (int c = lane; c < a.chunks; c += 64) {
+    for (int c = lane; c < a.chunks; c += 16) {
         const float t = p[c].top;
         if (t > w.top || (t == w.top && p[c].word < w.word)) w.word = p[c].word;
         w.top = max_nan(w.top, t);
     }
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
+    for (int d = 8; d > 0; d >>= 1) {
         const float ot = __shfl_xor(w.top, d);
         const int ow = __shfl_xor(w.word, d);
         if (ot > w.top || (ot == w.top && ow < w.word)) w.word = ow;
         w.top = max_nan(w.top, ot);
     }
-    if (!w.good() || rate == 0.0) return w;
-    for (int c = lane; c < a.chunks; c += 64) w.sum += p[c].sum * power(p[c].top, w.top, rate);
+    if (rate == 0.0) return w;
+    if (w.good())
+        for (int c = lane; c < a.chunks; c += 16) w.sum += p[c].sum * power(p[c].top, w.top, rate);
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) w.sum += __shfl_xor(w.sum, d);
+    for (int d = 8; d > 0; d >>= 1) w.sum += __shfl_xor(w.sum, d);
     return w;
 }
 
@@ -207,101 +248,108 @@ struct Stop {
     Whole row;
 };
 
-// By the whole workgroup: wave w looks at the places w, w + kWaves, ...
-__device__ __forceinline__ Stop stop_of(const Args& a, int b, double rate, int* refused,
-                                        Whole* found) {
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+// By the whole workgroup, 16 lanes a row; `rows` has a place for each.
+struct StopSpace {
+    Whole rows[kMaxRowsOf];
+    int refused;
+};
+__device__ __forceinline__ Stop stop_of(const Args& a, int b, double rate, StopSpace& space) {
+    const int lane = threadIdx.x & 15;
     const int n = length_of(a, b);
     const int64_t row0 = (int64_t)b * (a.D + 1);
-    if (threadIdx.x == 0) *refused = n;
+    if (threadIdx.x == 0) space.refused = n;
     __syncthreads();
-    for (int i = w; i < n; i += kWaves) {
+    for (int i0 = 0; i0 <= n; i0 += kThreads / 16) {
+        const int i = i0 + threadIdx.x / 16;
+        if (i > n) break;
+        // what is read of the draft's own word, beside the parts
+        const int64_t x = i < n ? draft_of(a, b, i) : -1;
+        const bool in = x >= 0 && x < a.V;
+        const float l = in && rate != 0.0 ? logit(a, b, i, x) : 0.f;
+        const double q = in && a.probs != nullptr ? (double)prob(a, b, i, x) : 1.0;
+        const double u = a.uniforms[row0 + i];
         const Whole r = whole(a, row0 + i, rate, lane);
-        const int64_t x = draft_of(a, b, i);
-        bool ok = r.good() && x >= 0 && x < a.V;
-        if (ok && rate == 0.0) {
-            ok = x == r.word;
-        } else if (ok) {
-            const double q = a.probs == nullptr ? 1.0 : (double)prob(a, b, i, x);
-            const double u = a.uniforms[row0 + i];
-            ok = u * q * r.sum < power(logit(a, b, i, x), r.top, rate);
-        }
-        if (!ok) {
-            if (lane == 0) atomicMin(refused, i);
-            break;
+        bool ok = r.good() && in;
+        if (ok) ok = rate == 0.0 ? x == r.word : u * q * r.sum < power(l, r.top, rate);
+        if (lane == 0) {
+            space.rows[i] = r;
+            if (i < n && !ok) atomicMin(&space.refused, i);
         }
     }
     __syncthreads();
     Stop s;
-    s.n = *refused;
+    s.n = space.refused;
     s.length = n;
-    if (w == 0) {
-        const Whole r = whole(a, row0 + s.n, rate, lane);
-        if (lane == 0) *found = r;
-    }
-    __syncthreads();
-    s.row = *found;
+    s.row = space.rows[s.n];
     return s;
 }
 
-// What a word is drawn by behind the accepted tokens, times the row's sum.
-template <bool F32, int VEC>
+// What the words of a chunk are drawn by behind the accepted tokens, times the row's sum.
+template <bool F32, int NV>
 struct Weights {
-    const Args& a;
-    const Stop& s;
-    double rate;
-    Row<F32> row;
-    int64_t refused;            // without probabilities: the refused draft
-    bool less;                  // take off what the drafter had
-    int b;
+    using C = Chunk<F32, NV, true>;
+    static constexpr int VEC = C::VEC;
+    double p[NV][VEC];
+    int first;                  // the thread's words are first .. first + NV VEC - 1
 
-    __device__ __forceinline__ Weights(const Args& args, const Stop& stop, double r, int seq,
-                                       bool take)
-        : a(args), s(stop), rate(r), row(args.logits, seq * args.ldb + stop.n * args.ldd),
-          refused(-1), less(take), b(seq) {
-        if (take && args.probs == nullptr) refused = draft_of(args, seq, stop.n);
-    }
-    __device__ __forceinline__ double of(int v, float l) const {
-        double p = power(l, s.row.top, rate);
-        if (less) {
-            if (a.probs == nullptr) {
-                if (v == refused) p = 0.0;
-            } else {
-                // (one instruction in every kernel: whether it is above 0 has to agree)
-                const double d = __builtin_fma(-(double)prob(a, b, s.n, v), s.row.sum, p);
-                p = d > 0.0 ? d : 0.0;
-            }
-        }
-        return p;
-    }
-    // This thread's share of a chunk's sum.
-    __device__ __forceinline__ double sum_of(int chunk) const {
-        const int first = chunk * a.size - row.head, last = first + a.size;
-        double sum = 0.0;
-        for (int v = first + (int)threadIdx.x * VEC; v < last && v < a.V; v += kThreads * VEC) {
-            float f[VEC];
-            row.load(v, a.V, -__builtin_inff(), f);
+    // less: take off what the drafter had (refused: its one word, without probabilities)
+    __device__ __forceinline__ void load(const Args& a, int b, const Stop& s, double rate,
+                                         int chunk, bool less, int64_t refused) {
+        const Row<F32> row(a.logits, b * a.ldb + s.n * a.ldd);
+        C c;
+        c.load(row, chunk, a.V);
+        first = C::word(row, chunk, 0);
+        const bool off = less && a.probs != nullptr;
+        float q[NV][VEC];
+        if (off) {
+            const int64_t at = b * a.pdb + s.n * a.pdd;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                if (f[j] != -__builtin_inff()) sum += of(v + j, f[j]);
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const int v = first + i * VEC + j;
+                    const int in = v < 0 ? 0 : v < a.V ? v : a.V - 1;
+                    q[i][j] = a.probs_f32 ? value<true>(a.probs, at + in)
+                                          : value<false>(a.probs, at + in);
+                }
         }
-        return sum;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                double w = power(c.f[i][j], s.row.top, rate);
+                if (off) {
+                    // (one instruction in every kernel: whether it is above 0 has to agree)
+                    const double d = __builtin_fma(-(double)q[i][j], s.row.sum, w);
+                    w = w > 0.0 && d > 0.0 ? d : 0.0;
+                } else if (less && first + i * VEC + j == refused) {
+                    w = 0.0;
+                }
+                p[i][j] = w;
+            }
+    }
+    __device__ __forceinline__ double sum() const {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s += p[i][j];
+        return s;
     }
 };
 
-template <bool F32>
+template <bool F32, int NV>
 __global__ __launch_bounds__(kThreads) void rest_kernel(Args a) {
     __shared__ double sums[kWaves];
-    __shared__ int refused;
-    __shared__ Whole found;
+    __shared__ StopSpace space;
     const int b = blockIdx.y * 32768 + blockIdx.z, chunk = blockIdx.x;
     if (b >= a.B) return;
     const double rate = rate_of(a, b);
-    const Stop s = stop_of(a, b, rate, &refused, &found);
+    const Stop s = stop_of(a, b, rate, space);
     if (rate == 0.0 || s.n == s.length || !s.row.good()) return;
-    constexpr int VEC = Row<F32>::VEC;
-    const Weights<F32, VEC> weights(a, s, rate, b, true);
-    const double sum = block_sum(weights.sum_of(chunk), sums);
+    Weights<F32, NV> weights;
+    weights.load(a, b, s, rate, chunk, true, -1);
+    const double sum = block_sum(weights.sum(), sums);
     if (threadIdx.x == 0) a.rest[(int64_t)b * a.chunks + chunk] = sum;
 }
 
@@ -315,44 +363,43 @@ __device__ __forceinline__ double wave_scan(double v, int lane) {
     return v;
 }
 
-template <bool F32>
+template <bool F32, int NV>
 __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
     __shared__ double sums[kWaves];
-    __shared__ int refused, where, final;
-    __shared__ Whole found;
+    __shared__ StopSpace space;
+    __shared__ int where, hit, final;
     __shared__ double below;
     const int b = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const double rate = rate_of(a, b);
-    const Stop s = stop_of(a, b, rate, &refused, &found);
+    const Stop s = stop_of(a, b, rate, space);
     const int64_t row0 = (int64_t)b * (a.D + 1);
-    constexpr int VEC = Row<F32>::VEC;
     int token = -1;
     if (s.row.good() && rate == 0.0) {
         token = s.row.word;
     } else if (s.row.good()) {
         const bool was_refused = s.n < s.length;
-        bool less = was_refused;
-        if (less && a.probs == nullptr) {
-            const int64_t x = draft_of(a, b, s.n);
-            less = x >= 0 && x < a.V;
+        // without probabilities: the refused word, if it is one
+        int64_t x = -1;
+        if (was_refused && a.probs == nullptr) {
+            x = draft_of(a, b, s.n);
+            if (x < 0 || x >= a.V) x = -1;
         }
-        // sums of the chunks: kept (the rest), or the parts' rescaled
+        const bool less = was_refused && (a.probs != nullptr || x >= 0);
+        // its chunk without it: added up again, as a difference would leave a rounding
+        // where nothing is left
+        int cx = -1;
+        double cx_sum = 0.0;
+        if (x >= 0) {
+            const Row<F32> row(a.logits, b * a.ldb + s.n * a.ldd);
+            cx = (int)((x + row.head) / Weights<F32, NV>::C::kWords);
+            Weights<F32, NV> weights;
+            weights.load(a, b, s, rate, cx, true, x);
+            cx_sum = block_sum(weights.sum(), sums);
+        }
         const Part* part = a.parts + (row0 + s.n) * a.chunks;
         const double* rest = a.rest + (int64_t)b * a.chunks;
-        const auto chunk_of = [&](int64_t v) {
-            const Row<F32> r(a.logits, b * a.ldb + s.n * a.ldd);
-            return (int)((v + r.head) / a.size);
-        };
-        const int64_t x = less && a.probs == nullptr ? draft_of(a, b, s.n) : -1;
-        const int cx = x >= 0 ? chunk_of(x) : -1;
-        // the refused draft's chunk without it: added up again, as a difference would leave
-        // a rounding where nothing is left
-        double cx_sum = 0.0;
-        if (cx >= 0) {
-            const Weights<F32, VEC> weights(a, s, rate, b, true);
-            cx_sum = block_sum(weights.sum_of(cx), sums);
-        }
         auto chunk_sum = [&](int c, bool off) {
+            if (c >= a.chunks) return 0.0;
             if (off && a.probs != nullptr) return rest[c];
             if (off && c == cx) return cx_sum;
             return part[c].sum * power(part[c].top, s.row.top, rate);
@@ -364,8 +411,7 @@ __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
             for (int pass = 0; pass < 2; ++pass) {
                 total = 0.0;
                 for (int c0 = 0; c0 < a.chunks; c0 += 64)
-                    total += __shfl(wave_scan(c0 + lane < a.chunks ? chunk_sum(c0 + lane, off) : 0.0,
-                                              lane), 63);
+                    total += __shfl(wave_scan(chunk_sum(c0 + lane, off), lane), 63);
                 if (total > 0.0 || !off) break;
                 off = false;
             }
@@ -373,75 +419,59 @@ __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
             double run = 0.0, before = 0.0;
             int at = -1;
             for (int c0 = 0; c0 < a.chunks && at < 0; c0 += 64) {
-                const double v = c0 + lane < a.chunks ? chunk_sum(c0 + lane, off) : 0.0;
+                const double v = chunk_sum(c0 + lane, off);
                 const double inc = wave_scan(v, lane);
-                const uint64_t hit = __ballot(run + inc > aim && v > 0.0);
-                if (hit != 0) {
-                    const int src = __builtin_ctzll(hit);
+                const uint64_t found = __ballot(run + inc > aim && v > 0.0);
+                if (found != 0) {
+                    const int src = __builtin_ctzll(found);
                     at = c0 + src;
                     before = run + __shfl(inc - v, src);
                 }
                 run += __shfl(inc, 63);
             }
-            if (at < 0) {           // the last chunk of positive weight
+            bool last = false;
+            if (at < 0) {           // the last word of the last chunk of positive weight
+                last = true;
                 for (int c0 = 0; c0 < a.chunks; c0 += 64) {
-                    const double v = c0 + lane < a.chunks ? chunk_sum(c0 + lane, off) : 0.0;
-                    const uint64_t some = __ballot(v > 0.0);
+                    const uint64_t some = __ballot(chunk_sum(c0 + lane, off) > 0.0);
                     if (some != 0) at = c0 + 63 - __builtin_clzll(some);
                 }
-                before = -1.0;      // its last word
             }
             if (lane == 0) {
                 where = off ? at : -1 - at;
-                below = before < 0.0 ? __builtin_inf() : aim - before;
+                below = last ? __builtin_inf() : aim - before;
+                hit = 0x7FFFFFFF;
+                final = -1;
             }
         }
         __syncthreads();
-        less = where >= 0;
-        const int chunk = less ? where : -1 - where;
-        const double aim = below;
-        const Weights<F32, VEC> weights(a, s, rate, b, less);
-        const int first = chunk * a.size - weights.row.head, last = first + a.size;
-        double run = 0.0;
-        int hit = 0x7FFFFFFF, most = -1;
-        for (int v0 = first; v0 < last && v0 < a.V; v0 += kThreads * VEC) {
-            const int v = v0 + (int)threadIdx.x * VEC;
-            double p[VEC], mine = 0.0;
-            float f[VEC];
-            weights.row.load(v, v < last ? a.V : 0, -__builtin_inff(), f);
+        const bool off = where >= 0;
+        Weights<F32, NV> weights;
+        weights.load(a, b, s, rate, off ? where : -1 - where, off, x);
+        const double mine = weights.sum(), inc = wave_scan(mine, lane);
+        if (lane == 63) sums[w] = inc;
+        __syncthreads();
+        double at = inc - mine;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                p[j] = f[j] != -__builtin_inff() ? weights.of(v + j, f[j]) : 0.0;
-                mine += p[j];
-            }
-            const double inc = wave_scan(mine, lane);
-            __syncthreads();
-            if (lane == 63) sums[w] = inc;
-            __syncthreads();
-            double at = run + inc - mine;
+        for (int k = 0; k < kWaves; ++k)
+            if (k < w) at += sums[k];
+        int first_hit = 0x7FFFFFFF, most = -1;
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k) {
-                if (k < w) at += sums[k];
-                run += sums[k];
-            }
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                at += p[j];
-                if (p[j] > 0.0) {
-                    most = v + j;
-                    if (at > aim && v + j < hit) hit = v + j;
+            for (int j = 0; j < Weights<F32, NV>::VEC; ++j) {
+                const double p = weights.p[i][j];
+                const int v = weights.first + i * Weights<F32, NV>::VEC + j;
+                at += p;
+                if (p > 0.0) {
+                    most = v;
+                    if (at > below && v < first_hit) first_hit = v;
                 }
             }
-        }
-        if (threadIdx.x == 0) {
-            refused = 0x7FFFFFFF;
-            final = -1;
-        }
+        if (first_hit != 0x7FFFFFFF) atomicMin(&hit, first_hit);
+        if (most >= 0) atomicMax(&final, most);
         __syncthreads();
-        atomicMin(&refused, hit);
-        atomicMax(&final, most);
-        __syncthreads();
-        token = refused != 0x7FFFFFFF ? refused : final;
+        token = hit != 0x7FFFFFFF ? hit : final;
     }
     for (int i = threadIdx.x; i <= a.D; i += kThreads)
         a.tokens[row0 + i] = i < s.n ? (int)draft_of(a, b, i) : i == s.n ? token : -1;
@@ -450,45 +480,61 @@ __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Words of a chunk.
-int chunk_size(int64_t rows, int64_t V) {
-    int size = 8192;
-    while (size > 2048 && rows * ((V + size - 1) / size) < 1024) size /= 2;
-    return size;
+// Vectors of 16 bytes a thread holds of a chunk: as many as leave the GPU some chunks.
+int vectors(int64_t rows, int64_t V, bool f32) {
+    const int64_t words = kThreads * (f32 ? 4 : 8);
+    int nv = f32 ? 8 : 4;
+    while (nv > 1 && rows * ((V + words * nv - 1) / (words * nv)) < 1024) nv /= 2;
+    return nv;
 }
-int64_t chunk_count(int64_t rows, int64_t V) {
-    const int size = chunk_size(rows, V);
+int64_t chunk_count(int64_t rows, int64_t V, bool f32) {
+    const int64_t size = (int64_t)vectors(rows, V, f32) * kThreads * (f32 ? 4 : 8);
     return (V + 7 + size - 1) / size;       // a row may start 7 words behind a boundary
 }
 
-template <bool F32>
+template <bool F32, int NV>
 hipError_t launch(const Args& a, hipStream_t s) {
     const auto grid = [&](int64_t rows) {
         const unsigned y = (unsigned)((rows + 32767) / 32768);
         return dim3((unsigned)a.chunks, y, (unsigned)(y > 1 ? 32768 : rows));
     };
-    hipLaunchKernelGGL(parts_kernel<F32>, grid((int64_t)a.B * (a.D + 1)), dim3(kThreads), 0, s, a);
-    if (a.probs != nullptr && a.D > 0)
-        hipLaunchKernelGGL(rest_kernel<F32>, grid(a.B), dim3(kThreads), 0, s, a);
-    hipLaunchKernelGGL(pick_kernel<F32>, dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((parts_kernel<F32, NV>), grid((int64_t)a.B * (a.D + 1)), dim3(kThreads), 0,
+                       s, a);
+    if (a.probs != nullptr)
+        hipLaunchKernelGGL((rest_kernel<F32, NV>), grid(a.B), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((pick_kernel<F32, NV>), dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
     return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t launch_by(int nv, const Args& a, hipStream_t s) {
+    switch (nv) {
+        case 1: return launch<F32, 1>(a, s);
+        case 2: return launch<F32, 2>(a, s);
+        case 4: return launch<F32, 4>(a, s);
+        default: break;
+    }
+    if constexpr (F32) return launch<F32, 8>(a, s);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
 
 size_t workspace_bytes(int64_t B, int64_t D, int64_t V) {
-    const int64_t chunks = chunk_count(B * (D + 1), V);
-    return up256((size_t)(B * (D + 1) * chunks) * sizeof(Part)) + (size_t)(B * chunks) * 8;
+    const int64_t rows = B * (D + 1);
+    const int64_t c32 = chunk_count(rows, V, true), c16 = chunk_count(rows, V, false);
+    const int64_t chunks = c32 > c16 ? c32 : c16;
+    return up256((size_t)(rows * chunks) * sizeof(Part)) + (size_t)(B * chunks) * 8;
 }
 
 hipError_t launch_verify(Args a, void* ws, hipStream_t s) {
     const int64_t rows = (int64_t)a.B * (a.D + 1);
-    a.size = chunk_size(rows, a.V);
-    a.chunks = (int)chunk_count(rows, a.V);
+    a.chunks = (int)chunk_count(rows, a.V, a.f32);
     a.parts = static_cast<Part*>(ws);
     a.rest = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) +
                                        up256((size_t)(rows * a.chunks) * sizeof(Part)));
-    return a.f32 ? launch<true>(a, s) : launch<false>(a, s);
+    const int nv = vectors(rows, a.V, a.f32);
+    return a.f32 ? launch_by<true>(nv, a, s) : launch_by<false>(nv, a, s);
 }
 
 }  // namespace draft

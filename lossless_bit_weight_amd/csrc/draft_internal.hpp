@@ -30,7 +30,7 @@ struct Args {
     const float* temperature;
     int* tokens;
     int* accepted;
-    int size, chunks;       // words of a chunk, chunks a row
+    int chunks;             // a row's
     // workspace
     Part* parts;            // [B (D + 1)][chunks]
     double* rest;           // [B][chunks] with probs: sums of max(0, p - q)

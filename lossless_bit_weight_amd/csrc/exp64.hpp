@@ -2,6 +2,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stdint.h>
 
 // t = n + f with n the nearest whole number, and 2^f = sum of (f ln 2)^k / k! up to
 // k = 11, whose remainder at |f| = 1/2 is 6.3e-15 relative.  Below -1100 it is 0, above
@@ -22,5 +23,28 @@ __device__ __forceinline__ double exp2_64(double t) {
     p = __builtin_fma(p, f, 0.6931471805599453);
     p = __builtin_fma(p, f, 1.0);
     return __builtin_ldexp(p, (int)n);
+}
+// 2^(d rate) for d up to 0 in fewer instructions; `least` = -1000 / rate, and below it
+// the result is 2^-1000.
+__device__ __forceinline__ double exp2_64_low(double d, double rate, double least) {
+    d = __builtin_fmax(d, least);
+    // the nearest whole number in the last bits of the sum with 3 * 2^51
+    const double shifted = __builtin_fma(d, rate, 0x1.8p52);
+    const double f = __builtin_fma(d, rate, -(shifted - 0x1.8p52));
+    double p = 4.4455382718708116e-10;
+    p = __builtin_fma(p, f, 7.054911620801123e-09);
+    p = __builtin_fma(p, f, 1.01780860092397e-07);
+    p = __builtin_fma(p, f, 1.321548679014431e-06);
+    p = __builtin_fma(p, f, 1.5252733804059841e-05);
+    p = __builtin_fma(p, f, 0.0001540353039338161);
+    p = __builtin_fma(p, f, 0.0013333558146428443);
+    p = __builtin_fma(p, f, 0.009618129107628477);
+    p = __builtin_fma(p, f, 0.05550410866482158);
+    p = __builtin_fma(p, f, 0.24022650695910072);
+    p = __builtin_fma(p, f, 0.6931471805599453);
+    p = __builtin_fma(p, f, 1.0);
+    // 2^n times p, which lies in 0.7 .. 1.5
+    const uint64_t n = (uint64_t)(uint32_t)__double2loint(shifted) << 52;
+    return __longlong_as_double((long long)((uint64_t)__double_as_longlong(p) + n));
 }
 constexpr double kLog2E = 1.4426950408889634;
