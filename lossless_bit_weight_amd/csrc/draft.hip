@@ -20,7 +20,6 @@ namespace draft {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
@@ -64,7 +63,9 @@ struct Row {
     }
 };
 
-// The sum over a workgroup, in every thread, in an order that depends on nothing.
+// The sum over a workgroup of T threads, in every thread, in an order that depends on
+// nothing.
+template <int T>
 __device__ __forceinline__ double block_sum(double v, double* part) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
@@ -73,21 +74,21 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
     __syncthreads();
     v = 0.0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += part[w];
+    for (int w = 0; w < T / 64; ++w) v += part[w];
     return v;
 }
 
 __device__ __forceinline__ int length_of(const Args& a, int b) {
-    if (a.lengths == nullptr) return a.D;
-    const int n = a.lengths[b];
+    const int n = a.lengths == nullptr ? a.D : a.lengths[b];
     return n < 0 ? 0 : n > a.D ? a.D : n;
 }
 // log2(e) / tau, or 0 for greedy
-__device__ __forceinline__ double rate_of(const Args& a, int b) {
-    if (a.temperature == nullptr) return kLog2E;
-    const float tau = a.temperature[b];
+__device__ __forceinline__ double rate_of(float tau) {
     // (an infinite one: all words of finite logits alike)
     return tau > 0.f ? __builtin_fmax(kLog2E / (double)tau, 1e-300) : 0.0;
+}
+__device__ __forceinline__ float temperature_of(const Args& a, int b) {
+    return a.temperature == nullptr ? 1.f : a.temperature[b];
 }
 __device__ __forceinline__ int64_t draft_of(const Args& a, int b, int i) {
     const int64_t at = (int64_t)b * a.D + i;
@@ -104,17 +105,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return a != a || b != b ? __builtin_nanf("") : a > b ? a : b;
 }
 
-// Chunk `chunk` of a row in registers: NV vectors a thread, vector i of thread t at
-// (NEAR: NV t + i; else t + kThreads i) vectors behind the chunk's first.
-template <bool F32, int NV, bool NEAR>
+// Chunk `chunk` of a row in the registers of T threads: NV vectors each, vector i of
+// thread t at (NEAR: NV t + i; else t + T i) vectors behind the chunk's first.
+template <bool F32, int NV, int T, bool NEAR>
 struct Chunk {
     static constexpr int VEC = Row<F32>::VEC;
-    static constexpr int kWords = kThreads * VEC * NV;
+    static constexpr int kWords = T * VEC * NV;
     float f[NV][VEC];
 
     __device__ __forceinline__ static int word(const Row<F32>& r, int chunk, int i) {
         return chunk * kWords - r.head +
-               (NEAR ? (int)threadIdx.x * NV + i : i * kThreads + (int)threadIdx.x) * VEC;
+               (NEAR ? (int)threadIdx.x * NV + i : i * T + (int)threadIdx.x) * VEC;
     }
     __device__ __forceinline__ void load(const Row<F32>& r, int chunk, int V) {
         const int first = chunk * kWords - r.head;
@@ -130,16 +131,19 @@ struct Chunk {
 
 template <bool F32, int NV>
 __global__ __launch_bounds__(kThreads) void parts_kernel(Args a) {
+    constexpr int kWaves = kThreads / 64;
     __shared__ double sums[kWaves];
     __shared__ float tops[kWaves];
     __shared__ int words[kWaves];
     const int row = blockIdx.y * 32768 + blockIdx.z;
     const int chunk = blockIdx.x;
     const int b = row / (a.D + 1), i = row % (a.D + 1);
-    if (row >= a.B * (a.D + 1) || i > length_of(a, b)) return;
-    const double rate = rate_of(a, b);
+    if (row >= a.B * (a.D + 1)) return;
+    const float tau = temperature_of(a, b);
+    if (i > length_of(a, b)) return;
+    const double rate = rate_of(tau);
     const Row<F32> r(a.logits, b * a.ldb + i * a.ldd);
-    using C = Chunk<F32, NV, false>;
+    using C = Chunk<F32, NV, kThreads, false>;
     constexpr int VEC = C::VEC;
     C c;
     c.load(r, chunk, a.V);
@@ -191,28 +195,27 @@ __global__ __launch_bounds__(kThreads) void parts_kernel(Args a) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
                 sum += exp2_64_low((double)c.f[k][j] - from, rate, least);
-        sum = block_sum(sum, sums);
+        sum = block_sum<kThreads>(sum, sums);
     }
     if (threadIdx.x == 0) a.parts[(int64_t)row * a.chunks + chunk] = Part{sum, top, word};
 }
 
-// A row as a whole.
-struct Whole {
-    double sum;         // of 2^((l - top) rate)
-    float top;          // NaN or -inf: no distribution
-    int word;           // of the largest logit
-    __device__ __forceinline__ bool good() const { return top > -__builtin_inff(); }
-};
-
 // From the row's chunks, by 16 lanes of a row (`lane` 0 .. 15 of them), in every one.
 __device__ __forceinline__ Whole whole(const Args& a, int64_t row, double rate, int lane) {
     const Part* p = a.parts + row * a.chunks;
+    // one pass: the sum is kept in powers of the largest logit so far
     Whole w{0.0, -__builtin_inff(), 0x7FFFFFFF};
     for (int c = lane; c < a.chunks; c += 16) {
-        const float t = p[c].top;
-        if (t > w.top || (t == w.top && p[c].word < w.word)) w.word = p[c].word;
-        w.top = max_nan(w.top, t);
+        const Part part = p[c];
+        if (part.top > w.top || (part.top == w.top && part.word < w.word)) w.word = part.word;
+        const float top = max_nan(w.top, part.top);
+        if (rate != 0.0 && top > -__builtin_inff()) {
+            const double old = w.sum > 0.0 ? w.sum * power(w.top, top, rate) : 0.0;
+            w.sum = old + part.sum * (part.top == top ? 1.0 : power(part.top, top, rate));
+        }
+        w.top = top;
     }
+    const float mine = w.top;
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) {
         const float ot = __shfl_xor(w.top, d);
@@ -221,8 +224,7 @@ __device__ __forceinline__ Whole whole(const Args& a, int64_t row, double rate, 
         w.top = max_nan(w.top, ot);
     }
     if (rate == 0.0) return w;
-    if (w.good())
-        for (int c = lane; c < a.chunks; c += 16) w.sum += p[c].sum * power(p[c].top, w.top, rate);
+    w.sum = w.good() && w.sum > 0.0 ? w.sum * power(mine, w.top, rate) : 0.0;
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) w.sum += __shfl_xor(w.sum, d);
     return w;
@@ -241,32 +243,29 @@ __device__ __forceinline__ float prob(const Args& a, int b, int i, int64_t v) {
     return a.probs_f32 ? value<true>(a.probs, at) : value<false>(a.probs, at);
 }
 
-// Where sequence b stops: its accepted tokens and the row behind them.
-struct Stop {
-    int n;              // accepted
-    int length;
-    Whole row;
-};
-
-// By the whole workgroup, 16 lanes a row; `rows` has a place for each.
+// By the whole workgroup of T threads, 16 lanes a row; `space` has a place for each.
 struct StopSpace {
     Whole rows[kMaxRowsOf];
     int refused;
 };
-__device__ __forceinline__ Stop stop_of(const Args& a, int b, double rate, StopSpace& space) {
+template <int T>
+__device__ __forceinline__ Stop stop_of(const Args& a, int b, StopSpace& space) {
     const int lane = threadIdx.x & 15;
-    const int n = length_of(a, b);
     const int64_t row0 = (int64_t)b * (a.D + 1);
+    // what depends on nothing first, together
+    const float tau = temperature_of(a, b);
+    const int n = length_of(a, b);
+    int i = threadIdx.x / 16;
+    int64_t x = i < a.D ? draft_of(a, b, i) : -1;
+    const double rate = rate_of(tau);
     if (threadIdx.x == 0) space.refused = n;
     __syncthreads();
-    for (int i0 = 0; i0 <= n; i0 += kThreads / 16) {
-        const int i = i0 + threadIdx.x / 16;
-        if (i > n) break;
-        // what is read of the draft's own word, beside the parts
-        const int64_t x = i < n ? draft_of(a, b, i) : -1;
-        const bool in = x >= 0 && x < a.V;
-        const float l = in && rate != 0.0 ? logit(a, b, i, x) : 0.f;
-        const double q = in && a.probs != nullptr ? (double)prob(a, b, i, x) : 1.0;
+    for (; i <= n; i += T / 16) {
+        if (i >= T / 16) x = i < n ? draft_of(a, b, i) : -1;
+        // the draft's own word, beside the parts
+        const bool in = i < n && x >= 0 && x < a.V;
+        const float l = logit(a, b, i, in ? x : 0);
+        const double q = a.probs != nullptr && in ? (double)prob(a, b, i, x) : 1.0;
         const double u = a.uniforms[row0 + i];
         const Whole r = whole(a, row0 + i, rate, lane);
         bool ok = r.good() && in;
@@ -280,49 +279,68 @@ __device__ __forceinline__ Stop stop_of(const Args& a, int b, double rate, StopS
     Stop s;
     s.n = space.refused;
     s.length = n;
+    s.rate = rate;
     s.row = space.rows[s.n];
     return s;
 }
 
+// N values of a row from word v on, on no boundary but their own (those outside 0 .. V-1
+// are some of the others).
+template <int N>
+__device__ __forceinline__ void probs_at(const Args& a, int64_t at, int v, float* q) {
+    if (v >= 0 && v + N <= a.V) {
+        if (a.probs_f32) {
+            typedef float v_t __attribute__((ext_vector_type(N), aligned(4)));
+            const v_t d = *reinterpret_cast<const v_t*>(static_cast<const float*>(a.probs) + at + v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) q[j] = d[j];
+        } else {
+            typedef uint16_t v_t __attribute__((ext_vector_type(N), aligned(2)));
+            const v_t d =
+                *reinterpret_cast<const v_t*>(static_cast<const uint16_t*>(a.probs) + at + v);
+#pragma unroll
+            for (int j = 0; j < N; ++j) q[j] = __uint_as_float((uint32_t)d[j] << 16);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int in = v + j < 0 ? 0 : v + j < a.V ? v + j : a.V - 1;
+            q[j] = a.probs_f32 ? value<true>(a.probs, at + in) : value<false>(a.probs, at + in);
+        }
+    }
+}
+
 // What the words of a chunk are drawn by behind the accepted tokens, times the row's sum.
-template <bool F32, int NV>
+template <bool F32, int NV, int T, bool NEAR>
 struct Weights {
-    using C = Chunk<F32, NV, true>;
+    using C = Chunk<F32, NV, T, NEAR>;
     static constexpr int VEC = C::VEC;
     double p[NV][VEC];
-    int first;                  // the thread's words are first .. first + NV VEC - 1
+    int word[NV];               // the first of each vector
 
     // less: take off what the drafter had (refused: its one word, without probabilities)
-    __device__ __forceinline__ void load(const Args& a, int b, const Stop& s, double rate,
-                                         int chunk, bool less, int64_t refused) {
+    __device__ __forceinline__ void load(const Args& a, int b, const Stop& s, int chunk, bool less,
+                                         int64_t refused) {
         const Row<F32> row(a.logits, b * a.ldb + s.n * a.ldd);
         C c;
         c.load(row, chunk, a.V);
-        first = C::word(row, chunk, 0);
         const bool off = less && a.probs != nullptr;
         float q[NV][VEC];
-        if (off) {
-            const int64_t at = b * a.pdb + s.n * a.pdd;
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const int v = first + i * VEC + j;
-                    const int in = v < 0 ? 0 : v < a.V ? v : a.V - 1;
-                    q[i][j] = a.probs_f32 ? value<true>(a.probs, at + in)
-                                          : value<false>(a.probs, at + in);
-                }
+        for (int i = 0; i < NV; ++i) {
+            word[i] = C::word(row, chunk, i);
+            if (off) probs_at<VEC>(a, b * a.pdb + s.n * a.pdd, word[i], q[i]);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                double w = power(c.f[i][j], s.row.top, rate);
+                double w = power(c.f[i][j], s.row.top, s.rate);
                 if (off) {
                     // (one instruction in every kernel: whether it is above 0 has to agree)
                     const double d = __builtin_fma(-(double)q[i][j], s.row.sum, w);
                     w = w > 0.0 && d > 0.0 ? d : 0.0;
-                } else if (less && first + i * VEC + j == refused) {
+                } else if (less && word[i] + j == refused) {
                     w = 0.0;
                 }
                 p[i][j] = w;
@@ -340,16 +358,16 @@ struct Weights {
 
 template <bool F32, int NV>
 __global__ __launch_bounds__(kThreads) void rest_kernel(Args a) {
-    __shared__ double sums[kWaves];
+    __shared__ double sums[kThreads / 64];
     __shared__ StopSpace space;
     const int b = blockIdx.y * 32768 + blockIdx.z, chunk = blockIdx.x;
     if (b >= a.B) return;
-    const double rate = rate_of(a, b);
-    const Stop s = stop_of(a, b, rate, space);
-    if (rate == 0.0 || s.n == s.length || !s.row.good()) return;
-    Weights<F32, NV> weights;
-    weights.load(a, b, s, rate, chunk, true, -1);
-    const double sum = block_sum(weights.sum(), sums);
+    const Stop s = stop_of<kThreads>(a, b, space);
+    if (chunk == 0 && threadIdx.x == 0) a.stops[b] = s;
+    if (s.rate == 0.0 || s.n == s.length || !s.row.good()) return;
+    Weights<F32, NV, kThreads, false> weights;
+    weights.load(a, b, s, chunk, true, -1);
+    const double sum = block_sum<kThreads>(weights.sum(), sums);
     if (threadIdx.x == 0) a.rest[(int64_t)b * a.chunks + chunk] = sum;
 }
 
@@ -363,18 +381,24 @@ __device__ __forceinline__ double wave_scan(double v, int lane) {
     return v;
 }
 
-template <bool F32, int NV>
-__global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
-    __shared__ double sums[kWaves];
+// T threads of NV vectors: the chunks are those of parts_kernel.
+template <bool F32, int NV, int T>
+__global__ __launch_bounds__(T) void pick_kernel(Args a) {
+    __shared__ double sums[T / 64];
     __shared__ StopSpace space;
     __shared__ int where, hit, final;
     __shared__ double below;
     const int b = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const double rate = rate_of(a, b);
-    const Stop s = stop_of(a, b, rate, space);
     const int64_t row0 = (int64_t)b * (a.D + 1);
+    const double u = a.uniforms[row0 + a.D];
+    Stop s;
+    if (a.probs != nullptr)
+        s = a.stops[b];             // as rest_kernel found it
+    else
+        s = stop_of<T>(a, b, space);
     int token = -1;
-    if (s.row.good() && rate == 0.0) {
+    using W = Weights<F32, NV, T, true>;
+    if (s.row.good() && s.rate == 0.0) {
         token = s.row.word;
     } else if (s.row.good()) {
         const bool was_refused = s.n < s.length;
@@ -391,10 +415,10 @@ __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
         double cx_sum = 0.0;
         if (x >= 0) {
             const Row<F32> row(a.logits, b * a.ldb + s.n * a.ldd);
-            cx = (int)((x + row.head) / Weights<F32, NV>::C::kWords);
-            Weights<F32, NV> weights;
-            weights.load(a, b, s, rate, cx, true, x);
-            cx_sum = block_sum(weights.sum(), sums);
+            cx = (int)((x + row.head) / W::C::kWords);
+            W weights;
+            weights.load(a, b, s, cx, true, x);
+            cx_sum = block_sum<T>(weights.sum(), sums);
         }
         const Part* part = a.parts + (row0 + s.n) * a.chunks;
         const double* rest = a.rest + (int64_t)b * a.chunks;
@@ -402,25 +426,30 @@ __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
             if (c >= a.chunks) return 0.0;
             if (off && a.probs != nullptr) return rest[c];
             if (off && c == cx) return cx_sum;
-            return part[c].sum * power(part[c].top, s.row.top, rate);
+            return part[c].sum * power(part[c].top, s.row.top, s.rate);
         };
-        // wave 0: the whole sum, then the chunk
+        // wave 0: the whole sum, then the chunk (64 chunks and fewer: both from one scan)
         if (w == 0) {
-            double total = 0.0;
+            double total = 0.0, v = 0.0, inc = 0.0;
             bool off = less;
             for (int pass = 0; pass < 2; ++pass) {
                 total = 0.0;
-                for (int c0 = 0; c0 < a.chunks; c0 += 64)
-                    total += __shfl(wave_scan(chunk_sum(c0 + lane, off), lane), 63);
+                for (int c0 = 0; c0 < a.chunks; c0 += 64) {
+                    v = chunk_sum(c0 + lane, off);
+                    inc = wave_scan(v, lane);
+                    total += __shfl(inc, 63);
+                }
                 if (total > 0.0 || !off) break;
                 off = false;
             }
-            const double aim = (double)a.uniforms[row0 + a.D] * total;
+            const double aim = u * total;
             double run = 0.0, before = 0.0;
             int at = -1;
             for (int c0 = 0; c0 < a.chunks && at < 0; c0 += 64) {
-                const double v = chunk_sum(c0 + lane, off);
-                const double inc = wave_scan(v, lane);
+                if (a.chunks > 64) {
+                    v = chunk_sum(c0 + lane, off);
+                    inc = wave_scan(v, lane);
+                }
                 const uint64_t found = __ballot(run + inc > aim && v > 0.0);
                 if (found != 0) {
                     const int src = __builtin_ctzll(found);
@@ -446,22 +475,22 @@ __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
         }
         __syncthreads();
         const bool off = where >= 0;
-        Weights<F32, NV> weights;
-        weights.load(a, b, s, rate, off ? where : -1 - where, off, x);
+        W weights;
+        weights.load(a, b, s, off ? where : -1 - where, off, x);
         const double mine = weights.sum(), inc = wave_scan(mine, lane);
         if (lane == 63) sums[w] = inc;
         __syncthreads();
         double at = inc - mine;
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k)
+        for (int k = 0; k < T / 64; ++k)
             if (k < w) at += sums[k];
         int first_hit = 0x7FFFFFFF, most = -1;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < Weights<F32, NV>::VEC; ++j) {
+            for (int j = 0; j < W::VEC; ++j) {
                 const double p = weights.p[i][j];
-                const int v = weights.first + i * Weights<F32, NV>::VEC + j;
+                const int v = weights.word[i] + j;
                 at += p;
                 if (p > 0.0) {
                     most = v;
@@ -473,7 +502,7 @@ __global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
         __syncthreads();
         token = hit != 0x7FFFFFFF ? hit : final;
     }
-    for (int i = threadIdx.x; i <= a.D; i += kThreads)
+    for (int i = threadIdx.x; i <= a.D; i += T)
         a.tokens[row0 + i] = i < s.n ? (int)draft_of(a, b, i) : i == s.n ? token : -1;
     if (threadIdx.x == 0) a.accepted[b] = s.n;
 }
@@ -502,7 +531,9 @@ hipError_t launch(const Args& a, hipStream_t s) {
                        s, a);
     if (a.probs != nullptr)
         hipLaunchKernelGGL((rest_kernel<F32, NV>), grid(a.B), dim3(kThreads), 0, s, a);
-    hipLaunchKernelGGL((pick_kernel<F32, NV>), dim3((unsigned)a.B), dim3(kThreads), 0, s, a);
+    constexpr int kWide = NV >= 4 ? 4 : 1;      // a long chunk over more threads
+    hipLaunchKernelGGL((pick_kernel<F32, NV / kWide, kThreads * kWide>), dim3((unsigned)a.B),
+                       dim3(kThreads * kWide), 0, s, a);
     return hipGetLastError();
 }
 
@@ -524,15 +555,19 @@ size_t workspace_bytes(int64_t B, int64_t D, int64_t V) {
     const int64_t rows = B * (D + 1);
     const int64_t c32 = chunk_count(rows, V, true), c16 = chunk_count(rows, V, false);
     const int64_t chunks = c32 > c16 ? c32 : c16;
-    return up256((size_t)(rows * chunks) * sizeof(Part)) + (size_t)(B * chunks) * 8;
+    return up256((size_t)(rows * chunks) * sizeof(Part)) + up256((size_t)B * sizeof(Stop)) +
+           (size_t)(B * chunks) * 8;
 }
 
 hipError_t launch_verify(Args a, void* ws, hipStream_t s) {
     const int64_t rows = (int64_t)a.B * (a.D + 1);
     a.chunks = (int)chunk_count(rows, a.V, a.f32);
-    a.parts = static_cast<Part*>(ws);
-    a.rest = reinterpret_cast<double*>(static_cast<uint8_t*>(ws) +
-                                       up256((size_t)(rows * a.chunks) * sizeof(Part)));
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    a.parts = reinterpret_cast<Part*>(p);
+    p += up256((size_t)(rows * a.chunks) * sizeof(Part));
+    a.stops = reinterpret_cast<Stop*>(p);
+    p += up256((size_t)a.B * sizeof(Stop));
+    a.rest = reinterpret_cast<double*>(p);
     const int nv = vectors(rows, a.V, a.f32);
     return a.f32 ? launch_by<true>(nv, a, s) : launch_by<false>(nv, a, s);
 }

@@ -15,6 +15,21 @@ struct Part {
     int word;
 };
 
+// A row as a whole.
+struct Whole {
+    double sum;         // of 2^((l - top) rate)
+    float top;          // NaN or -inf: no distribution
+    int word;           // of the largest logit
+    __device__ __forceinline__ bool good() const { return top > -__builtin_inff(); }
+};
+
+// Where a sequence stops: its accepted tokens and the row behind them.
+struct Stop {
+    Whole row;
+    double rate;        // log2(e) / tau, 0: greedy
+    int n, length;      // accepted, drafted
+};
+
 struct Args {
     const void* logits;
     int f32;
@@ -33,7 +48,8 @@ struct Args {
     int chunks;             // a row's
     // workspace
     Part* parts;            // [B (D + 1)][chunks]
-    double* rest;           // [B][chunks] with probs: sums of max(0, p - q)
+    Stop* stops;            // [B], with probs
+    double* rest;           // [B][chunks], with probs: sums of max(0, p - q)
 };
 
 size_t workspace_bytes(int64_t B, int64_t D, int64_t V);
