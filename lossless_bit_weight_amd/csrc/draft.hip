@@ -371,14 +371,27 @@ __global__ __launch_bounds__(kThreads) void rest_kernel(Args a) {
     if (threadIdx.x == 0) a.rest[(int64_t)b * a.chunks + chunk] = sum;
 }
 
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ double wave_scan(double v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
+// Inclusive sum over the lanes of a wave: along the rows of 16 lanes, then over the rows.
+__device__ __forceinline__ double wave_scan(double v) {
+    const auto add = [&](auto ctrl, auto rows) {
+        constexpr int C = decltype(ctrl)::value, R = decltype(rows)::value;
+        const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), C, R, 0xF, false);
+        const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), C, R, 0xF, false);
+        v += __hiloint2double(hi, lo);
+    };
+    using std::integral_constant;
+    add(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});    // row_shr:1
+    add(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});    // row_shr:2
+    add(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});    // row_shr:4
+    add(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});    // row_shr:8
+    add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});    // row_bcast:15
+    add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});    // row_bcast:31
     return v;
+}
+// A lane's value, the same lane for all.
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                            __builtin_amdgcn_readlane(__double2loint(v), lane));
 }
 
 // T threads of NV vectors: the chunks are those of parts_kernel.
@@ -409,19 +422,23 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
             if (x < 0 || x >= a.V) x = -1;
         }
         const bool less = was_refused && (a.probs != nullptr || x >= 0);
-        // its chunk without it: added up again, as a difference would leave a rounding
-        // where nothing is left
+        const Part* part = a.parts + (row0 + s.n) * a.chunks;
+        const double* rest = a.rest + (int64_t)b * a.chunks;
+        // the refused word's chunk without it: their difference, but where that is next to
+        // nothing (and would keep a rounding where nothing is left) added up again
         int cx = -1;
         double cx_sum = 0.0;
         if (x >= 0) {
             const Row<F32> row(a.logits, b * a.ldb + s.n * a.ldd);
             cx = (int)((x + row.head) / W::C::kWords);
-            W weights;
-            weights.load(a, b, s, cx, true, x);
-            cx_sum = block_sum<T>(weights.sum(), sums);
+            const double all = part[cx].sum * power(part[cx].top, s.row.top, s.rate);
+            cx_sum = all - power(row.one((int)x), s.row.top, s.rate);
+            if (!(cx_sum > 1e-6 * all)) {
+                W weights;
+                weights.load(a, b, s, cx, true, x);
+                cx_sum = block_sum<T>(weights.sum(), sums);
+            }
         }
-        const Part* part = a.parts + (row0 + s.n) * a.chunks;
-        const double* rest = a.rest + (int64_t)b * a.chunks;
         auto chunk_sum = [&](int c, bool off) {
             if (c >= a.chunks) return 0.0;
             if (off && a.probs != nullptr) return rest[c];
@@ -436,8 +453,8 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
                 total = 0.0;
                 for (int c0 = 0; c0 < a.chunks; c0 += 64) {
                     v = chunk_sum(c0 + lane, off);
-                    inc = wave_scan(v, lane);
-                    total += __shfl(inc, 63);
+                    inc = wave_scan(v);
+                    total += lane_value(inc, 63);
                 }
                 if (total > 0.0 || !off) break;
                 off = false;
@@ -448,15 +465,15 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
             for (int c0 = 0; c0 < a.chunks && at < 0; c0 += 64) {
                 if (a.chunks > 64) {
                     v = chunk_sum(c0 + lane, off);
-                    inc = wave_scan(v, lane);
+                    inc = wave_scan(v);
                 }
                 const uint64_t found = __ballot(run + inc > aim && v > 0.0);
                 if (found != 0) {
                     const int src = __builtin_ctzll(found);
                     at = c0 + src;
-                    before = run + __shfl(inc - v, src);
+                    before = run + lane_value(inc - v, src);
                 }
-                run += __shfl(inc, 63);
+                run += lane_value(inc, 63);
             }
             bool last = false;
             if (at < 0) {           // the last word of the last chunk of positive weight
@@ -477,7 +494,7 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
         const bool off = where >= 0;
         W weights;
         weights.load(a, b, s, off ? where : -1 - where, off, x);
-        const double mine = weights.sum(), inc = wave_scan(mine, lane);
+        const double mine = weights.sum(), inc = wave_scan(mine);
         if (lane == 63) sums[w] = inc;
         __syncthreads();
         double at = inc - mine;
@@ -497,8 +514,10 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
                     if (at > below && v < first_hit) first_hit = v;
                 }
             }
-        if (first_hit != 0x7FFFFFFF) atomicMin(&hit, first_hit);
-        if (most >= 0) atomicMax(&final, most);
+        // the words ascend with the lanes: of a wave one lane has its first, one its last
+        const uint64_t hits = __ballot(first_hit != 0x7FFFFFFF), some = __ballot(most >= 0);
+        if (hits != 0 && lane == __builtin_ctzll(hits)) atomicMin(&hit, first_hit);
+        if (some != 0 && lane == 63 - __builtin_clzll(some)) atomicMax(&final, most);
         __syncthreads();
         token = hit != 0x7FFFFFFF ? hit : final;
     }
