@@ -69,19 +69,24 @@ def draft_workspace_bytes(B: int, D: int, V: int) -> int:
 
 def _words(t: torch.Tensor, what: str) -> tuple:
     """(strides of sequences and of rows) of a 3-D tensor with contiguous words."""
-    if t.stride(2) != 1 and t.shape[2] > 1 and t.numel():
+    ldb, ldd, unit = t.stride()
+    if unit != 1 and t.shape[2] > 1 and t.numel():
         raise ValueError("%s must have contiguous words" % what)
-    return t.stride(0), t.stride(1)
+    return ldb, ldd
 
 
-def _small(t, what: str, shape: tuple, dtypes: tuple, dev: int):
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_INTS = (torch.int32, torch.int64)
+
+
+def _small(t: torch.Tensor, what: str, shape: tuple, dtypes: tuple, dev: int) -> int:
     """The pointer of a contiguous tensor of the given shape and types."""
-    if t is None:
-        return None
-    _same(dev, _gpu(t, what))
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype not in dtypes or t.shape != shape \
+            or not t.is_contiguous():
+        _same(dev, _gpu(t, what))
+        if t.dtype not in dtypes:
+            raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
         raise ValueError("%s must be contiguous %s, got %s" % (what, shape, tuple(t.shape)))
     return t.data_ptr()
 
@@ -106,24 +111,28 @@ def draft_verify(logits: torch.Tensor, drafts: torch.Tensor, uniforms: torch.Ten
     D = rows - 1
     ldb, ldd = _words(logits, "logits")
     lt = _type_of(logits.dtype)
-    dp = _small(drafts, "drafts", (B, D), (torch.int32, torch.int64), dev)
-    up = _small(uniforms, "uniforms", (B, rows), (torch.float32,), dev)
-    np_ = _small(lengths, "lengths", (B,), (torch.int32,), dev)
-    tp = _small(temperature, "temperature", (B,), (torch.float32,), dev)
+    dp = _small(drafts, "drafts", (B, D), _INTS, dev)
+    up = _small(uniforms, "uniforms", (B, rows), _F32, dev)
+    np_ = None if lengths is None else _small(lengths, "lengths", (B,), _I32, dev)
+    tp = None if temperature is None else _small(temperature, "temperature", (B,), _F32, dev)
     qp, qt, pdb, pdd = None, 0, 0, 0
     if draft_probs is not None:
-        _same(dev, _gpu(draft_probs, "draft_probs"))
-        if tuple(draft_probs.shape) != (B, D, V):
+        if draft_probs.get_device() != dev or draft_probs.shape != (B, D, V):
+            _same(dev, _gpu(draft_probs, "draft_probs"))
             raise ValueError("draft_probs must be %s, got %s"
                              % ((B, D, V), tuple(draft_probs.shape)))
         qp, qt = draft_probs.data_ptr(), _type_of(draft_probs.dtype)
         pdb, pdd = _words(draft_probs, "draft_probs")
     if tokens is None:
         tokens = logits.new_empty((B, rows), dtype=torch.int32)
+        op = tokens.data_ptr()
+    else:
+        op = _small(tokens, "tokens", (B, rows), _I32, dev)
     if accepted is None:
-        accepted = logits.new_empty((B,), dtype=torch.int32)
-    op = _small(tokens, "tokens", (B, rows), (torch.int32,), dev)
-    ap = _small(accepted, "accepted", (B,), (torch.int32,), dev)
+        accepted = logits.new_empty(B, dtype=torch.int32)
+        ap = accepted.data_ptr()
+    else:
+        ap = _small(accepted, "accepted", (B,), _I32, dev)
     keep, wsp, wsb = _workspace(draft_workspace_bytes(B, D, V), workspace, logits)
     _check(lib().draft_verify(logits.data_ptr(), lt, B, D, V, ldb, ldd, dp,
                               int(drafts.dtype is torch.int64), up, qp, qt, pdb, pdd, np_, tp, op,
