@@ -161,16 +161,16 @@ hipError_t launch_small(const GemmArgs& a, hipStream_t s) {
 
 // ---- a few rows of x, shared through LDS ------------------------------------------
 // A workgroup: 16 MT rows of x by 16 WN weight rows; KW groups of WN waves take every
-// KW-th unit of four groups of K.  A unit's weights come to registers one unit ahead of
+// KW-th unit of UG groups of K.  A unit's weights come to registers one unit ahead of
 // their products; its x goes through LDS, double-buffered, where the WN waves share it:
-// row m of a unit is 32 pieces of 16 bytes, piece p at place (p & 16) | ((p ^ m) & 15).
+// row m of a unit is 8 UG pieces of 16 bytes, piece p at place (p & 16) | ((p ^ m) & 15).
 // A read takes one piece from 16 rows for each q; the LDS serves it 16 lanes at a time,
 // rows 0-3 and 12-15 of one q with rows 4-11 of the next, which lie in 16 different
 // places then, and so do the 16 pieces that 16 lanes write.
-template <int MT, int WN, int KW>
+template <int MT, int WN, int KW, int UG>
 struct Mid {
     static constexpr int kThreads = WN * KW * 64;
-    static constexpr int kAllPieces = 16 * MT * 32;                         // of x a unit
+    static constexpr int kAllPieces = 16 * MT * 8 * UG;                         // of x a unit
     static constexpr int kPieces = (kAllPieces + WN * 64 - 1) / (WN * 64);  // a thread
     static constexpr int kStage = kAllPieces * 16;
     static constexpr int lds() {
@@ -179,10 +179,11 @@ struct Mid {
     }
 };
 
-template <int MT, int WN, int KW>
+template <int MT, int WN, int KW, int UG>
 __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, int nb) {
-    using T = Mid<MT, WN, KW>;
-    constexpr int P = T::kPieces;
+    using T = Mid<MT, WN, KW, UG>;
+    constexpr int P = T::kPieces, kRow = 8 * UG;
+    static_assert(UG == 4 || (UG == 2 && KW == 1), "a unit's place in its scales' dword is its slot");
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -198,8 +199,9 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         bm = i / width;
     }
     const int m0 = bm * 16 * MT;
-    const int u0 = blockIdx.y * (a.gs / 4);
-    const int u1 = u0 + a.gs / 4 < a.Q ? u0 + a.gs / 4 : a.Q;
+    const int U = (a.G + UG - 1) / UG;
+    const int u0 = blockIdx.y * (a.gs / UG);
+    const int u1 = u0 + a.gs / UG < U ? u0 + a.gs / UG : U;
     const int its = (u1 - u0 + KW - 1) / KW;
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
 
@@ -219,8 +221,8 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         int piece = (i * WN + wn) * 64 + lane;
         if (T::kAllPieces % (WN * 64) != 0 && piece > T::kAllPieces - 64 + lane)
             piece = T::kAllPieces - 64 + lane;
-        const int row = piece / 32, p = piece % 32;
-        at[i] = (row * 32 + ((p & 16) | ((p ^ row) & 15))) * 16;
+        const int row = piece / kRow, p = piece % kRow;
+        at[i] = (row * kRow + ((p & 16) | ((p ^ row) & 15))) * 16;
         const int m = m0 + row < a.M ? m0 + row : a.M - 1;
         xp[i] = a.x + (int64_t)m * a.ldv;
         xk[i] = 16 * p;
@@ -231,7 +233,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         const int m = m0 + 16 * t + c < a.M ? m0 + 16 * t + c : a.M - 1;
         xs[t] = a.xs + (int64_t)m * a.lds + 4 * q;
     }
-    u32x4_t wb[2][4], xb[P];
+    u32x4_t wb[2][UG], xb[P];
     uint32_t ws[2], xsc[2][MT];
     bool xin[P];
     // (no branch: a place past the last unit, group or K is a valid one whose x is
@@ -239,22 +241,22 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
     auto load = [&](int slot, int it) {
         const int u = u0 + it * KW + kw;
         const int uc = u < u1 ? u : u1 - 1;
-        ws[slot] = load4(scalar(sp + (int64_t)uc * kScaleBlock), lane4);
+        ws[slot] = load4(scalar(sp + (int64_t)(uc * UG / 4) * kScaleBlock), lane4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int g = uc * 4 + j < a.G ? uc * 4 + j : a.G - 1;
+        for (int j = 0; j < UG; ++j) {
+            const int g = uc * UG + j < a.G ? uc * UG + j : a.G - 1;
             const global_t from = scalar(wp + (int64_t)g * kCodeBlock);
             wb[slot][j] = MT == 1 ? load16_nt(from, lane16) : load16(from, lane16);
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int k = u * 512 + xk[i];
+            const int k = u * (128 * UG) + xk[i];
             xin[i] = u < u1 && k < a.K;
             xb[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[i] ? k : 0));
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-            xsc[slot][t] = *reinterpret_cast<const uint32_t*>(xs[t] + 16 * uc);
+            xsc[slot][t] = *reinterpret_cast<const uint32_t*>(xs[t] + 16 * (uc * UG / 4));
     };
     auto stage = [&](int buf) {
 #pragma unroll
@@ -278,17 +280,20 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
                 u32x4_t xv[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int p = 8 * J + 4 * h + q;
+                    const int p = 8 * (J % UG) + 4 * h + q;
                     xv[h] = *reinterpret_cast<const u32x4_t*>(
-                        xl + ((16 * t + c) * 32 + ((p & 16) | ((p ^ c) & 15))) * 16);
+                        xl + ((16 * t + c) * kRow + ((p & 16) | ((p ^ c) & 15))) * 16);
                 }
-                acc[t] = mfma<J>(wb[slot][J], xv[0], xv[1], acc[t], ws[slot], xsc[slot][t]);
+                acc[t] = mfma<J>(wb[slot][J % UG], xv[0], xv[1], acc[t], ws[slot], xsc[slot][t]);
             }
         };
-        group(std::integral_constant<int, 0>{});
-        group(std::integral_constant<int, 1>{});
-        group(std::integral_constant<int, 2>{});
-        group(std::integral_constant<int, 3>{});
+        constexpr int J0 = UG == 4 ? 0 : 2 * slot;
+        group(std::integral_constant<int, J0>{});
+        group(std::integral_constant<int, J0 + 1>{});
+        if constexpr (UG == 4) {
+            group(std::integral_constant<int, 2>{});
+            group(std::integral_constant<int, 3>{});
+        }
     };
     load(0, 0);
     stage(0);
@@ -348,14 +353,10 @@ struct Tile {
     static constexpr int kStage = kPieces * kThreads * 16;
 };
 
-template <int MT, int R, int WN, int AHEAD, int WGS>
-__global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, int nb) {
+template <int MT, int R, int WN, int AHEAD>
+__global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, int nb) {
     using T = Tile<MT, R, WN>;
     constexpr int P = T::kPieces;
-    // x comes in kRuns runs of H pieces a step, each asked for when the one before is
-    // stored: no more in flight than the registers that 8 x 4 sums leave
-    constexpr int kRuns = P >= 4 ? 4 : 1, H = P / kRuns;
-    static_assert(P % kRuns == 0 && MT % kRuns == 0, "whole runs");
     __shared__ __align__(16) uint8_t xs[2][T::kStage];
     __shared__ __align__(16) uint8_t ss[2][T::kThreads * 8];      // (BM rows are read)
 
@@ -392,12 +393,12 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
         wp[r] = a.w.codes + t * a.G * kCodeBlock;
         sp[r] = a.w.scales + t * a.Q * kScaleBlock;
     }
-    const uint32_t lane16 = lane * 16, lane4 = lane * 4;
+    const uint32_t lane16 = lane * 16;
     // x: thread t holds piece t % 8 of rows t / 8 + 8 WN i (past the last row: the last)
     const int p = tid & 7;
     const uint8_t* xbase = a.x + (int64_t)m0 * a.ldv;
     const int row_last = a.M - 1 - m0;
-    // (offsets of 128 rows less than 2^24 apart)
+    // (offsets of 64 rows less than 2^24 apart)
     const uint32_t xfirst = (uint32_t)(tid >> 3) * (uint32_t)a.ldv;
     const uint32_t xstride = (uint32_t)(T::kThreads / 8) * (uint32_t)a.ldv;
     const uint32_t xlast =
@@ -407,7 +408,7 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
     const uint32_t soff =
         (uint32_t)(srow < row_last ? srow : row_last) * (uint32_t)a.lds + 8 * (tid & 1);
 
-    u32x4_t wreg[AHEAD == 1 ? 2 : 4][R], xreg[H];
+    u32x4_t wreg[AHEAD == 1 ? 2 : 4][R], xreg[P];
     u32x2_t sreg;
     bool xin = false;
     uint32_t ws[2][R];
@@ -419,6 +420,9 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
     };
     auto load_scales = [&](int slot, int g) {
         const int o = (g < ge ? g : ge - 1) >> 2;
+        uint32_t lane4 = lane16;        // (computed anew: kept, it would cost a register)
+        asm volatile("" : "+v"(lane4));
+        lane4 >>= 2;
 #pragma unroll
         for (int r = 0; r < R; ++r)
             ws[slot][r] = load4(scalar(sp[r] + (int64_t)o * kScaleBlock), lane4);
@@ -426,25 +430,21 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
     };
     // (no branch: a load past the last group, row or K reads a valid place and is
     // replaced by zeros or, past the last step, never used)
-    auto load_x = [&](int run, int g) {
+    auto load_x = [&](int g) {
         const int k = 128 * (g < ge ? g : ge - 1);
         const bool k_in = k + 16 * p < a.K;
         xin = g < ge && k_in;
         const uint32_t piece = k_in ? 16u * p : 0u;
-        // (computed anew in every step: kept, the rows' offsets would cost more registers
-        // than there are)
-        uint32_t first = xfirst;
-        asm volatile("" : "+v"(first));
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const uint32_t off = first + (run * H + i) * xstride;
+        for (int i = 0; i < P; ++i) {
+            const uint32_t off = xfirst + i * xstride;
             xreg[i] = load16(scalar(xbase + k), (off < xlast ? off : xlast) + piece);
         }
     };
-    auto store_x = [&](int run, int buf) {
+    auto store_x = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const int r = (tid >> 3) + (run * H + i) * (T::kThreads / 8);
+        for (int i = 0; i < P; ++i) {
+            const int r = (tid >> 3) + i * (T::kThreads / 8);
             u32x4_t v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = xin ? xreg[i][e] : 0u;
@@ -465,11 +465,8 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
     load_scales(0, gb);
     load_w(0, gb);
     if constexpr (AHEAD == 2) load_w(1, gb + 1);
-#pragma unroll
-    for (int run = 0; run < kRuns; ++run) {
-        load_x(run, gb);
-        store_x(run, 0);
-    }
+    load_x(gb);
+    store_x(0);
     store_scales(0);
     __syncthreads();
 
@@ -477,7 +474,7 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
         constexpr int J = decltype(jc)::value;
         constexpr int cur = J & 1, kSlots = AHEAD == 1 ? 2 : 4;
         load_w((J + AHEAD) % kSlots, g + AHEAD);
-        load_x(0, g + 1);
+        load_x(g + 1);
         if constexpr (J == 2) load_scales(1, g + 2);
         // x operands are read one tile (of 16 rows) ahead of the products on them
         u32x4_t xv[2][2];
@@ -499,12 +496,8 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
                 acc[i][r] = mfma<J>(wreg[J % kSlots][r], xv[i & 1][0], xv[i & 1][1], acc[i][r],
                                     ws[0][r], xsc[i & 1]);
             __builtin_amdgcn_sched_barrier(0);
-            if ((i + 1) % (MT / kRuns) == 0) {
-                const int run = i / (MT / kRuns);
-                store_x(run, cur ^ 1);
-                if (run + 1 < kRuns) load_x(run + 1, g + 1);
-            }
         }
+        store_x(cur ^ 1);
         if constexpr (J == 3) store_scales((quad & 1) ^ 1);
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
@@ -520,11 +513,7 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
         for (int r = 0; r < R; ++r) ws[0][r] = ws[1][r];
     }
 
-    // lane (c, q): row c of a 16-row tile of x, weight rows 4 q .. 4 q + 3 (both computed
-    // anew: kept, they would cost registers in the loop)
-    int again = threadIdx.x;
-    asm volatile("" : "+v"(again));
-    const int ce = again & 15, qe = again >> 4 & 3;
+    // lane (c, q): row c of a 16-row tile of x, weight rows 4 q .. 4 q + 3
     const int64_t n0 = (int64_t)bn * T::BN + w * R * 16;
     const bool f32 = a.S > 1 || a.y_f32;
     const int64_t ld = a.S > 1 ? a.N : a.ldy;
@@ -535,7 +524,7 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
     const bool wide = ld % (16 / size) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int64_t m = m0 + 16 * i + ce;
+        const int64_t m = m0 + 16 * i + c;
         uint8_t* o = out + (m * ld + n0) * size;
 #pragma unroll
         for (int r = 0; r < R; r += 2) {
@@ -550,13 +539,13 @@ __global__ __launch_bounds__(WN * 64, WGS) void tile_kernel(GemmArgs a, int mb, 
                 mx4::swap16(p0, p2);
                 mx4::swap16(p1, p3);
                 if (m < a.M)
-                    *reinterpret_cast<u32x4_t*>(o + 2 * (16 * (r + (qe & 1)) + 8 * (qe >> 1))) =
+                    *reinterpret_cast<u32x4_t*>(o + 2 * (16 * (r + (q & 1)) + 8 * (q >> 1))) =
                         u32x4_t{p0, p1, p2, p3};
                 continue;
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int n = 16 * (r + h) + 4 * qe;
+                const int n = 16 * (r + h) + 4 * q;
                 const f32x4_t v = acc[i][r + h];
                 const int64_t left = m < a.M ? a.N - n0 - n : 0;
                 if (f32 && wide && left >= 4) {
@@ -595,24 +584,24 @@ hipError_t launch_join(const GemmArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int MT, int R, int WN, int AHEAD, int WGS>
+template <int MT, int R, int WN, int AHEAD>
 hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
     using T = Tile<MT, R, WN>;
     const int mb = (a.M + T::BM - 1) / T::BM;
     const int nb = (int)((a.N + T::BN - 1) / T::BN);
-    hipLaunchKernelGGL((tile_kernel<MT, R, WN, AHEAD, WGS>),
+    hipLaunchKernelGGL((tile_kernel<MT, R, WN, AHEAD>),
                        dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S), dim3(T::kThreads), 0, s,
                        a, mb, nb);
     return launch_join(a, s);
 }
 
-template <int MT, int WN, int KW>
+template <int MT, int WN, int KW, int UG>
 hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
-    using T = Mid<MT, WN, KW>;
+    using T = Mid<MT, WN, KW, UG>;
     static_assert(T::lds() <= 65536, "more LDS than a launch gets without asking");
     const int mb = (a.M + 16 * MT - 1) / (16 * MT);
     const int nb = (int)((tiles(a.N) + WN - 1) / WN);
-    hipLaunchKernelGGL((mid_kernel<MT, WN, KW>), dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S),
+    hipLaunchKernelGGL((mid_kernel<MT, WN, KW, UG>), dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S),
                        dim3(T::kThreads), T::lds(), s, a, mb, nb);
     return launch_join(a, s);
 }
@@ -622,32 +611,96 @@ hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
 constexpr int64_t kFarRows = (int64_t)1 << 24;
 
 // Kernel and split of a product.
-enum Kernel { kSmall, kMid16, kMid32, kMid48, kMid64, kTile64, kTile128 };
+enum Kernel { kOne4, kOne8, kTwo4, kTwo8, kMid16x2, kMid16, kMid32, kMid32x2, kTile32, kTile64,
+              kTile64x4 };
 struct Plan {
     Kernel kernel;
+    int wn;                 // kMid16: waves beside each other
     int S, gs;              // K slices, groups a slice (a multiple of 4)
 };
 
+// Waves beside each other that spread nt tiles best over 256 CUs: the CU with the most of
+// them decides, one that has a single workgroup, whose barriers nothing fills, counts a
+// fifth more (34816 x 5120, 2176 tiles, M = 1 / 16: 5 waves 17.1 / 19.5 us, 4 18.8 / 23.7).
+int spread(int64_t nt) {
+    static const int kWaves[] = {9, 7, 5, 4};
+    int best = 4;
+    int64_t least = -1;
+    for (const int w : kWaves) {
+        const int64_t most = ((nt + w - 1) / w + 255) / 256;
+        const int64_t cost = most * w * (most == 1 ? 6 : 5);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = w;
+        }
+    }
+    return best;
+}
+
+// By rows of x (M), tiles of 16 weight rows (nt), pairs of a weight tile and 16 rows of x
+// (t) and groups of K (G).  us, graphs over weights in turn; MX4 x for comparison:
+//   up to 16 rows and few tiles: every wave on its own x, one tile a workgroup whose 4 or
+//     (long K) 8 waves split K (1024 x 17408 M = 1 7.4, 16-row workgroups through LDS in 12
+//     slices 8.4; 7168 x 5120 6.1, two tiles 7.5; MX4 x 6.1); above 8 rows x costs as much as
+//     one tile's weights: two tiles (7168 x 5120 M = 16 8.8, one 9.7; MX4 x 6.5).  A long K,
+//     more than 4 rows: x shared, K in slices (5120 x 17408 M = 16 15.7, 17.7 without
+//     sharing, 13.5 with MX4 x).
+//   up to 16 rows and many tiles: x shared by the waves of as many tiles as spread() says
+//     (34816 x 5120 M = 16 19.5, two tiles without sharing 27.0; MX4 x 19.5); a short K is
+//     over before sharing pays (65536 x 1024 M = 1 8.4, shared 10.0).
+//   above: as long as the pairs of tiles are few, those same workgroups of 16 rows beside
+//     each other (1024 x 1024 M = 64 3.2, 32 rows through LDS 5.0; 7168 x 5120 M = 33 12.9,
+//     32 rows 14.0; MX4 x 10.0), then 32 rows (M = 128 18.2, 64 x 128 tiles in eight slices
+//     22.1; MX4 x 14.4).  Many tiles, M = 17-32: 32 rows, units of two groups (34816 x 5120
+//     M = 17 24.9, units of four 26.7; MX4 x 22.2); to 64: 32 x 128 tiles (M = 64 35.1, 64 x 128
+//     38.0; MX4 x 28.0).
+//   a long K (17408) above 16 rows: 32 rows in slices to 48 rows or few pairs (5120 rows
+//     M = 33 20.9, 64 x 128 tiles 21.4; MX4 x 19.5), then 64 x 128 tiles in slices (M = 64
+//     23.2, 32 rows 24.8; MX4 x 20.3).
+//   many rows: 64 x 256 tiles if they give 440 workgroups (34816 x 5120 M = 512 107.6,
+//     64 x 128 110.0, 128 x 256 143.7; M = 4096 621, 128 x 256 644; MX4 x 74 and 389), else
+//     64 x 128, from K = 4096 on in slices up to 640 workgroups (7168 x 5120 M = 256 28.0
+//     with three, 31.7 with one; MX4 x 20.5).
 Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
-    const int Q = (int)mx4::quads(K);
+    const int G = (int)mx4::groups(K), Q = (int)mx4::quads(K);
+    const int64_t nt = tiles(N), t = nt * tiles(M);
+    const bool many = nt >= 1024, lengthy = G >= 96;
     const auto blocks = [&](int64_t bm, int64_t bn) {
         return (M + bm - 1) / bm * ((N + bn - 1) / bn);
     };
     const auto slices = [](int64_t want, int64_t have) { return (want + have / 2) / have; };
-    Plan p{kSmall, 1, 4 * Q};
+    Plan p{kOne4, 4, 1, 4 * Q};
     int64_t S = 1;
     if (M <= 16) {
-        p.kernel = kSmall;
-    } else if (M <= 64) {
-        p.kernel = M <= 32 ? kMid32 : M <= 48 ? kMid48 : kMid64;
-        if (K >= 4096) S = slices(512, blocks(64, 64));
-    } else if (blocks(128, 256) >= 440) {
-        p.kernel = kTile128;
+        if (many && G >= 32) {
+            p.kernel = kMid16;
+            p.wn = spread(nt);
+        } else if (M > 4 && G >= 48 && nt <= 384) {
+            p.kernel = kMid16x2;
+            S = slices(480, blocks(16, 32));
+        } else if (M <= 8 || nt <= 256) {
+            p.kernel = G >= 24 && !many ? kOne8 : kOne4;
+        } else {
+            p.kernel = G >= 48 ? kTwo8 : kTwo4;
+        }
+    } else if (many && M <= 64) {
+        p.kernel = M <= 32 ? kMid32x2 : kTile32;
+    } else if (lengthy && (M <= 48 || t <= 400)) {
+        p.kernel = kMid32;
+        S = slices(480, blocks(32, 64));
+    } else if (!lengthy && !many && t <= 4096) {
+        p.kernel = t <= 400    ? kOne4
+                   : t <= 800  ? kTwo4
+                   : t <= 1200 ? kMid16x2
+                   : t <= 2000 ? kMid16
+                               : kMid32;
+    } else if (blocks(64, 256) >= 440) {
+        p.kernel = kTile64x4;
     } else {
         p.kernel = kTile64;
-        if (K >= 4096) S = slices(640, blocks(64, 128));
+        if (G >= 32) S = slices(640, blocks(64, 128));
     }
-    if (S > Q) S = Q;
+    if (S > Q / 2) S = Q / 2;
     if (S < 1) S = 1;
     const int qs = (int)((Q + S - 1) / S);      // quads a slice
     p.S = (Q + qs - 1) / qs;
@@ -669,16 +722,28 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     a.gs = p.gs;
     a.part = static_cast<float*>(ws);
     Kernel k = p.kernel;
-    if (k >= kTile64 && (a.ldv >= kFarRows || a.lds >= kFarRows)) k = kSmall;
-    if (k == kSmall) a.S = 1;
+    if (k >= kTile32 && (a.ldv >= kFarRows || a.lds >= kFarRows)) {
+        k = kTwo4;
+        a.S = 1;
+    }
     switch (k) {
-        case kMid16: return launch_mid<1, 4, 2>(a, s);
-        case kMid32: return launch_mid<2, 4, 1>(a, s);
-        case kMid48: return launch_mid<3, 4, 1>(a, s);
-        case kMid64: return launch_mid<4, 4, 1>(a, s);
-        case kTile64: return launch_tile<4, 2, 4, 2, 2>(a, s);
-        case kTile128: return launch_tile<8, 4, 4, 1, 2>(a, s);
-        default: return launch_small<2, 4>(a, s);
+        case kOne8: return launch_small<1, 8>(a, s);
+        case kTwo4: return launch_small<2, 4>(a, s);
+        case kTwo8: return launch_small<2, 8>(a, s);
+        case kMid16x2: return launch_mid<1, 2, 2, 4>(a, s);
+        case kMid16:
+            switch (p.wn) {
+                case 5: return launch_mid<1, 5, 1, 4>(a, s);
+                case 7: return launch_mid<1, 7, 1, 4>(a, s);
+                case 9: return launch_mid<1, 9, 1, 4>(a, s);
+                default: return launch_mid<1, 4, 1, 4>(a, s);
+            }
+        case kMid32: return launch_mid<2, 4, 1, 4>(a, s);
+        case kMid32x2: return launch_mid<2, 4, 1, 2>(a, s);
+        case kTile32: return launch_tile<2, 2, 4, 2>(a, s);
+        case kTile64: return launch_tile<4, 2, 4, 2>(a, s);
+        case kTile64x4: return launch_tile<4, 4, 4, 1>(a, s);
+        default: return launch_small<1, 4>(a, s);
     }
 }
 
