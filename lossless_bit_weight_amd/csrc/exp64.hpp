@@ -24,10 +24,8 @@ __device__ __forceinline__ double exp2_64(double t) {
     p = __builtin_fma(p, f, 1.0);
     return __builtin_ldexp(p, (int)n);
 }
-// 2^(d rate) for d up to 0 in fewer instructions; `least` = -1000 / rate, and below it
-// the result is 2^-1000.
-__device__ __forceinline__ double exp2_64_low(double d, double rate, double least) {
-    d = __builtin_fmax(d, least);
+// 2^(d rate) for |d rate| up to 1021 in fewer instructions, none of them a conversion.
+__device__ __forceinline__ double exp2_64_within(double d, double rate) {
     // the nearest whole number in the last bits of the sum with 3 * 2^51
     const double shifted = __builtin_fma(d, rate, 0x1.8p52);
     const double f = __builtin_fma(d, rate, -(shifted - 0x1.8p52));
@@ -46,5 +44,9 @@ __device__ __forceinline__ double exp2_64_low(double d, double rate, double leas
     // 2^n times p, which lies in 0.7 .. 1.5
     const uint64_t n = (uint64_t)(uint32_t)__double2loint(shifted) << 52;
     return __longlong_as_double((long long)((uint64_t)__double_as_longlong(p) + n));
+}
+// The same for d up to 0; `least` = -1000 / rate, and below it the result is 2^-1000.
+__device__ __forceinline__ double exp2_64_low(double d, double rate, double least) {
+    return exp2_64_within(__builtin_fmax(d, least), rate);
 }
 constexpr double kLog2E = 1.4426950408889634;

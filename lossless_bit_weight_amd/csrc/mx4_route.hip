@@ -9,7 +9,7 @@
 // that differ in the last of fp32's bits is then the same for every way of computing
 // them; or the fp32 logit in the upper half).  The chosen ones are taken by maxima over
 // the wave of the upper halves, and of the lower ones and the indices only where several
-// share the largest: seven instructions a maximum, no LDS.  The scores of the chosen are
+// share the largest: six lane moves a maximum, no LDS.  The scores of the chosen are
 // computed again from their logits, a lane each, so that softmax with renormalised shares
 // and no bias needs no exponential of the others.
 // Bound by instructions: 8191 tokens, 256 experts in 8 groups, sigmoid and bias: see
@@ -83,13 +83,22 @@ __device__ __forceinline__ double wave_sum(double v) {
     });
     return v;
 }
+// The wave's largest: along the rows of 16 lanes, over the rows, then from the last lane (a
+// lane without a source keeps its own).
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    within(64, [&](auto d) {
-        uint32_t a, b;
-        exchange<decltype(d)::value>(v, a, b);
-        v = a > b ? a : b;
-    });
-    return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+    const auto step = [&](auto ctrl) {
+        constexpr int C = decltype(ctrl)::value;
+        const uint32_t o =
+            (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, C, 0xF, 0xF, false);
+        v = v > o ? v : o;
+    };
+    step(std::integral_constant<int, 0x111>{});     // row_shr:1
+    step(std::integral_constant<int, 0x112>{});     // row_shr:2
+    step(std::integral_constant<int, 0x114>{});     // row_shr:4
+    step(std::integral_constant<int, 0x118>{});     // row_shr:8
+    step(std::integral_constant<int, 0x142>{});     // row_bcast:15
+    step(std::integral_constant<int, 0x143>{});     // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 template <bool F32>
@@ -97,13 +106,22 @@ __device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
     if constexpr (F32) return static_cast<const float*>(a.logits)[t * a.ldl + e];
     return __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[t * a.ldl + e] << 16);
 }
+// (results are selected, not branched to, so that the slots of a lane overlap)
+constexpr double kLeast = -707.0;       // exp of less counts as 0
 __device__ __forceinline__ double sigmoid(float l) {
-    const double d = l;
-    return d != d ? d : 1.0 / (1.0 + exp2_64(-d * kLog2E));
+    const double d = l, in = __builtin_fmin(__builtin_fmax(d, kLeast), -kLeast);
+    const double x = 1.0 + exp2_64_within(-in, kLog2E);
+    double s = __builtin_amdgcn_rcp(x);
+    s = __builtin_fma(__builtin_fma(-x, s, 1.0), s, s);
+    s = __builtin_fma(__builtin_fma(-x, s, 1.0), s, s);
+    s = d < kLeast ? 0.0 : s;
+    return d == d ? s : d;
 }
 // exp(l - top), whose sum is softmax's denominator
 __device__ __forceinline__ double power(float l, float top) {
-    return l == -__builtin_inff() ? 0.0 : exp2_64(((double)l - (double)top) * kLog2E);
+    const double d = (double)l - (double)top;
+    const double p = exp2_64_within(__builtin_fmax(d, kLeast), kLog2E);
+    return d < kLeast || l == -__builtin_inff() ? 0.0 : p;
 }
 
 template <int EV, bool F32>
@@ -157,25 +175,30 @@ __global__ __launch_bounds__(256) void pick_kernel(RouteArgs a, int groups, int 
     }
     uint32_t hi[EV], lo[EV];            // ranks; 0: not to be chosen
     double value[EV];                   // s + bias, -inf for those
+    if (any_bias) {
+        float b[EV];
 #pragma unroll
-    for (int i = 0; i < EV; ++i) {
-        const bool in = g < groups && i * L + r < per;
-        bool may = l[i] != -__builtin_inff();
-        if (any_bias) {
-            const float b = a.bias[in ? first + i * L : 0];
-            may = may && b != -__builtin_inff();
-            value[i] = score[i] + (double)b;
-            const uint64_t o = order64(l[i] != l[i] ? (double)l[i] : value[i]);
-            hi[i] = (uint32_t)(o >> 32);
-            lo[i] = (uint32_t)o;
-        } else {
-            value[i] = all ? score[i] : 0.0;
-            hi[i] = order32(l[i]);
-            lo[i] = 0;
+        for (int i = 0; i < EV; ++i) {
+            const bool in = g < groups && i * L + r < per;
+            b[i] = a.bias[in ? first + i * L : 0];
         }
-        hi[i] = may ? hi[i] : 0u;
-        lo[i] = may ? lo[i] : 0u;
-        value[i] = may ? value[i] : -__builtin_inf();
+#pragma unroll
+        for (int i = 0; i < EV; ++i) {
+            const bool may = l[i] != -__builtin_inff() && b[i] != -__builtin_inff();
+            const double v = score[i] + (double)b[i];
+            const uint64_t o = order64(l[i] != l[i] ? (double)l[i] : v);
+            hi[i] = may ? (uint32_t)(o >> 32) : 0u;
+            lo[i] = may ? (uint32_t)o : 0u;
+            value[i] = may ? v : -__builtin_inf();
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EV; ++i) {
+            const bool may = l[i] != -__builtin_inff();
+            hi[i] = may ? order32(l[i]) : 0u;
+            lo[i] = 0;
+            value[i] = may && all ? score[i] : -__builtin_inf();
+        }
     }
 
     if (limited) {
@@ -237,32 +260,25 @@ __global__ __launch_bounds__(256) void pick_kernel(RouteArgs a, int groups, int 
 
     int found = -1;
     for (int j = 0; j < a.top_k; ++j) {
-        uint32_t best = 0;
+        // the lane's largest, of equal ones its lowest expert
+        uint64_t top_key = (uint64_t)hi[0] << 32 | lo[0];
+        int mine = first;
 #pragma unroll
-        for (int i = 0; i < EV; ++i) best = hi[i] > best ? hi[i] : best;
-        best = wave_max(best);
-        if (best == 0) break;
-        int e = 0, n = 0;
-#pragma unroll
-        for (int i = 0; i < EV; ++i) {
-            const uint64_t hits = __ballot(hi[i] == best);
-            n += __popcll(hits);
-            if (hits != 0) {
-                const int src = __builtin_ctzll(hits);
-                e = (src >> log_lanes) * per + (src & (L - 1)) + i * L;
-            }
+        for (int i = 1; i < EV; ++i) {
+            const uint64_t k = (uint64_t)hi[i] << 32 | lo[i];
+            mine = k > top_key ? first + i * L : mine;
+            top_key = k > top_key ? k : top_key;
         }
-        if (n > 1) {            // the largest lower half, and of its experts the lowest
-            uint32_t low = 0, at = 0;
-#pragma unroll
-            for (int i = 0; i < EV; ++i)
-                if (hi[i] == best && lo[i] > low) low = lo[i];
-            low = wave_max(low);
-#pragma unroll
-            for (int i = 0; i < EV; ++i)
-                if (hi[i] == best && lo[i] == low && ~(uint32_t)(first + i * L) > at)
-                    at = ~(uint32_t)(first + i * L);
-            e = (int)~wave_max(at);
+        const uint32_t best = (uint32_t)(top_key >> 32), low = (uint32_t)top_key;
+        const uint32_t most = wave_max(best);
+        if (most == 0) break;
+        uint64_t hits = __ballot(best == most);
+        int e;
+        if (__popcll(hits) == 1) {
+            e = __builtin_amdgcn_readlane(mine, __builtin_ctzll(hits));
+        } else {            // the largest lower half, and of its experts the lowest
+            const uint32_t lower = wave_max(best == most ? low : 0u);
+            e = (int)~wave_max(best == most && low == lower ? ~(uint32_t)mine : 0u);
         }
 #pragma unroll
         for (int i = 0; i < EV; ++i) hi[i] = first + i * L == e ? 0u : hi[i];
