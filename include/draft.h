@@ -45,7 +45,8 @@ const char *draft_status_string(int status);
  * word (the lowest of a tie), and the token behind is that word of row a.
  *   tokens[b, .]  = the a accepted tokens, the one behind them, then -1;
  *   accepted[b]   = a.
- * Probabilities, their sums and the running sums are held in 64 bits.
+ * Probabilities, their sums and the running sums are held in 64 bits; a word
+ * of less than 2^-1000 of its row's largest probability counts as 0.
  * A row that holds a NaN or +inf, or nothing but -inf, has no distribution: its
  * draft is refused, and the token drawn from it is -1.  A draft outside
  * 0 .. V-1 is refused, and what is drawn then is as if q were q_a with nothing

@@ -95,9 +95,11 @@ __device__ __forceinline__ int64_t draft_of(const Args& a, int b, int i) {
     return a.drafts_i64 ? static_cast<const int64_t*>(a.drafts)[at]
                         : static_cast<const int*>(a.drafts)[at];
 }
-// 2^((l - top) rate)
-__device__ __forceinline__ double power(float l, float top, double rate) {
-    return l == -__builtin_inff() ? 0.0 : exp2_64(((double)l - (double)top) * rate);
+// 2^((l - top) rate), 0 below 2^-1000 (least = -1000 / rate); selected, not branched to, so
+// that a thread's words overlap.
+__device__ __forceinline__ double power(float l, float top, double rate, double least) {
+    const double d = (double)l - (double)top, p = exp2_64_low(d, rate, least);
+    return d < least || l == -__builtin_inff() ? 0.0 : p;
 }
 
 // max that keeps a NaN
@@ -153,14 +155,15 @@ __global__ __launch_bounds__(kThreads) void parts_kernel(Args a) {
     float top = -__builtin_inff();
     int sbits = (int)0x80000000;
     uint32_t ubits = 0;
+    const auto larger = [](auto a, auto b) { return a > b ? a : b; };
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            const float f = c.f[k][j];
-            top = __builtin_fmaxf(top, f);
-            sbits = __float_as_int(f) > sbits ? __float_as_int(f) : sbits;
-            ubits = __float_as_uint(f) > ubits ? __float_as_uint(f) : ubits;
+        for (int j = 0; j < VEC; j += 2) {
+            const float f = c.f[k][j], g = c.f[k][j + 1];
+            top = __builtin_fmaxf(top, __builtin_fmaxf(f, g));
+            sbits = larger(sbits, larger(__float_as_int(f), __float_as_int(g)));
+            ubits = larger(ubits, larger(__float_as_uint(f), __float_as_uint(g)));
         }
     if (sbits >= 0x7F800000 || ubits > 0xFF800000u) top = __builtin_nanf("");
 #pragma unroll
@@ -201,7 +204,8 @@ __global__ __launch_bounds__(kThreads) void parts_kernel(Args a) {
 }
 
 // From the row's chunks, by 16 lanes of a row (`lane` 0 .. 15 of them), in every one.
-__device__ __forceinline__ Whole whole(const Args& a, int64_t row, double rate, int lane) {
+__device__ __forceinline__ Whole whole(const Args& a, int64_t row, double rate, double least,
+                                       int lane) {
     const Part* p = a.parts + row * a.chunks;
     // one pass: the sum is kept in powers of the largest logit so far
     Whole w{0.0, -__builtin_inff(), 0x7FFFFFFF};
@@ -210,8 +214,8 @@ __device__ __forceinline__ Whole whole(const Args& a, int64_t row, double rate, 
         if (part.top > w.top || (part.top == w.top && part.word < w.word)) w.word = part.word;
         const float top = max_nan(w.top, part.top);
         if (rate != 0.0 && top > -__builtin_inff()) {
-            const double old = w.sum > 0.0 ? w.sum * power(w.top, top, rate) : 0.0;
-            w.sum = old + part.sum * (part.top == top ? 1.0 : power(part.top, top, rate));
+            const double old = w.sum > 0.0 ? w.sum * power(w.top, top, rate, least) : 0.0;
+            w.sum = old + part.sum * (part.top == top ? 1.0 : power(part.top, top, rate, least));
         }
         w.top = top;
     }
@@ -224,7 +228,7 @@ __device__ __forceinline__ Whole whole(const Args& a, int64_t row, double rate, 
         w.top = max_nan(w.top, ot);
     }
     if (rate == 0.0) return w;
-    w.sum = w.good() && w.sum > 0.0 ? w.sum * power(mine, w.top, rate) : 0.0;
+    w.sum = w.good() && w.sum > 0.0 ? w.sum * power(mine, w.top, rate, least) : 0.0;
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) w.sum += __shfl_xor(w.sum, d);
     return w;
@@ -257,7 +261,7 @@ __device__ __forceinline__ Stop stop_of(const Args& a, int b, StopSpace& space) 
     const int n = length_of(a, b);
     int i = threadIdx.x / 16;
     int64_t x = i < a.D ? draft_of(a, b, i) : -1;
-    const double rate = rate_of(tau);
+    const double rate = rate_of(tau), least = -1000.0 / rate;
     if (threadIdx.x == 0) space.refused = n;
     __syncthreads();
     for (; i <= n; i += T / 16) {
@@ -267,9 +271,9 @@ __device__ __forceinline__ Stop stop_of(const Args& a, int b, StopSpace& space) 
         const float l = logit(a, b, i, in ? x : 0);
         const double q = a.probs != nullptr && in ? (double)prob(a, b, i, x) : 1.0;
         const double u = a.uniforms[row0 + i];
-        const Whole r = whole(a, row0 + i, rate, lane);
+        const Whole r = whole(a, row0 + i, rate, least, lane);
         bool ok = r.good() && in;
-        if (ok) ok = rate == 0.0 ? x == r.word : u * q * r.sum < power(l, r.top, rate);
+        if (ok) ok = rate == 0.0 ? x == r.word : u * q * r.sum < power(l, r.top, rate, least);
         if (lane == 0) {
             space.rows[i] = r;
             if (i < n && !ok) atomicMin(&space.refused, i);
@@ -280,6 +284,7 @@ __device__ __forceinline__ Stop stop_of(const Args& a, int b, StopSpace& space) 
     s.n = space.refused;
     s.length = n;
     s.rate = rate;
+    s.least = least;
     s.row = space.rows[s.n];
     return s;
 }
@@ -335,7 +340,7 @@ struct Weights {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                double w = power(c.f[i][j], s.row.top, s.rate);
+                double w = power(c.f[i][j], s.row.top, s.rate, s.least);
                 if (off) {
                     // (one instruction in every kernel: whether it is above 0 has to agree)
                     const double d = __builtin_fma(-(double)q[i][j], s.row.sum, w);
@@ -431,8 +436,8 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
         if (x >= 0) {
             const Row<F32> row(a.logits, b * a.ldb + s.n * a.ldd);
             cx = (int)((x + row.head) / W::C::kWords);
-            const double all = part[cx].sum * power(part[cx].top, s.row.top, s.rate);
-            cx_sum = all - power(row.one((int)x), s.row.top, s.rate);
+            const double all = part[cx].sum * power(part[cx].top, s.row.top, s.rate, s.least);
+            cx_sum = all - power(row.one((int)x), s.row.top, s.rate, s.least);
             if (!(cx_sum > 1e-6 * all)) {
                 W weights;
                 weights.load(a, b, s, cx, true, x);
@@ -443,7 +448,7 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
             if (c >= a.chunks) return 0.0;
             if (off && a.probs != nullptr) return rest[c];
             if (off && c == cx) return cx_sum;
-            return part[c].sum * power(part[c].top, s.row.top, s.rate);
+            return part[c].sum * power(part[c].top, s.row.top, s.rate, s.least);
         };
         // wave 0: the whole sum, then the chunk (64 chunks and fewer: both from one scan)
         if (w == 0) {
@@ -528,10 +533,11 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Vectors of 16 bytes a thread holds of a chunk: as many as leave the GPU some chunks.
+// Vectors of 16 bytes a thread holds of a chunk: as many as leave the GPU some chunks, four
+// at most (32 x 16 rows of 129280 fp32 words 67 us, eight 69).
 int vectors(int64_t rows, int64_t V, bool f32) {
     const int64_t words = kThreads * (f32 ? 4 : 8);
-    int nv = f32 ? 8 : 4;
+    int nv = 4;
     while (nv > 1 && rows * ((V + words * nv - 1) / (words * nv)) < 1024) nv /= 2;
     return nv;
 }
@@ -561,11 +567,8 @@ hipError_t launch_by(int nv, const Args& a, hipStream_t s) {
     switch (nv) {
         case 1: return launch<F32, 1>(a, s);
         case 2: return launch<F32, 2>(a, s);
-        case 4: return launch<F32, 4>(a, s);
-        default: break;
+        default: return launch<F32, 4>(a, s);
     }
-    if constexpr (F32) return launch<F32, 8>(a, s);
-    return hipErrorInvalidValue;
 }
 
 }  // namespace

@@ -26,7 +26,7 @@ struct Whole {
 // Where a sequence stops: its accepted tokens and the row behind them.
 struct Stop {
     Whole row;
-    double rate;        // log2(e) / tau, 0: greedy
+    double rate, least; // log2(e) / tau, 0: greedy; and -1000 / rate
     int n, length;      // accepted, drafted
 };
 
