@@ -68,11 +68,15 @@ __device__ __forceinline__ u32x4_t load16_nt(const uint8_t* p) {
     return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
 }
 
-// A uniform pointer the compiler keeps in scalar registers: folded with the lane's
-// offset it would hold two vector registers through the loop.
+// A uniform pointer to global memory that the compiler keeps in scalar registers: folded
+// with the lane's offset it would hold two vector registers through the loop.  (What is
+// read through it must not look like a generic pointer: every wait for LDS would wait for
+// flat loads too.)
 __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
-    asm volatile("" : "+s"(p));
-    return p;
+    typedef const __attribute__((address_space(1))) uint8_t* global_t;
+    global_t g = (global_t)p;
+    asm volatile("" : "+s"(g));
+    return (const uint8_t*)g;
 }
 
 template <bool NT>
