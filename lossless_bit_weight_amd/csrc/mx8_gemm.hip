@@ -21,28 +21,17 @@ using mx4::kCodeBlock;
 using mx4::kScaleBlock;
 using mx4::tiles;
 
-// A uniform pointer to global memory that the compiler keeps in scalar registers (folded
-// with the lane's offset it would hold two vector registers through the loop), and 16, 8 or 4
-// bytes at a lane's offset from it.  In the generic address space these would be flat loads,
-// which every wait for LDS waits for too.
-typedef const __attribute__((address_space(1))) uint8_t* global_t;
-__device__ __forceinline__ global_t scalar(const uint8_t* p) {
-    global_t g = (global_t)p;
-    asm volatile("" : "+s"(g));
-    return g;
+using mx4::scalar;
+
+// 16, 8 or 4 bytes at a lane's offset from a scalar pointer.
+__device__ __forceinline__ u32x4_t load16(const uint8_t* p, uint32_t at) {
+    return *reinterpret_cast<const u32x4_t*>(p + at);
 }
-__device__ __forceinline__ u32x4_t load16(global_t p, uint32_t at) {
-    return *reinterpret_cast<const __attribute__((address_space(1))) u32x4_t*>(p + at);
+__device__ __forceinline__ u32x2_t load8(const uint8_t* p, uint32_t at) {
+    return *reinterpret_cast<const u32x2_t*>(p + at);
 }
-__device__ __forceinline__ u32x4_t load16_nt(global_t p, uint32_t at) {
-    return __builtin_nontemporal_load(
-        reinterpret_cast<const __attribute__((address_space(1))) u32x4_t*>(p + at));
-}
-__device__ __forceinline__ u32x2_t load8(global_t p, uint32_t at) {
-    return *reinterpret_cast<const __attribute__((address_space(1))) u32x2_t*>(p + at);
-}
-__device__ __forceinline__ uint32_t load4(global_t p, uint32_t at) {
-    return *reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(p + at);
+__device__ __forceinline__ uint32_t load4(const uint8_t* p, uint32_t at) {
+    return *reinterpret_cast<const uint32_t*>(p + at);
 }
 
 __device__ __forceinline__ void store_y(const GemmArgs& a, int64_t m, int64_t n, float v) {
@@ -245,8 +234,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
 #pragma unroll
         for (int j = 0; j < UG; ++j) {
             const int g = uc * UG + j < a.G ? uc * UG + j : a.G - 1;
-            const global_t from = scalar(wp + (int64_t)g * kCodeBlock);
-            wb[slot][j] = MT == 1 ? load16_nt(from, lane16) : load16(from, lane16);
+            wb[slot][j] = mx4::load16<MT == 1>(scalar(wp + (int64_t)g * kCodeBlock) + lane16);
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -619,22 +607,12 @@ struct Plan {
     int S, gs;              // K slices, groups a slice (a multiple of 4)
 };
 
-// Waves beside each other that spread nt tiles best over 256 CUs: the CU with the most of
-// them decides, one that has a single workgroup, whose barriers nothing fills, counts a
-// fifth more (34816 x 5120, 2176 tiles, M = 1 / 16: 5 waves 17.1 / 19.5 us, 4 18.8 / 23.7).
+// Four or five waves beside each other, whichever spreads nt tiles better over 256 CUs: the
+// CU with the most of them decides (34816 x 5120, 2176 tiles, M = 1 / 16: five 17.1 / 19.5 us,
+// four 18.8 / 23.7).
 int spread(int64_t nt) {
-    static const int kWaves[] = {9, 7, 5, 4};
-    int best = 4;
-    int64_t least = -1;
-    for (const int w : kWaves) {
-        const int64_t most = ((nt + w - 1) / w + 255) / 256;
-        const int64_t cost = most * w * (most == 1 ? 6 : 5);
-        if (least < 0 || cost < least) {
-            least = cost;
-            best = w;
-        }
-    }
-    return best;
+    const auto most = [&](int64_t w) { return ((nt + w - 1) / w + 255) / 256 * w; };
+    return most(5) <= most(4) ? 5 : 4;
 }
 
 // By rows of x (M), tiles of 16 weight rows (nt), pairs of a weight tile and 16 rows of x
@@ -732,12 +710,7 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
         case kTwo8: return launch_small<2, 8>(a, s);
         case kMid16x2: return launch_mid<1, 2, 2, 4>(a, s);
         case kMid16:
-            switch (p.wn) {
-                case 5: return launch_mid<1, 5, 1, 4>(a, s);
-                case 7: return launch_mid<1, 7, 1, 4>(a, s);
-                case 9: return launch_mid<1, 9, 1, 4>(a, s);
-                default: return launch_mid<1, 4, 1, 4>(a, s);
-            }
+            return p.wn == 5 ? launch_mid<1, 5, 1, 4>(a, s) : launch_mid<1, 4, 1, 4>(a, s);
         case kMid32: return launch_mid<2, 4, 1, 4>(a, s);
         case kMid32x2: return launch_mid<2, 4, 1, 2>(a, s);
         case kTile32: return launch_tile<2, 2, 4, 2>(a, s);
