@@ -150,16 +150,16 @@ hipError_t launch_small(const GemmArgs& a, hipStream_t s) {
 
 // ---- a few rows of x, shared through LDS ------------------------------------------
 // A workgroup: 16 MT rows of x by 16 WN weight rows; KW groups of WN waves take every
-// KW-th unit of UG groups of K.  A unit's weights come to registers one unit ahead of
+// KW-th unit of four groups of K.  A unit's weights come to registers one unit ahead of
 // their products; its x goes through LDS, double-buffered, where the WN waves share it:
-// row m of a unit is 8 UG pieces of 16 bytes, piece p at place (p & 16) | ((p ^ m) & 15).
+// row m of a unit is 32 pieces of 16 bytes, piece p at place (p & 16) | ((p ^ m) & 15).
 // A read takes one piece from 16 rows for each q; the LDS serves it 16 lanes at a time,
 // rows 0-3 and 12-15 of one q with rows 4-11 of the next, which lie in 16 different
 // places then, and so do the 16 pieces that 16 lanes write.
-template <int MT, int WN, int KW, int UG>
+template <int MT, int WN, int KW>
 struct Mid {
     static constexpr int kThreads = WN * KW * 64;
-    static constexpr int kAllPieces = 16 * MT * 8 * UG;                         // of x a unit
+    static constexpr int kAllPieces = 16 * MT * 32;                         // of x a unit
     static constexpr int kPieces = (kAllPieces + WN * 64 - 1) / (WN * 64);  // a thread
     static constexpr int kStage = kAllPieces * 16;
     static constexpr int lds() {
@@ -168,11 +168,10 @@ struct Mid {
     }
 };
 
-template <int MT, int WN, int KW, int UG>
+template <int MT, int WN, int KW>
 __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, int nb) {
-    using T = Mid<MT, WN, KW, UG>;
-    constexpr int P = T::kPieces, kRow = 8 * UG;
-    static_assert(UG == 4 || (UG == 2 && KW == 1), "a unit's place in its scales' dword is its slot");
+    using T = Mid<MT, WN, KW>;
+    constexpr int P = T::kPieces;
     extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -188,9 +187,8 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         bm = i / width;
     }
     const int m0 = bm * 16 * MT;
-    const int U = (a.G + UG - 1) / UG;
-    const int u0 = blockIdx.y * (a.gs / UG);
-    const int u1 = u0 + a.gs / UG < U ? u0 + a.gs / UG : U;
+    const int u0 = blockIdx.y * (a.gs / 4);
+    const int u1 = u0 + a.gs / 4 < a.Q ? u0 + a.gs / 4 : a.Q;
     const int its = (u1 - u0 + KW - 1) / KW;
     const uint32_t lane16 = lane * 16, lane4 = lane * 4;
 
@@ -210,8 +208,8 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         int piece = (i * WN + wn) * 64 + lane;
         if (T::kAllPieces % (WN * 64) != 0 && piece > T::kAllPieces - 64 + lane)
             piece = T::kAllPieces - 64 + lane;
-        const int row = piece / kRow, p = piece % kRow;
-        at[i] = (row * kRow + ((p & 16) | ((p ^ row) & 15))) * 16;
+        const int row = piece / 32, p = piece % 32;
+        at[i] = (row * 32 + ((p & 16) | ((p ^ row) & 15))) * 16;
         const int m = m0 + row < a.M ? m0 + row : a.M - 1;
         xp[i] = a.x + (int64_t)m * a.ldv;
         xk[i] = 16 * p;
@@ -222,7 +220,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         const int m = m0 + 16 * t + c < a.M ? m0 + 16 * t + c : a.M - 1;
         xs[t] = a.xs + (int64_t)m * a.lds + 4 * q;
     }
-    u32x4_t wb[2][UG], xb[P];
+    u32x4_t wb[2][4], xb[P];
     uint32_t ws[2], xsc[2][MT];
     bool xin[P];
     // (no branch: a place past the last unit, group or K is a valid one whose x is
@@ -230,21 +228,21 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
     auto load = [&](int slot, int it) {
         const int u = u0 + it * KW + kw;
         const int uc = u < u1 ? u : u1 - 1;
-        ws[slot] = load4(scalar(sp + (int64_t)(uc * UG / 4) * kScaleBlock), lane4);
+        ws[slot] = load4(scalar(sp + (int64_t)uc * kScaleBlock), lane4);
 #pragma unroll
-        for (int j = 0; j < UG; ++j) {
-            const int g = uc * UG + j < a.G ? uc * UG + j : a.G - 1;
+        for (int j = 0; j < 4; ++j) {
+            const int g = uc * 4 + j < a.G ? uc * 4 + j : a.G - 1;
             wb[slot][j] = mx4::load16<MT == 1>(scalar(wp + (int64_t)g * kCodeBlock) + lane16);
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const int k = u * (128 * UG) + xk[i];
+            const int k = u * 512 + xk[i];
             xin[i] = u < u1 && k < a.K;
             xb[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[i] ? k : 0));
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-            xsc[slot][t] = *reinterpret_cast<const uint32_t*>(xs[t] + 16 * (uc * UG / 4));
+            xsc[slot][t] = *reinterpret_cast<const uint32_t*>(xs[t] + 16 * uc);
     };
     auto stage = [&](int buf) {
 #pragma unroll
@@ -268,20 +266,17 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
                 u32x4_t xv[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int p = 8 * (J % UG) + 4 * h + q;
+                    const int p = 8 * J + 4 * h + q;
                     xv[h] = *reinterpret_cast<const u32x4_t*>(
-                        xl + ((16 * t + c) * kRow + ((p & 16) | ((p ^ c) & 15))) * 16);
+                        xl + ((16 * t + c) * 32 + ((p & 16) | ((p ^ c) & 15))) * 16);
                 }
-                acc[t] = mfma<J>(wb[slot][J % UG], xv[0], xv[1], acc[t], ws[slot], xsc[slot][t]);
+                acc[t] = mfma<J>(wb[slot][J], xv[0], xv[1], acc[t], ws[slot], xsc[slot][t]);
             }
         };
-        constexpr int J0 = UG == 4 ? 0 : 2 * slot;
-        group(std::integral_constant<int, J0>{});
-        group(std::integral_constant<int, J0 + 1>{});
-        if constexpr (UG == 4) {
-            group(std::integral_constant<int, 2>{});
-            group(std::integral_constant<int, 3>{});
-        }
+        group(std::integral_constant<int, 0>{});
+        group(std::integral_constant<int, 1>{});
+        group(std::integral_constant<int, 2>{});
+        group(std::integral_constant<int, 3>{});
     };
     load(0, 0);
     stage(0);
@@ -327,8 +322,8 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
 // ---- many rows of x -------------------------------------------------------------
 // A workgroup of WN waves computes 16 MT rows of x by 16 R WN weight rows; a wave all
 // the rows by 16 R, its sums in registers.  Weight pieces go from memory to registers
-// in the layout the matrix instructions take them, AHEAD groups ahead; x through LDS,
-// double-buffered, where the waves share it, asked for one group ahead: row m of a group
+// in the layout the matrix instructions take them; x through LDS, double-buffered, where the
+// waves share it; both are asked for AHEAD groups ahead.  Row m of a group
 // is 8 pieces of 16 bytes, piece p at place p ^ (m / 2 & 7), so that two rows fill the
 // 16 places that are served at once (a read's rows as in mid_kernel).  x's scales go
 // through LDS too, by quads of groups.
@@ -396,9 +391,9 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
     const uint32_t soff =
         (uint32_t)(srow < row_last ? srow : row_last) * (uint32_t)a.lds + 8 * (tid & 1);
 
-    u32x4_t wreg[AHEAD == 1 ? 2 : 4][R], xreg[P];
+    u32x4_t wreg[2 * AHEAD][R], xreg[AHEAD][P];
     u32x2_t sreg;
-    bool xin = false;
+    bool xin[AHEAD];
     uint32_t ws[2][R];
     auto load_w = [&](int slot, int g) {
         const int gg = g < ge ? g : ge - 1;
@@ -418,24 +413,24 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
     };
     // (no branch: a load past the last group, row or K reads a valid place and is
     // replaced by zeros or, past the last step, never used)
-    auto load_x = [&](int g) {
+    auto load_x = [&](int set, int g) {
         const int k = 128 * (g < ge ? g : ge - 1);
         const bool k_in = k + 16 * p < a.K;
-        xin = g < ge && k_in;
+        xin[set] = g < ge && k_in;
         const uint32_t piece = k_in ? 16u * p : 0u;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const uint32_t off = xfirst + i * xstride;
-            xreg[i] = load16(scalar(xbase + k), (off < xlast ? off : xlast) + piece);
+            xreg[set][i] = load16(scalar(xbase + k), (off < xlast ? off : xlast) + piece);
         }
     };
-    auto store_x = [&](int buf) {
+    auto store_x = [&](int set, int buf) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int r = (tid >> 3) + i * (T::kThreads / 8);
             u32x4_t v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = xin ? xreg[i][e] : 0u;
+            for (int e = 0; e < 4; ++e) v[e] = xin[set] ? xreg[set][i][e] : 0u;
             *reinterpret_cast<u32x4_t*>(&xs[buf][r * 128 + ((p ^ (r >> 1 & 7)) << 4)]) = v;
         }
     };
@@ -453,16 +448,19 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
     load_scales(0, gb);
     load_w(0, gb);
     if constexpr (AHEAD == 2) load_w(1, gb + 1);
-    load_x(gb);
-    store_x(0);
+    load_x(0, gb);
+    store_x(0, 0);
+    if constexpr (AHEAD == 2) load_x(1, gb + 1);
     store_scales(0);
     __syncthreads();
 
     auto step = [&](auto jc, int g, int quad) {
         constexpr int J = decltype(jc)::value;
-        constexpr int cur = J & 1, kSlots = AHEAD == 1 ? 2 : 4;
+        constexpr int cur = J & 1, kSlots = 2 * AHEAD;
+        // the registers of x that hold this step's, stored before it, take a later step's
+        constexpr int set = AHEAD == 2 ? cur : 0, next_set = AHEAD == 2 ? cur ^ 1 : 0;
         load_w((J + AHEAD) % kSlots, g + AHEAD);
-        load_x(g + 1);
+        load_x(set, g + AHEAD);
         if constexpr (J == 2) load_scales(1, g + 2);
         // x operands are read one tile (of 16 rows) ahead of the products on them
         u32x4_t xv[2][2];
@@ -485,7 +483,7 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
                                     ws[0][r], xsc[i & 1]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        store_x(cur ^ 1);
+        store_x(next_set, cur ^ 1);
         if constexpr (J == 3) store_scales((quad & 1) ^ 1);
         __syncthreads();
         __builtin_amdgcn_sched_barrier(0);
@@ -583,13 +581,13 @@ hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
     return launch_join(a, s);
 }
 
-template <int MT, int WN, int KW, int UG>
+template <int MT, int WN, int KW>
 hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
-    using T = Mid<MT, WN, KW, UG>;
+    using T = Mid<MT, WN, KW>;
     static_assert(T::lds() <= 65536, "more LDS than a launch gets without asking");
     const int mb = (a.M + 16 * MT - 1) / (16 * MT);
     const int nb = (int)((tiles(a.N) + WN - 1) / WN);
-    hipLaunchKernelGGL((mid_kernel<MT, WN, KW, UG>), dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S),
+    hipLaunchKernelGGL((mid_kernel<MT, WN, KW>), dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S),
                        dim3(T::kThreads), T::lds(), s, a, mb, nb);
     return launch_join(a, s);
 }
@@ -599,8 +597,7 @@ hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
 constexpr int64_t kFarRows = (int64_t)1 << 24;
 
 // Kernel and split of a product.
-enum Kernel { kOne4, kOne8, kTwo4, kTwo8, kMid16x2, kMid16, kMid32, kMid32x2, kTile32, kTile64,
-              kTile64x4 };
+enum Kernel { kOne4, kOne8, kTwo4, kTwo8, kMid16x2, kMid16, kMid32, kTile32, kTile64, kTile64x4 };
 struct Plan {
     Kernel kernel;
     int wn;                 // kMid16: waves beside each other
@@ -615,6 +612,29 @@ int spread(int64_t nt) {
     return most(5) <= most(4) ? 5 : 4;
 }
 
+// Slices of Q quads for a product by `blocks` tiles, and its time in us: a quad takes `least`
+// however little there is to do, `each` for every workgroup of the busiest CU beyond that;
+// joining slices costs a launch and their sums written and read.  Measured, 64 x 128 tiles:
+// 5120 x 17408, M = 64, 40 tiles: 6 slices 20.3, 3 27.4, 12 22.5; M = 256, 160 tiles: 3 41.2,
+// 2 44.8, 1 54.5; 7168 x 5120, M = 256, 224 tiles: 1 19.8, 2 26.6.
+double slice(int64_t blocks, int64_t M, int64_t N, int Q, double least, double each,
+             int* slices) {
+    double best = 0.0;
+    *slices = 0;
+    for (int S = 1; S <= Q && S <= 64; ++S) {
+        const int qs = (Q + S - 1) / S;
+        if ((Q + qs - 1) / qs != S) continue;
+        const double busy = each * (double)((blocks * S + 255) / 256);
+        const double join = S > 1 ? 3.0 + (double)S * M * N * 8 / 3.2e6 : 0.0;
+        const double time = qs * (busy > least ? busy : least) + join;
+        if (*slices == 0 || time < best) {
+            best = time;
+            *slices = S;
+        }
+    }
+    return best;
+}
+
 // By rows of x (M), tiles of 16 weight rows (nt), pairs of a weight tile and 16 rows of x
 // (t) and groups of K (G).  us, graphs over weights in turn; MX4 x for comparison:
 //   up to 16 rows and few tiles: every wave on its own x, one tile a workgroup whose 4 or
@@ -626,19 +646,15 @@ int spread(int64_t nt) {
 //   up to 16 rows and many tiles: x shared by the waves of as many tiles as spread() says
 //     (34816 x 5120 M = 16 19.5, two tiles without sharing 27.0; MX4 x 19.5); a short K is
 //     over before sharing pays (65536 x 1024 M = 1 8.4, shared 10.0).
-//   above: as long as the pairs of tiles are few, those same workgroups of 16 rows beside
+//   above, as long as the pairs of tiles are few: those same workgroups of 16 rows beside
 //     each other (1024 x 1024 M = 64 3.2, 32 rows through LDS 5.0; 7168 x 5120 M = 33 12.9,
-//     32 rows 14.0; MX4 x 10.0), then 32 rows (M = 128 18.2, 64 x 128 tiles in eight slices
-//     22.1; MX4 x 14.4).  Many tiles, M = 17-32: 32 rows, units of two groups (34816 x 5120
-//     M = 17 24.9, units of four 26.7; MX4 x 22.2); to 64: 32 x 128 tiles (M = 64 35.1, 64 x 128
-//     38.0; MX4 x 28.0).
-//   a long K (17408) above 16 rows: 32 rows in slices to 48 rows or few pairs (5120 rows
-//     M = 33 20.9, 64 x 128 tiles 21.4; MX4 x 19.5), then 64 x 128 tiles in slices (M = 64
-//     23.2, 32 rows 24.8; MX4 x 20.3).
-//   many rows: 64 x 256 tiles if they give 440 workgroups (34816 x 5120 M = 512 107.6,
-//     64 x 128 110.0, 128 x 256 143.7; M = 4096 621, 128 x 256 644; MX4 x 74 and 389), else
-//     64 x 128, from K = 4096 on in slices up to 640 workgroups (7168 x 5120 M = 256 28.0
-//     with three, 31.7 with one; MX4 x 20.5).
+//     32 rows 14.0; MX4 x 10.0), then 32 rows (M = 96 17.2, 32 x 128 tiles 17.7); of a long K
+//     32 rows in slices up to M = 32 (5120 x 17408 M = 17 16.4, MX4 x 15.3).
+//   else tiles: 32 x 128 for many of them up to M = 64 (34816 x 5120 M = 64 30.4, 64 x 128
+//     34.4; MX4 x 25.9); 64 x 256 if they give 384 workgroups (M = 512 91, 64 x 128 110;
+//     M = 4096 574 to 600; MX4 x 66 and 389); else, in slices, what slice() gives less time
+//     for, 64 x 128 or 32 x 128 (7168 x 5120 M = 512 25.7 and 33.6, M = 160 19.2 and 18.5;
+//     MX4 x 20.4 and 15.4).
 Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
     const int G = (int)mx4::groups(K), Q = (int)mx4::quads(K);
     const int64_t nt = tiles(N), t = nt * tiles(M);
@@ -661,24 +677,29 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
         } else {
             p.kernel = G >= 48 ? kTwo8 : kTwo4;
         }
-    } else if (many && M <= 64) {
-        p.kernel = M <= 32 ? kMid32x2 : kTile32;
-    } else if (lengthy && (M <= 48 || t <= 400)) {
+        if (S > Q / 2) S = Q / 2;
+    } else if (lengthy && M <= 32 && nt <= 400) {
         p.kernel = kMid32;
         S = slices(480, blocks(32, 64));
-    } else if (!lengthy && !many && t <= 4096) {
+        if (S > Q / 2) S = Q / 2;
+    } else if (!lengthy && !many && t <= 3200) {
         p.kernel = t <= 400    ? kOne4
                    : t <= 800  ? kTwo4
                    : t <= 1200 ? kMid16x2
                    : t <= 2000 ? kMid16
                                : kMid32;
-    } else if (blocks(64, 256) >= 440) {
+    } else if (many && M <= 64) {
+        p.kernel = kTile32;
+    } else if (blocks(64, 256) >= 384) {
         p.kernel = kTile64x4;
     } else {
-        p.kernel = kTile64;
-        if (G >= 32) S = slices(640, blocks(64, 128));
+        int s64, s32;
+        const double t64 = slice(blocks(64, 128), M, N, Q, 1.5, 1.03, &s64);
+        const double t32 = slice(blocks(32, 128), M, N, Q, 1.25, 0.72, &s32);
+        const bool small = t32 < 0.97 * t64;
+        p.kernel = small ? kTile32 : kTile64;
+        S = small ? s32 : s64;
     }
-    if (S > Q / 2) S = Q / 2;
     if (S < 1) S = 1;
     const int qs = (int)((Q + S - 1) / S);      // quads a slice
     p.S = (Q + qs - 1) / qs;
@@ -708,11 +729,10 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
         case kOne8: return launch_small<1, 8>(a, s);
         case kTwo4: return launch_small<2, 4>(a, s);
         case kTwo8: return launch_small<2, 8>(a, s);
-        case kMid16x2: return launch_mid<1, 2, 2, 4>(a, s);
+        case kMid16x2: return launch_mid<1, 2, 2>(a, s);
         case kMid16:
-            return p.wn == 5 ? launch_mid<1, 5, 1, 4>(a, s) : launch_mid<1, 4, 1, 4>(a, s);
-        case kMid32: return launch_mid<2, 4, 1, 4>(a, s);
-        case kMid32x2: return launch_mid<2, 4, 1, 2>(a, s);
+            return p.wn == 5 ? launch_mid<1, 5, 1>(a, s) : launch_mid<1, 4, 1>(a, s);
+        case kMid32: return launch_mid<2, 4, 1>(a, s);
         case kTile32: return launch_tile<2, 2, 4, 2>(a, s);
         case kTile64: return launch_tile<4, 2, 4, 2>(a, s);
         case kTile64x4: return launch_tile<4, 4, 4, 1>(a, s);
