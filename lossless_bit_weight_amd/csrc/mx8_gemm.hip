@@ -34,6 +34,9 @@ __device__ __forceinline__ uint32_t load4(const uint8_t* p, uint32_t at) {
     return *reinterpret_cast<const uint32_t*>(p + at);
 }
 
+// Partial sums' row, whole 16-byte pieces.
+__host__ __device__ inline int64_t part_row(int64_t N) { return (N + 3) & ~(int64_t)3; }
+
 __device__ __forceinline__ void store_y(const GemmArgs& a, int64_t m, int64_t n, float v) {
     if (a.y_f32)
         static_cast<float*>(a.y)[m * a.ldy + n] = v;
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
 #pragma unroll
         for (int k = 0; k < KW; ++k) s += red[k * WN * MT * 256 + from];
         if (a.S > 1)
-            a.part[((int64_t)blockIdx.y * a.M + m0 + m) * a.N + nn] = s;
+            a.part[((int64_t)blockIdx.y * a.M + m0 + m) * part_row(a.N) + nn] = s;
         else
             store_y(a, m0 + m, nn, s);
     }
@@ -502,19 +505,22 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
     // lane (c, q): row c of a 16-row tile of x, weight rows 4 q .. 4 q + 3
     const int64_t n0 = (int64_t)bn * T::BN + w * R * 16;
     const bool f32 = a.S > 1 || a.y_f32;
-    const int64_t ld = a.S > 1 ? a.N : a.ldy;
-    uint8_t* out = a.S > 1 ? reinterpret_cast<uint8_t*>(a.part + (int64_t)slice * a.M * a.N)
-                           : static_cast<uint8_t*>(a.y);
+    const int64_t ld = a.S > 1 ? part_row(a.N) : a.ldy;
+    uint8_t* out = a.S > 1
+                       ? reinterpret_cast<uint8_t*>(a.part + (int64_t)slice * a.M * part_row(a.N))
+                       : static_cast<uint8_t*>(a.y);
     const int size = f32 ? 4 : 2;
-    // 16 bytes at a time where every row of y starts on such a boundary
-    const bool wide = ld % (16 / size) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    // 16 bytes at a time on any boundary that y's type has (5003 x 17376, M = 1024: 122 us
+    // with single values, 120)
+    typedef uint32_t pairs_t __attribute__((ext_vector_type(4), aligned(2)));
+    typedef float four_t __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const int64_t m = m0 + 16 * i + c;
         uint8_t* o = out + (m * ld + n0) * size;
 #pragma unroll
         for (int r = 0; r < R; r += 2) {
-            if (!f32 && wide && n0 + 16 * (r + 2) <= a.N) {
+            if (!f32 && n0 + 16 * (r + 2) <= a.N) {
                 // BF16: lanes q and q ^ 1 trade halves of two tiles, and hold eight outputs
                 // in a row each (64 bytes of a row a store instead of 32)
                 const f32x4_t v = acc[i][r], v2 = acc[i][r + 1];
@@ -525,8 +531,8 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
                 mx4::swap16(p0, p2);
                 mx4::swap16(p1, p3);
                 if (m < a.M)
-                    *reinterpret_cast<u32x4_t*>(o + 2 * (16 * (r + (q & 1)) + 8 * (q >> 1))) =
-                        u32x4_t{p0, p1, p2, p3};
+                    *reinterpret_cast<pairs_t*>(o + 2 * (16 * (r + (q & 1)) + 8 * (q >> 1))) =
+                        pairs_t{p0, p1, p2, p3};
                 continue;
             }
 #pragma unroll
@@ -534,8 +540,8 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
                 const int n = 16 * (r + h) + 4 * q;
                 const f32x4_t v = acc[i][r + h];
                 const int64_t left = m < a.M ? a.N - n0 - n : 0;
-                if (f32 && wide && left >= 4) {
-                    *reinterpret_cast<f32x4_t*>(o + 4 * n) = v;
+                if (f32 && left >= 4) {
+                    *reinterpret_cast<four_t*>(o + 4 * n) = v;
                     continue;
                 }
 #pragma unroll
@@ -551,21 +557,28 @@ __global__ __launch_bounds__(WN * 64, 3) void tile_kernel(GemmArgs a, int mb, in
     }
 }
 
-// y = the slices' partial sums in slice order.
+// y = the slices' partial sums in slice order, four to a thread.
 __global__ __launch_bounds__(256) void join_kernel(GemmArgs a) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t MN = (int64_t)a.M * a.N;
-    if (i >= MN) return;
-    float s = 0.f;
+    const int64_t row = part_row(a.N), all = a.M * row;
+    if (4 * i >= all) return;
+    f32x4_t s = {0, 0, 0, 0};
 #pragma unroll 8
-    for (int v = 0; v < a.S; ++v) s += a.part[v * MN + i];
-    store_y(a, i / a.N, i % a.N, s);
+    for (int v = 0; v < a.S; ++v) {
+        const f32x4_t p = *reinterpret_cast<const f32x4_t*>(a.part + v * all + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += p[e];
+    }
+    const int64_t m = 4 * i / row, n = 4 * i % row;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) store_y(a, m, n + e, s[e]);
 }
 
 hipError_t launch_join(const GemmArgs& a, hipStream_t s) {
     if (a.S > 1) {
-        const int64_t MN = (int64_t)a.M * a.N;
-        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((MN + 255) / 256)), dim3(256), 0, s, a);
+        const int64_t fours = a.M * part_row(a.N) / 4;
+        hipLaunchKernelGGL(join_kernel, dim3((unsigned)((fours + 255) / 256)), dim3(256), 0, s, a);
     }
     return hipGetLastError();
 }
@@ -712,7 +725,7 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (M == 0) return 0;
     const Plan p = plan_gemm(M, N, K);
-    return p.S > 1 ? (size_t)p.S * M * N * 4 : 0;
+    return p.S > 1 ? (size_t)p.S * M * part_row(N) * 4 : 0;
 }
 
 hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {

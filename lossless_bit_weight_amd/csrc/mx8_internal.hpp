@@ -132,7 +132,7 @@ struct GemmArgs {
     int64_t ldy;
     int y_f32;
     int S, gs;              // K slices over workgroups, groups a slice (a multiple of 4)
-    float* part;            // S > 1: partial sums [S][M][N]
+    float* part;            // S > 1: partial sums [S][M][N rounded up to 4]
 };
 
 hipError_t launch_quantize(const void* x, int x_f32, int64_t R, int64_t K, int64_t ldx,
