@@ -399,6 +399,9 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
                             __builtin_amdgcn_readlane(__double2loint(v), lane));
 }
 
+// A grid's x holds fewer than 2^32 work items: more sequences go along y.
+constexpr int kGridX = 1 << 21;
+
 // T threads of NV vectors: the chunks are those of parts_kernel.
 template <bool F32, int NV, int T>
 __global__ __launch_bounds__(T) void pick_kernel(Args a) {
@@ -406,7 +409,9 @@ __global__ __launch_bounds__(T) void pick_kernel(Args a) {
     __shared__ StopSpace space;
     __shared__ int where, hit, final;
     __shared__ double below;
-    const int b = blockIdx.x, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int b = blockIdx.y * kGridX + blockIdx.x;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    if (b >= a.B) return;
     const int64_t row0 = (int64_t)b * (a.D + 1);
     const double u = a.uniforms[row0 + a.D];
     Stop s;
@@ -557,7 +562,9 @@ hipError_t launch(const Args& a, hipStream_t s) {
     if (a.probs != nullptr)
         hipLaunchKernelGGL((rest_kernel<F32, NV>), grid(a.B), dim3(kThreads), 0, s, a);
     constexpr int kWide = NV >= 4 ? 4 : 1;      // a long chunk over more threads
-    hipLaunchKernelGGL((pick_kernel<F32, NV / kWide, kThreads * kWide>), dim3((unsigned)a.B),
+    const dim3 picks((unsigned)(a.B < kGridX ? a.B : kGridX),
+                     (unsigned)((a.B + kGridX - 1) / kGridX));
+    hipLaunchKernelGGL((pick_kernel<F32, NV / kWide, kThreads * kWide>), picks,
                        dim3(kThreads * kWide), 0, s, a);
     return hipGetLastError();
 }

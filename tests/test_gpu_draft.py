@@ -255,3 +255,18 @@ def test_tokens_follow_the_targets_distribution():
     tokens, _ = draft.draft_verify(logits, drafts, u, draft_probs=q)
     f = np.bincount(tokens[:, 0].cpu().numpy(), minlength=V) / B
     assert np.all(np.abs(f - p) <= 6 * np.sqrt(p * (1 - p) / B))
+
+
+def test_more_sequences_than_one_launch_axis_holds():
+    """2^22 and some sequences by workgroups of 1024 threads: more than 2^32 work items."""
+    P, V = 64, 5
+    B = (1 << 22) + 2 * P
+    rng = np.random.default_rng(4)
+    logits, u = _dev(rng.standard_normal((P, 1, V))), _dev(rng.random((P, 1)))
+    none = torch.empty(P, 0, dtype=torch.int32, device="cuda")
+    want, _ = draft.draft_verify(logits, none, u)
+    assert len(set(want.flatten().tolist())) == V
+    tokens, accepted = draft.draft_verify(logits.repeat(B // P, 1, 1),
+                                          none.new_empty((B, 0)), u.repeat(B // P, 1))
+    assert torch.equal(tokens.view(-1, P), want.view(1, P).expand(B // P, P))
+    assert bool((accepted == 0).all())
