@@ -28,6 +28,9 @@ __device__ __forceinline__ double row_sum(double v, double* part) {
     return v;
 }
 
+// A grid's x holds fewer than 2^32 work items: more blocks go along y.
+constexpr int64_t kGridX = (int64_t)1 << 21;
+
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 
 // RES: 0 none, 1 BF16, 2 fp32
@@ -36,7 +39,8 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_kernel(NormArgs a) {
     __shared__ double part[TPR > 64 ? TPR / 64 : 1];
     constexpr int kRows = threads_of(TPR) / TPR;
     const int t = threadIdx.x % TPR;
-    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    int64_t row =
+        ((int64_t)blockIdx.y * kGridX + blockIdx.x) * kRows + threadIdx.x / TPR;
     const bool live = row < a.M;
     if (!live) row = a.M - 1;           // (a row of its own wave or lanes: nothing is stored)
 
@@ -130,7 +134,10 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_kernel(NormArgs a) {
 template <int TPR, int C>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
     constexpr int kRows = threads_of(TPR) / TPR;
-    const dim3 grid((unsigned)((a.M + kRows - 1) / kRows)), block(threads_of(TPR));
+    const int64_t blocks = (a.M + kRows - 1) / kRows;
+    const dim3 grid((unsigned)(blocks < kGridX ? blocks : kGridX),
+                    (unsigned)((blocks + kGridX - 1) / kGridX));
+    const dim3 block(threads_of(TPR));
     const int res = a.res == nullptr ? 0 : a.res_f32 ? 2 : 1;
     switch (res * 2 + a.x_f32) {
         case 0: hipLaunchKernelGGL((norm_kernel<TPR, C, false, 0>), grid, block, 0, s, a); break;

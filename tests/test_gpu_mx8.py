@@ -228,6 +228,23 @@ def test_norm_in_place(dtype):
     assert torch.equal(y, x) and torch.equal(s, r)
 
 
+def test_norm_of_more_rows_than_one_launch_axis_holds():
+    """2^22 and some rows by workgroups of 1024 threads: more than 2^32 work items."""
+    M, K, P = (1 << 22) + 3 * 32, 4128, 32
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("60 GiB of memory")
+    rows = _dev(_values((P, K), 8))
+    w = _dev(_values(K, 9))
+    want = mx8.mx8_rms_norm(rows, w, out_dtype=torch.bfloat16)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    x.view(-1, P, K).copy_(rows)
+    mx8.mx8_rms_norm(x, w, out=x)
+    for first in (0, 1 << 20, (1 << 21) - P, 1 << 21, (1 << 22) - P, 1 << 22, M - P):
+        assert torch.equal(x[first:first + P], want)
+    del x
+    torch.cuda.empty_cache()
+
+
 def test_norm_of_views():
     full = _dev(_values((7, 160), 4))
     rfull = _dev(_values((7, 200), 5), torch.float32)
@@ -247,7 +264,7 @@ def test_norm_of_views():
 
 # few rows, tiles of 16, 32, 64, 128 rows and one past them; ragged N and K; a long K; then
 # every kernel by its rule: waves that split K over one tile (4, 8 of them) and two, 16 rows
-# shared by 2 x 2 waves and by 4 and 5, 32 rows in units of four and two groups, tiles of
+# shared by 2 x 2 waves and by 4 and 5, 32 rows, tiles of
 # 32 x 128, 64 x 128 (whole and in slices) and 64 x 256
 GEMM_SHAPES = [(16, 5000, 544), (16, 7000, 6176), (13, 512, 6176), (129, 3000, 160),
                (5, 16400, 4128), (16, 23000, 4096), (160, 5120, 640), (256, 5000, 12320),
