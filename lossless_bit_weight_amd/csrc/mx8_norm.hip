@@ -1,29 +1,31 @@
 // mx8_norm.hip -- residual addition, root-mean-square norm and its output in BF16,
 // fp32 or MX8 (../../include/mx8.h states the operation).
 //
-// s = x + residual is read once and stays in registers: TPR threads hold a row, C
-// chunks of eight values each, thread t the chunks t + TPR i.  The sum of squares is
-// held in 64 bits (two instructions a value beside the memory's time), so that no
-// square overflows that s itself does not.  Then y = s * r * weight from the
-// registers; in MX8 the four lanes of a quad hold one block.  One pass over the
-// data, bound by memory.
+// s = x + residual is read once and stays in registers: a row's threads hold C chunks of
+// eight values each, thread t of T the chunks t + T i.  The sum of squares is held in 64
+// bits (two instructions a value beside the memory's time), so that no square overflows
+// that s itself does not.  Then y = s * r * weight from the registers; in MX8 the four
+// lanes of a quad hold one block.
+// One pass over the data, bound by memory: 4096 x 5120, fp32 x, BF16 residual, MX8 out:
+// 34.0 us (189 MB, 5.6 TB/s, part of it from the last-level cache); 20680 x 128, BF16 in
+// and out, 4.4 us (10.6 MB, 2.4 TB/s with the launch's start and end).  One row of 5120,
+// 3.6 us, is a launch's start and end and the way to memory and back.
 #include "mx8_internal.hpp"
 
 namespace mx8 {
 namespace {
 
-template <int TPR>
+// Over the T threads of a row, or (T = 0) over the workgroup.
+template <int T>
 __device__ __forceinline__ double row_sum(double v, double* part) {
-    constexpr int kLanes = TPR < 64 ? TPR : 64;
+    constexpr int kLanes = T != 0 ? T : 64;
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    if constexpr (TPR > 64) {
-        const int w = threadIdx.x >> 6;
-        if ((threadIdx.x & 63) == 0) part[w] = v;
+    if constexpr (T == 0) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
         __syncthreads();
         v = 0.0;
-#pragma unroll
-        for (int i = 0; i < TPR / 64; ++i) v += part[i];
+        for (int i = 0; i < (int)blockDim.x / 64; ++i) v += part[i];
     }
     return v;
 }
@@ -31,18 +33,20 @@ __device__ __forceinline__ double row_sum(double v, double* part) {
 // A grid's x holds fewer than 2^32 work items: more blocks go along y.
 constexpr int64_t kGridX = (int64_t)1 << 21;
 
-constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+constexpr int kMost = 1024;             // threads of a row
 
+// T: threads of a row, of which a workgroup of 256 has several; 0: a row's are the workgroup.
 // RES: 0 none, 1 BF16, 2 fp32
-template <int TPR, int C, bool XF32, int RES>
-__global__ __launch_bounds__(threads_of(TPR)) void norm_kernel(NormArgs a) {
-    __shared__ double part[TPR > 64 ? TPR / 64 : 1];
-    constexpr int kRows = threads_of(TPR) / TPR;
-    const int t = threadIdx.x % TPR;
-    int64_t row =
-        ((int64_t)blockIdx.y * kGridX + blockIdx.x) * kRows + threadIdx.x / TPR;
+template <int T, int C, bool XF32, int RES>
+__global__ __launch_bounds__(T != 0 ? 256 : kMost) void norm_kernel(NormArgs a) {
+    __shared__ double part[T != 0 ? 1 : kMost / 64];
+    constexpr int kRows = T != 0 ? 256 / T : 1;
+    const int TPR = T != 0 ? T : (int)blockDim.x;
+    const int t = T != 0 ? threadIdx.x % T : threadIdx.x;
+    int64_t row = ((int64_t)blockIdx.y * kGridX + blockIdx.x) * kRows;
+    if constexpr (T != 0) row += threadIdx.x / T;
     const bool live = row < a.M;
-    if (!live) row = a.M - 1;           // (a row of its own wave or lanes: nothing is stored)
+    if (!live) row = a.M - 1;           // (lanes or a workgroup of their own: nothing is stored)
 
     // (the weights of long rows are read behind the sum: there are no registers for them)
     constexpr bool kEarly = C <= 2;
@@ -89,7 +93,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_kernel(NormArgs a) {
             }
         }
     }
-    sum = row_sum<TPR>(sum, part);
+    sum = row_sum<T>(sum, part);
     double r64 = 1.0 / __builtin_sqrt(sum / a.K + (double)a.eps);
     // a factor outside fp32's normal range: a power of two (exact) goes to the values first
     if (r64 < 0x1p-100 || r64 > 0x1p100) {
@@ -131,36 +135,41 @@ __global__ __launch_bounds__(threads_of(TPR)) void norm_kernel(NormArgs a) {
     }
 }
 
-template <int TPR, int C>
+template <int T, int C>
 hipError_t launch(const NormArgs& a, hipStream_t s) {
-    constexpr int kRows = threads_of(TPR) / TPR;
+    constexpr int kRows = T != 0 ? 256 / T : 1;
     const int64_t blocks = (a.M + kRows - 1) / kRows;
     const dim3 grid((unsigned)(blocks < kGridX ? blocks : kGridX),
                     (unsigned)((blocks + kGridX - 1) / kGridX));
-    const dim3 block(threads_of(TPR));
+    const dim3 block(T != 0 ? 256 : (a.K / 8 + 64 * C - 1) / (64 * C) * 64);
     const int res = a.res == nullptr ? 0 : a.res_f32 ? 2 : 1;
     switch (res * 2 + a.x_f32) {
-        case 0: hipLaunchKernelGGL((norm_kernel<TPR, C, false, 0>), grid, block, 0, s, a); break;
-        case 1: hipLaunchKernelGGL((norm_kernel<TPR, C, true, 0>), grid, block, 0, s, a); break;
-        case 2: hipLaunchKernelGGL((norm_kernel<TPR, C, false, 1>), grid, block, 0, s, a); break;
-        case 3: hipLaunchKernelGGL((norm_kernel<TPR, C, true, 1>), grid, block, 0, s, a); break;
-        case 4: hipLaunchKernelGGL((norm_kernel<TPR, C, false, 2>), grid, block, 0, s, a); break;
-        default: hipLaunchKernelGGL((norm_kernel<TPR, C, true, 2>), grid, block, 0, s, a);
+        case 0: hipLaunchKernelGGL((norm_kernel<T, C, false, 0>), grid, block, 0, s, a); break;
+        case 1: hipLaunchKernelGGL((norm_kernel<T, C, true, 0>), grid, block, 0, s, a); break;
+        case 2: hipLaunchKernelGGL((norm_kernel<T, C, false, 1>), grid, block, 0, s, a); break;
+        case 3: hipLaunchKernelGGL((norm_kernel<T, C, true, 1>), grid, block, 0, s, a); break;
+        case 4: hipLaunchKernelGGL((norm_kernel<T, C, false, 2>), grid, block, 0, s, a); break;
+        default: hipLaunchKernelGGL((norm_kernel<T, C, true, 2>), grid, block, 0, s, a);
     }
     return hipGetLastError();
 }
 
 }  // namespace
 
+// A chunk a thread keeps most loads on their way and the fewest behind each other; a row of
+// up to 64 threads is a part of a wave or a wave (40000 x 128: 16 threads 10.8 us, 64 23.7;
+// 40000 x 256: 32 threads 17.6, 64 26.2).  Beyond 512 chunks many rows go faster by two, as
+// a CU has places for more workgroups at different points of their rows (4096 x 5120: two
+// 34.0 us, one 39.8; 4096 x 4096: 25.3 and 25.0; 64 x 5120: 4.7 and 4.1; 1024 x 7168: 14.7
+// and 15.9).  More than two only where 1024 threads need them.
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     const int chunks = a.K / 8;
     if (chunks <= 16) return launch<16, 1>(a, s);
+    if (chunks <= 32) return launch<32, 1>(a, s);
     if (chunks <= 64) return launch<64, 1>(a, s);
-    if (chunks <= 256) return launch<256, 1>(a, s);
-    if (chunks <= 512) return launch<512, 1>(a, s);
-    if (chunks <= 1024) return launch<1024, 1>(a, s);
-    if (chunks <= 2048) return launch<1024, 2>(a, s);
-    return launch<1024, 4>(a, s);
+    if (chunks <= 512 || (chunks <= kMost && a.M < 512)) return launch<0, 1>(a, s);
+    if (chunks <= 2 * kMost) return launch<0, 2>(a, s);
+    return launch<0, 4>(a, s);
 }
 
 }  // namespace mx8

@@ -180,8 +180,8 @@ def test_norm_widths(M, K):
     _norm_case(M, K, "f32", "none", "f32", "f32")
 
 
-@pytest.mark.parametrize("K", [128, 512, 5120])
-@pytest.mark.parametrize("M", [257, 2049])
+@pytest.mark.parametrize("K", [128, 224, 256, 512, 544, 4096, 5120, 8192])
+@pytest.mark.parametrize("M", [257, 511, 512, 2049])
 def test_norm_many_rows(M, K):
     _norm_case(M, K, "bf16", "bf16", "bf16", "bf16")
 
@@ -229,7 +229,7 @@ def test_norm_in_place(dtype):
 
 
 def test_norm_of_more_rows_than_one_launch_axis_holds():
-    """2^22 and some rows by workgroups of 1024 threads: more than 2^32 work items."""
+    """2^22 and some rows, a workgroup each: the grid's second axis."""
     M, K, P = (1 << 22) + 3 * 32, 4128, 32
     if torch.cuda.mem_get_info()[0] < 60 << 30:
         pytest.skip("60 GiB of memory")
