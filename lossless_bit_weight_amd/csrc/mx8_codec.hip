@@ -4,7 +4,9 @@
 // A wave takes 512 values of one row, a lane eight: the four lanes of a block
 // agree on its largest exponent in two quad permutes, every load and store of a
 // wave is contiguous, and the wave writes the 16 scale bytes of its 512 values,
-// those past K too.  Bound by memory: 2 (4) + 1.03 bytes a value.
+// those past K too.  Bound by memory: 2 (4) + 1.03 bytes a value: 4096 x 5120 BF16 to MX8
+// 13.6 us (4.7 TB/s), back 11.4 (5.6 TB/s).  Two pieces of a row a lane: 13.2, but 2.8
+// instead of 2.3 for one row; of fp32 17.3 instead of 16.9.
 #include "mx8_internal.hpp"
 
 namespace mx8 {
