@@ -615,7 +615,10 @@ hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
 constexpr int64_t kFarRows = (int64_t)1 << 24;
 
 // Kernel and split of a product.
-enum Kernel { kOne4, kOne8, kTwo4, kTwo8, kMid16x2, kMid16, kMid32, kTile32, kTile64, kTile64x4 };
+enum Kernel {
+    kOne4, kOne8, kTwo4, kTwo8, kMid16x2, kMid16, kMid32,
+    kTile32, kTile64, kTile64x5, kTile64x8      // and past: tile_kernel
+};
 struct Plan {
     Kernel kernel;
     int wn;                 // kMid16: waves beside each other
@@ -630,27 +633,45 @@ int spread(int64_t nt) {
     return most(5) <= most(4) ? 5 : 4;
 }
 
-// Slices of Q quads for a product by `blocks` tiles, and its time in us: a quad takes `least`
-// however little there is to do, `each` for every workgroup of the busiest CU beyond that;
-// joining slices costs a launch and their sums written and read.  Measured, 64 x 128 tiles:
-// 5120 x 17408, M = 64, 40 tiles: 6 slices 20.3, 3 27.4, 12 22.5; M = 256, 160 tiles: 3 41.2,
-// 2 44.8, 1 54.5; 7168 x 5120, M = 256, 224 tiles: 1 19.8, 2 26.6.
-double slice(int64_t blocks, int64_t M, int64_t N, int Q, double least, double each,
-             int* slices) {
+// The tile kernels: a quad of K takes the busiest CU `fixed` and `each` for every workgroup
+// that it has, and `least` at least (us; fitted to 190 products of 33 to 2048 rows by up to
+// 65536 x 1024 and 5120 x 17408 in 1 to 12 slices, of which the choice is within 0.6% of the
+// best measured one in the mean, 9% at most).  More columns a workgroup reread x less and
+// split the CUs coarser: 34816 x 5120, us by 32 x 128, 64 x 128, 64 x 160 and 64 x 256:
+// M = 64 30.5 / 34.4 / 26.3 / 39.1, 128 45.8 / 40.9 / 38.4 / 40.9, 256 76 / 63 / 77 / 55.
+struct Shape {
+    Kernel kernel;
+    int bm, bn;
+    double least, fixed, each;
+};
+constexpr Shape kShapes[] = {{kTile32, 32, 128, 0.0, 0.54, 0.75},
+                             {kTile64, 64, 128, 0.0, 0.79, 0.93},
+                             {kTile64x5, 64, 160, 0.0, 0.97, 1.23},
+                             {kTile64x8, 64, 256, 3.16, 0.26, 1.65}};
+
+// The one of them, and the slices of Q quads, that a product takes the least time by; joining
+// slices costs a launch and their sums written and read (5120 x 17408, M = 64, 64 x 128: 6
+// slices 20.3, 3 27.4, 12 22.5, M = 256: 3 41.2, 2 44.8, 1 54.5).
+Kernel pick_tile(int64_t M, int64_t N, int Q, int64_t* slices) {
+    Kernel kernel = kTile64x8;
     double best = 0.0;
     *slices = 0;
-    for (int S = 1; S <= Q && S <= 64; ++S) {
-        const int qs = (Q + S - 1) / S;
-        if ((Q + qs - 1) / qs != S) continue;
-        const double busy = each * (double)((blocks * S + 255) / 256);
-        const double join = S > 1 ? 3.0 + (double)S * M * N * 8 / 3.2e6 : 0.0;
-        const double time = qs * (busy > least ? busy : least) + join;
-        if (*slices == 0 || time < best) {
-            best = time;
-            *slices = S;
+    for (const Shape& h : kShapes) {
+        const int64_t blocks = (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn);
+        for (int S = 1; S <= Q && S <= 64 && (S == 1 || blocks * S <= 2048); ++S) {
+            const int qs = (Q + S - 1) / S;
+            if ((Q + qs - 1) / qs != S) continue;
+            const double busy = h.fixed + h.each * (double)((blocks * S + 255) / 256);
+            const double join = S > 1 ? 1.7 + (double)S * M * N * 8 / 3.2e6 : 0.0;
+            const double time = qs * (busy > h.least ? busy : h.least) + join;
+            if (*slices == 0 || time < best) {
+                best = time;
+                *slices = S;
+                kernel = h.kernel;
+            }
         }
     }
-    return best;
+    return kernel;
 }
 
 // By rows of x (M), tiles of 16 weight rows (nt), pairs of a weight tile and 16 rows of x
@@ -668,11 +689,7 @@ double slice(int64_t blocks, int64_t M, int64_t N, int Q, double least, double e
 //     each other (1024 x 1024 M = 64 3.2, 32 rows through LDS 5.0; 7168 x 5120 M = 33 12.9,
 //     32 rows 14.0; MX4 x 10.0), then 32 rows (M = 96 17.2, 32 x 128 tiles 17.7); of a long K
 //     32 rows in slices up to M = 32 (5120 x 17408 M = 17 16.4, MX4 x 15.3).
-//   else tiles: 32 x 128 for many of them up to M = 64 (34816 x 5120 M = 64 30.4, 64 x 128
-//     34.4; MX4 x 25.9); 64 x 256 if they give 384 workgroups (M = 512 91, 64 x 128 110;
-//     M = 4096 574 to 600; MX4 x 66 and 389); else, in slices, what slice() gives less time
-//     for, 64 x 128 or 32 x 128 (7168 x 5120 M = 512 25.7 and 33.6, M = 160 19.2 and 18.5;
-//     MX4 x 20.4 and 15.4).
+//   else tiles by pick_tile().
 Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
     const int G = (int)mx4::groups(K), Q = (int)mx4::quads(K);
     const int64_t nt = tiles(N), t = nt * tiles(M);
@@ -706,17 +723,8 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
                    : t <= 1200 ? kMid16x2
                    : t <= 2000 ? kMid16
                                : kMid32;
-    } else if (many && M <= 64) {
-        p.kernel = kTile32;
-    } else if (blocks(64, 256) >= 384) {
-        p.kernel = kTile64x4;
     } else {
-        int s64, s32;
-        const double t64 = slice(blocks(64, 128), M, N, Q, 1.5, 1.03, &s64);
-        const double t32 = slice(blocks(32, 128), M, N, Q, 1.25, 0.72, &s32);
-        const bool small = t32 < 0.97 * t64;
-        p.kernel = small ? kTile32 : kTile64;
-        S = small ? s32 : s64;
+        p.kernel = pick_tile(M, N, Q, &S);
     }
     if (S < 1) S = 1;
     const int qs = (int)((Q + S - 1) / S);      // quads a slice
@@ -753,7 +761,8 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
         case kMid32: return launch_mid<2, 4, 1>(a, s);
         case kTile32: return launch_tile<2, 2, 4, 2>(a, s);
         case kTile64: return launch_tile<4, 2, 4, 2>(a, s);
-        case kTile64x4: return launch_tile<4, 4, 4, 1>(a, s);
+        case kTile64x5: return launch_tile<4, 2, 5, 2>(a, s);
+        case kTile64x8: return launch_tile<4, 4, 4, 1>(a, s);
         default: return launch_small<1, 4>(a, s);
     }
 }
