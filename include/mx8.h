@@ -77,9 +77,11 @@ int mx8_dequantize(const void *values, int64_t ldv, const void *scales, int64_t 
 
 /*
  * mx8_rms_norm -- a residual stream's addition and the norm behind it:
- *   s    = x + residual, rounded to the residual's type (x itself without one);
- *   y    = s / sqrt(mean(s^2) + eps) * weight, rounded once to y's type.
- * The sum of squares and the root are 64 bits wide, the products fp32.
+ *   s    = x + residual in fp32, rounded to the residual's type (x itself without
+ *          one);
+ *   y    = s / sqrt(mean(s^2) + eps) * weight, rounded once to fp32 or MX8, or to
+ *          BF16 from fp32.
+ * Squares, their sum, the root and the products are 64 bits wide.
  *   x, residual   : device [M, K], BF16 bits or fp32 as x_type and res_type say,
  *                   row strides ldx and ldr elements; residual may be NULL.
  *   residual_out  : device [M, K] output for s, of res_type, row stride ldo; it

@@ -4,11 +4,11 @@
 // s = x + residual is read once and stays in registers: a row's threads hold C chunks of
 // eight values each, thread t of T the chunks t + T i.  The sum of squares is held in 64
 // bits (two instructions a value beside the memory's time), so that no square overflows
-// that s itself does not.  Then y = s * r * weight from the registers; in MX8 the four
-// lanes of a quad hold one block.
+// that s itself does not, and so is y = s * r * weight, from the registers, to be rounded
+// once (BF16: from fp32); in MX8 the four lanes of a quad hold one block.
 // One pass over the data, bound by memory: 4096 x 5120, fp32 x, BF16 residual, MX8 out:
-// 34.0 us (189 MB, 5.6 TB/s, part of it from the last-level cache); 20680 x 128, BF16 in
-// and out, 4.4 us (10.6 MB, 2.4 TB/s with the launch's start and end).  One row of 5120,
+// 35.9 us (189 MB, 5.3 TB/s, part of it from the last-level cache); 20680 x 128, BF16 in
+// and out, 4.9 us (10.6 MB, 2.2 TB/s with the launch's start and end).  One row of 5120,
 // 3.6 us, is a launch's start and end and the way to memory and back.
 #include "mx8_internal.hpp"
 
@@ -28,6 +28,17 @@ __device__ __forceinline__ double row_sum(double v, double* part) {
         for (int i = 0; i < (int)blockDim.x / 64; ++i) v += part[i];
     }
     return v;
+}
+
+// y in fp32's 24 bits, cut off, the last of them set if anything was cut: rounding that to
+// MX8 is the same as rounding y itself.  (Of values rounded to fp32 first, some in a million
+// land on a border of MX8 and go the wrong way from there.)  With it and the products in 64
+// bits 4096 x 5120 to MX8 takes 35.9 us; in fp32 throughout it took 33.7.
+__device__ __forceinline__ float to_odd(double y) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, y);
+    const uint32_t lo = (uint32_t)u, rest = lo & 0x1FFFFFFFu;
+    const uint32_t odd = rest != 0 ? 0x20000000u : 0u;
+    return (float)__builtin_bit_cast(double, (u & ~(uint64_t)0x1FFFFFFFu) | odd);
 }
 
 // A grid's x holds fewer than 2^32 work items: more blocks go along y.
@@ -94,24 +105,17 @@ __global__ __launch_bounds__(T != 0 ? 256 : kMost) void norm_kernel(NormArgs a) 
         }
     }
     sum = row_sum<T>(sum, part);
-    double r64 = 1.0 / __builtin_sqrt(sum / a.K + (double)a.eps);
-    // a factor outside fp32's normal range: a power of two (exact) goes to the values first
-    if (r64 < 0x1p-100 || r64 > 0x1p100) {
-        const float p = r64 > 1.0 ? 0x1p64f : 0x1p-64f;
-        r64 *= r64 > 1.0 ? 0x1p-64 : 0x1p64;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i].f[j] *= p;
-    }
-    const float r = (float)r64;
+    const double r = 1.0 / __builtin_sqrt(sum / a.K + (double)a.eps);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int k = 8 * (t + TPR * i);
         Eight& wi = w[kEarly ? i : 0];
         if constexpr (!kEarly) weights(wi, k < a.K ? k : 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i].f[j] = v[i].f[j] * r * wi.f[j];
+        for (int j = 0; j < 8; ++j) {
+            const double y = (double)v[i].f[j] * r * (double)wi.f[j];
+            v[i].f[j] = a.y_type == 2 ? to_odd(y) : (float)y;
+        }
         const bool in = live && k < a.K;
         if (a.y_type == 2) {
             uint32_t e;
