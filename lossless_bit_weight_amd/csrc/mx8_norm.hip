@@ -162,16 +162,16 @@ hipError_t launch(const NormArgs& a, hipStream_t s) {
 
 // A chunk a thread keeps most loads on their way and the fewest behind each other; a row of
 // up to 64 threads is a part of a wave or a wave (40000 x 128: 16 threads 10.8 us, 64 23.7;
-// 40000 x 256: 32 threads 17.6, 64 26.2).  Beyond 512 chunks many rows go faster by two, as
+// 40000 x 256: 32 threads 19.0, 64 30.1).  Beyond 512 chunks many rows go faster by two, as
 // a CU has places for more workgroups at different points of their rows (4096 x 5120: two
-// 34.0 us, one 39.8; 4096 x 4096: 25.3 and 25.0; 64 x 5120: 4.7 and 4.1; 1024 x 7168: 14.7
-// and 15.9).  More than two only where 1024 threads need them.
+// 35.9 us, one 41.2; 4096 x 7168: 48.7 and 61.6; 4096 x 4096: 27.2 and 26.7; 512 x 5120: 8.8
+// and 8.6; 64 x 5120: 5.2 and 4.5).  More than two only where 1024 threads need them.
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     const int chunks = a.K / 8;
     if (chunks <= 16) return launch<16, 1>(a, s);
     if (chunks <= 32) return launch<32, 1>(a, s);
     if (chunks <= 64) return launch<64, 1>(a, s);
-    if (chunks <= 512 || (chunks <= kMost && a.M < 512)) return launch<0, 1>(a, s);
+    if (chunks <= 512 || (chunks <= kMost && a.M <= 1024)) return launch<0, 1>(a, s);
     if (chunks <= 2 * kMost) return launch<0, 2>(a, s);
     return launch<0, 4>(a, s);
 }
