@@ -183,7 +183,7 @@ def test_norm_widths(M, K):
 
 
 @pytest.mark.parametrize("K", [128, 224, 256, 512, 544, 4096, 5120, 8192])
-@pytest.mark.parametrize("M", [257, 511, 512, 2049])
+@pytest.mark.parametrize("M", [257, 1024, 1025, 2049])
 def test_norm_many_rows(M, K):
     _norm_case(M, K, "bf16", "bf16", "bf16", "bf16")
 
