@@ -770,9 +770,9 @@ int spread(int64_t nt, bool few_rows) {
     return best;
 }
 
+// The figures below were taken with flat loads in the tile and 16-row kernels; as global
+// ones they take 2 to 17% less on either side of these rules.
 // By rows of x (M), tiles of 16 weight rows (nt) and groups of K (G).  Measured on
-// (Measured with flat loads in the tile and 16-row kernels; as global ones they take 2 to
-// 17% less on either side of these rules.)
 // QKV (nt = 448, G = 40), gate+up (2176, 40) and down (320, 136), us:
 //   up to 16 rows, BF16 x: every wave on its own x for few tiles (QKV M = 1 6.9 against
 //     7.8 through LDS, M = 16 9.8 against 11.1); shared through LDS for many tiles
