@@ -432,7 +432,7 @@ def mx4_route(logits: torch.Tensor, top_k: int, scores: str = "softmax",
             raise ValueError("bias must be %d contiguous values" % E)
         bp = bias.data_ptr()
     top_k = int(top_k)
-    k = top_k if top_k > 0 else 0
+    k = top_k if 0 < top_k <= MAX_TOP_K else 0      # (another one is refused below)
     if experts is None:
         experts = logits.new_empty((T, k), dtype=torch.int32)
         ep = experts.data_ptr()
