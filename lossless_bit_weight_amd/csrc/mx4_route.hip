@@ -158,8 +158,9 @@ __global__ __launch_bounds__(256) void pick_kernel(RouteArgs a, int groups, int 
         top = __uint_as_float(m >> 31 ? m & 0x7FFFFFFFu : ~m);
     }
     double score[EV], sum = 1.0;
-    const bool all = any_bias || (limited && a.terms == 2) || (!a.sigmoid && !a.renormalize);
-    if (all) {
+    // who needs the scores of all experts, and who their softmax's sum
+    const bool all = any_bias || (limited && a.terms == 2);
+    if (all || (!a.sigmoid && !a.renormalize)) {
         if (a.sigmoid) {
 #pragma unroll
             for (int i = 0; i < EV; ++i) score[i] = sigmoid(l[i]);
@@ -171,8 +172,9 @@ __global__ __launch_bounds__(256) void pick_kernel(RouteArgs a, int groups, int 
                 sum += score[i];
             }
             sum = wave_sum(sum);
+            if (all)
 #pragma unroll
-            for (int i = 0; i < EV; ++i) score[i] = bad ? __builtin_nan("") : score[i] / sum;
+                for (int i = 0; i < EV; ++i) score[i] = bad ? __builtin_nan("") : score[i] / sum;
         }
     }
     uint32_t hi[EV], lo[EV];            // ranks; 0: not to be chosen
