@@ -125,7 +125,7 @@ int mx8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
     if (bytes == nullptr) return W12_ERR_NULL;
     *bytes = 0;
     if (int rc = check_gemm_shape(M, N, K)) return rc;
-    if (M > 0) *bytes = mx8::gemm_workspace_bytes(M, N, K);
+    if (M > 0) *bytes = mx8::plan_gemm(M, N, K).workspace;
     return W12_OK;
 }
 
@@ -139,8 +139,8 @@ int mx8_gemm(const void* x_values, int64_t ldv, const void* x_scales, int64_t ld
     if (int rc = check_y(y, N, ldy, y_type)) return rc;
     if (!aligned(w_codes, 16) || !aligned(w_scales, 16)) return W12_ERR_ALIGN;
     if (M == 0) return W12_OK;
-    if (int rc = check_ws(workspace, workspace_bytes, mx8::gemm_workspace_bytes(M, N, K)))
-        return rc;
+    const mx8::Plan plan = mx8::plan_gemm(M, N, K);
+    if (int rc = check_ws(workspace, workspace_bytes, plan.workspace)) return rc;
     mx8::GemmArgs a{};
     a.x = static_cast<const uint8_t*>(x_values);
     a.xs = static_cast<const uint8_t*>(x_scales);
@@ -155,7 +155,7 @@ int mx8_gemm(const void* x_values, int64_t ldv, const void* x_scales, int64_t ld
     a.y = y;
     a.ldy = ldy;
     a.y_f32 = y_type == W12_OUT_F32;
-    return status_of(mx8::launch_gemm(a, workspace, static_cast<hipStream_t>(stream)));
+    return status_of(mx8::launch_gemm(a, plan, workspace, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -158,8 +158,8 @@ hipError_t launch_small(const GemmArgs& a, hipStream_t s) {
 
 // ---- a few rows of x, shared through LDS ------------------------------------------
 // A workgroup: 16 MT rows of x by 16 WN weight rows; KW groups of WN waves take every
-// KW-th unit of four groups of K.  A unit's weights come to registers one unit ahead of
-// their products; its x goes through LDS, double-buffered, where the WN waves share it:
+// KW-th unit of four groups of K.  A unit's weights and x come to registers AHEAD units ahead
+// of their products; its x goes through LDS, double-buffered, where the WN waves share it:
 // row m of a unit is 32 pieces of 16 bytes, piece p at place (p & 16) | ((p ^ m) & 15).
 // A read takes one piece from 16 rows for each q; the LDS serves it 16 lanes at a time,
 // rows 0-3 and 12-15 of one q with rows 4-11 of the next, which lie in 16 different
@@ -176,7 +176,7 @@ struct Mid {
     }
 };
 
-template <int MT, int WN, int KW>
+template <int MT, int WN, int KW, int AHEAD>
 __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, int nb) {
     using T = Mid<MT, WN, KW>;
     constexpr int P = T::kPieces;
@@ -228,12 +228,13 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         const int m = m0 + 16 * t + c < a.M ? m0 + 16 * t + c : a.M - 1;
         xs[t] = a.xs + (int64_t)m * a.lds + 4 * q;
     }
-    u32x4_t wb[2][4], xb[P];
-    uint32_t ws[2], xsc[2][MT];
-    bool xin[P];
+    constexpr int kSlots = 2 * AHEAD;
+    u32x4_t wb[kSlots][4], xb[AHEAD][P];
+    uint32_t ws[kSlots], xsc[kSlots][MT];
+    bool xin[AHEAD][P];
     // (no branch: a place past the last unit, group or K is a valid one whose x is
     // replaced by zeros)
-    auto load = [&](int slot, int it) {
+    auto load = [&](int slot, int set, int it) {
         const int u = u0 + it * KW + kw;
         const int uc = u < u1 ? u : u1 - 1;
         ws[slot] = load4(scalar(sp + (int64_t)uc * kScaleBlock), lane4);
@@ -245,19 +246,19 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int k = u * 512 + xk[i];
-            xin[i] = u < u1 && k < a.K;
-            xb[i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[i] ? k : 0));
+            xin[set][i] = u < u1 && k < a.K;
+            xb[set][i] = *reinterpret_cast<const u32x4_t*>(xp[i] + (xin[set][i] ? k : 0));
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t)
             xsc[slot][t] = *reinterpret_cast<const uint32_t*>(xs[t] + 16 * uc);
     };
-    auto stage = [&](int buf) {
+    auto stage = [&](int set, int buf) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             u32x4_t v;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = xin[i] ? xb[i][e] : 0u;
+            for (int e = 0; e < 4; ++e) v[e] = xin[set][i] ? xb[set][i][e] : 0u;
             *reinterpret_cast<u32x4_t*>(mine + buf * T::kStage + at[i]) = v;
         }
     };
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
     for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0, 0, 0, 0};
     auto product = [&](auto sc) {
         constexpr int slot = decltype(sc)::value;
-        const uint8_t* xl = mine + slot * T::kStage;
+        const uint8_t* xl = mine + (slot & 1) * T::kStage;
         auto group = [&](auto jc) {
             constexpr int J = decltype(jc)::value;
 #pragma unroll
@@ -286,22 +287,29 @@ __global__ __launch_bounds__(WN* KW * 64) void mid_kernel(GemmArgs a, int mb, in
         group(std::integral_constant<int, 2>{});
         group(std::integral_constant<int, 3>{});
     };
-    load(0, 0);
-    stage(0);
+    load(0, 0, 0);
+    if constexpr (AHEAD == 2) load(1, 1, 1);
+    stage(0, 0);
     __syncthreads();
     auto step = [&](auto sc, int it) {
         constexpr int slot = decltype(sc)::value;
-        load(slot ^ 1, it + 1);
+        load((slot + AHEAD) % kSlots, slot % AHEAD, it + AHEAD);
         __builtin_amdgcn_sched_barrier(0);
         product(sc);
         __builtin_amdgcn_sched_barrier(0);
-        stage(slot ^ 1);
+        stage((slot + 1) % AHEAD, (slot & 1) ^ 1);
         __syncthreads();
     };
-    for (int it = 0; it < its; it += 2) {
+    for (int it = 0; it < its; it += kSlots) {
         step(std::integral_constant<int, 0>{}, it);
         if (it + 1 >= its) break;
         step(std::integral_constant<int, 1>{}, it + 1);
+        if constexpr (AHEAD == 2) {
+            if (it + 2 >= its) break;
+            step(std::integral_constant<int, 2>{}, it + 2);
+            if (it + 3 >= its) break;
+            step(std::integral_constant<int, 3>{}, it + 3);
+        }
     }
 
     // the k groups' sums in their order
@@ -599,14 +607,15 @@ hipError_t launch_tile(GemmArgs& a, hipStream_t s) {
     return launch_join(a, s);
 }
 
-template <int MT, int WN, int KW>
+template <int MT, int WN, int KW, int AHEAD>
 hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
     using T = Mid<MT, WN, KW>;
     static_assert(T::lds() <= 65536, "more LDS than a launch gets without asking");
     const int mb = (a.M + 16 * MT - 1) / (16 * MT);
     const int nb = (int)((tiles(a.N) + WN - 1) / WN);
-    hipLaunchKernelGGL((mid_kernel<MT, WN, KW>), dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S),
-                       dim3(T::kThreads), T::lds(), s, a, mb, nb);
+    hipLaunchKernelGGL((mid_kernel<MT, WN, KW, AHEAD>),
+                       dim3((unsigned)((int64_t)mb * nb), (unsigned)a.S), dim3(T::kThreads),
+                       T::lds(), s, a, mb, nb);
     return launch_join(a, s);
 }
 
@@ -614,15 +623,12 @@ hipError_t launch_mid(GemmArgs& a, hipStream_t s) {
 // takes them.
 constexpr int64_t kFarRows = (int64_t)1 << 24;
 
-// Kernel and split of a product.
-enum Kernel {
-    kOne4, kOne8, kTwo4, kTwo8, kMid16x2, kMid16, kMid32,
+// The kernels by their rows of x and of W: 16 x 16 by 4 or 8 waves that split K, 16 x 32 by 4;
+// 16 x 64 or 80 (M up to 16, many tiles); 16 x 32, 16 x 64 and 32 x 64 by two groups of waves
+// that split K; tiles.
+enum Kernel : int {
+    kOne4, kOne8, kTwo4, kMid16, kMid16x2, kMid16x4, kMid32x4,
     kTile32, kTile64, kTile64x5, kTile64x8      // and past: tile_kernel
-};
-struct Plan {
-    Kernel kernel;
-    int wn;                 // kMid16: waves beside each other
-    int S, gs;              // K slices, groups a slice (a multiple of 4)
 };
 
 // Four or five waves beside each other, whichever spreads nt tiles better over 256 CUs: the
@@ -633,120 +639,109 @@ int spread(int64_t nt) {
     return most(5) <= most(4) ? 5 : 4;
 }
 
-// The tile kernels: a quad of K takes the busiest CU `fixed` and `each` for every workgroup
-// that it has, and `least` at least (us; fitted to 190 products of 33 to 2048 rows by up to
-// 65536 x 1024 and 5120 x 17408 in 1 to 12 slices, of which the choice is within 0.6% of the
-// best measured one in the mean, 9% at most).  More columns a workgroup reread x less and
-// split the CUs coarser: 34816 x 5120, us by 32 x 128, 64 x 128, 64 x 160 and 64 x 256:
-// M = 64 30.5 / 34.4 / 26.3 / 39.1, 128 45.8 / 40.9 / 38.4 / 40.9, 256 76 / 63 / 77 / 55.
-struct Shape {
+// What a product costs in us: a launch and its start, `start`; for each of a wave's quads of K
+// `fixed` and, for every workgroup that the busiest CU has, `each` and `rows` times the share
+// of its rows that x has, `least` at least, and for all of them what the weights' bytes take
+// (7.7 TB/s: these come from the last-level cache in part); and with K in slices a launch
+// that joins their sums, written and read.  Fitted to 730 products, of 1 to 2048 rows, 512 to
+// 65536 weight rows and K = 544 to 17408, by every kernel here in 1 to 12 slices: the choice
+// takes 0.9% more than the best of them in the mean, a fifth at most.
+// Graphs over weights in turn, us:
+//                      16x16/4 16x16/8  16x32  16x64  32x64 32x128 64x128 64x160 64x256
+//   7168 x 5120  M = 1     6.1     6.2    6.5    7.6
+//                M = 16    9.6     9.8    7.3    9.5   12.1
+//                M = 64                  17.2   15.8   13.4   16.2   17.4
+//   4096 x 4096  M = 64   10.6            8.7    7.4    9.0   10.1
+//   34816 x 5120 M = 64                                       30.5   34.4   26.3   39.1
+//                M = 128                                      45.8   40.9   38.4   40.9
+//                M = 256                                      76     63     77     55
+//   5120 x 17408 M = 64 in 6 slices                                  20.3 (3: 27.4, 12: 22.5)
+struct Cost {
     Kernel kernel;
-    int bm, bn;
-    double least, fixed, each;
+    int bm, bn, waves_k;
+    bool sliced;
+    double start, least, fixed, each, rows;
 };
-constexpr Shape kShapes[] = {{kTile32, 32, 128, 0.0, 0.54, 0.75},
-                             {kTile64, 64, 128, 0.0, 0.79, 0.93},
-                             {kTile64x5, 64, 160, 0.0, 0.97, 1.23},
-                             {kTile64x8, 64, 256, 3.16, 0.26, 1.65}};
+constexpr Cost kCosts[] = {
+    {kOne4, 16, 16, 4, false, 2.446, 0.002, 0.227, 0.572, 0.432},
+    {kOne8, 16, 16, 8, false, 2.032, 0.003, 0.012, 1.246, 0.860},
+    {kMid16x2, 16, 32, 2, true, 3.528, 0.094, 0.001, 0.483, 0.042},
+    {kMid16x4, 16, 64, 2, true, 3.456, 0.392, 0.000, 0.786, 0.212},
+    {kMid32x4, 32, 64, 2, true, 4.069, 0.190, 0.243, 0.859, 0.110},
+    {kTile32, 32, 128, 1, true, 3.033, 1.026, 0.212, 0.625, 0.017},
+    {kTile64, 64, 128, 1, true, 3.977, 1.295, 0.121, 0.893, 0.010},
+    {kTile64x5, 64, 160, 1, true, 3.926, 0.001, 0.845, 0.879, 0.043},
+    {kTile64x8, 64, 256, 1, true, 5.685, 0.022, 1.118, 0.788, 0.015}};
 
-// The one of them, and the slices of Q quads, that a product takes the least time by; joining
-// slices costs a launch and their sums written and read (5120 x 17408, M = 64, 64 x 128: 6
-// slices 20.3, 3 27.4, 12 22.5, M = 256: 3 41.2, 2 44.8, 1 54.5).
-Kernel pick_tile(int64_t M, int64_t N, int Q, int64_t* slices) {
-    Kernel kernel = kTile64x8;
+// The cheapest kernel from `first` on, and its slices of Q quads.
+Kernel cheapest(int64_t M, int64_t N, int64_t K, Kernel first, int* slices) {
+    const int Q = (int)mx4::quads(K);
+    const double weights = 0.13 * 0.53e-6 * (double)N * (double)K;
+    const double sums = 0.223 * 8e-6 * (double)M * (double)N;   // a slice's
+    Kernel kernel = first;
     double best = 0.0;
     *slices = 0;
-    for (const Shape& h : kShapes) {
-        const int64_t blocks = (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn);
-        for (int S = 1; S <= Q && S <= 64 && (S == 1 || blocks * S <= 2048); ++S) {
-            const int qs = (Q + S - 1) / S;
-            if ((Q + qs - 1) / qs != S) continue;
-            const double busy = h.fixed + h.each * (double)((blocks * S + 255) / 256);
-            const double join = S > 1 ? 1.7 + (double)S * M * N * 8 / 3.2e6 : 0.0;
-            const double time = qs * (busy > h.least ? busy : h.least) + join;
+    for (const Cost& c : kCosts) {
+        if (c.kernel < first) continue;
+        const int64_t blocks = (M + c.bm - 1) / c.bm * ((N + c.bn - 1) / c.bn);
+        const double each = c.each + c.rows * (double)(M < c.bm ? M : c.bm) / c.bm;
+        for (int qs = Q;;) {            // quads a slice: the fewest for each count of slices
+            const int S = (Q + qs - 1) / qs;
+            qs = (Q + S - 1) / S;
+            if (S > 1 && (!c.sliced || S > 12 || 2 * S > Q || blocks * S > 2048)) break;
+            const double busy = c.fixed + each * (double)((blocks * S + 255) / 256);
+            const int its = (qs + c.waves_k - 1) / c.waves_k;
+            const double work = its * (busy > c.least ? busy : c.least);
+            const double time = c.start + (work > weights ? work : weights) +
+                                (S > 1 ? 3.599 + S * sums : 0.0);
             if (*slices == 0 || time < best) {
                 best = time;
                 *slices = S;
-                kernel = h.kernel;
+                kernel = c.kernel;
             }
+            if (qs == 1) break;
+            --qs;
         }
     }
     return kernel;
 }
 
+}  // namespace
+
 // By rows of x (M), tiles of 16 weight rows (nt), pairs of a weight tile and 16 rows of x
-// (t) and groups of K (G).  us, graphs over weights in turn; MX4 x for comparison:
-//   up to 16 rows and few tiles: every wave on its own x, one tile a workgroup whose 4 or
-//     (long K) 8 waves split K (1024 x 17408 M = 1 7.4, 16-row workgroups through LDS in 12
-//     slices 8.4; 7168 x 5120 6.1, two tiles 7.5; MX4 x 6.1); above 8 rows x costs as much as
-//     one tile's weights: two tiles (7168 x 5120 M = 16 8.8, one 9.7; MX4 x 6.5).  A long K,
-//     more than 4 rows: x shared, K in slices (5120 x 17408 M = 16 15.7, 17.7 without
-//     sharing, 13.5 with MX4 x).
+// (t) and quads of K: cheapest(), but for
 //   up to 16 rows and many tiles: x shared by the waves of as many tiles as spread() says
-//     (34816 x 5120 M = 16 19.5, two tiles without sharing 27.0; MX4 x 19.5); a short K is
-//     over before sharing pays (65536 x 1024 M = 1 8.4, shared 10.0).
-//   above, as long as the pairs of tiles are few: those same workgroups of 16 rows beside
-//     each other (1024 x 1024 M = 64 3.2, 32 rows through LDS 5.0; 7168 x 5120 M = 33 12.9,
-//     32 rows 14.0; MX4 x 10.0), then 32 rows (M = 96 17.2, 32 x 128 tiles 17.7); of a long K
-//     32 rows in slices up to M = 32 (5120 x 17408 M = 17 16.4, MX4 x 15.3).
-//   else tiles by pick_tile().
+//     (34816 x 5120 M = 16 19.5 us, two tiles without sharing 27.0); a short K is over before
+//     sharing pays (65536 x 1024 M = 1 8.4, shared 10.0), above 8 rows two tiles a wave read
+//     x once for both;
+//   up to two quads: workgroups of one tile and one wave a quad overlap further than the
+//     costs say (6144 x 544 M = 33 4.1, 16 x 64 5.2, 64 x 128 5.8);
+//   more rows than 16 and many tiles: tiles.
 Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
-    const int G = (int)mx4::groups(K), Q = (int)mx4::quads(K);
+    const int Q = (int)mx4::quads(K);
     const int64_t nt = tiles(N), t = nt * tiles(M);
-    const bool many = nt >= 1024, lengthy = G >= 96;
-    const auto blocks = [&](int64_t bm, int64_t bn) {
-        return (M + bm - 1) / bm * ((N + bn - 1) / bn);
-    };
-    const auto slices = [](int64_t want, int64_t have) { return (want + have / 2) / have; };
-    Plan p{kOne4, 4, 1, 4 * Q};
-    int64_t S = 1;
-    if (M <= 16) {
-        if (many && G >= 32) {
-            p.kernel = kMid16;
-            p.wn = spread(nt);
-        } else if (M > 4 && G >= 48 && nt <= 384) {
-            p.kernel = kMid16x2;
-            S = slices(480, blocks(16, 32));
-        } else if (M <= 8 || nt <= 256) {
-            p.kernel = G >= 24 && !many ? kOne8 : kOne4;
-        } else {
-            p.kernel = G >= 48 ? kTwo8 : kTwo4;
-        }
-        if (S > Q / 2) S = Q / 2;
-    } else if (lengthy && M <= 32 && nt <= 400) {
-        p.kernel = kMid32;
-        S = slices(480, blocks(32, 64));
-        if (S > Q / 2) S = Q / 2;
-    } else if (!lengthy && !many && t <= 3200) {
-        p.kernel = t <= 400    ? kOne4
-                   : t <= 800  ? kTwo4
-                   : t <= 1200 ? kMid16x2
-                   : t <= 2000 ? kMid16
-                               : kMid32;
+    const bool many = nt >= 1024;
+    Kernel kernel;
+    int S = 1, wn = 0;
+    if (many && M <= 16) {
+        kernel = Q >= 8 ? kMid16 : M <= 8 ? kOne4 : kTwo4;
+        wn = spread(nt);
+    } else if (Q <= 2 && t <= 1400) {
+        kernel = kOne4;
     } else {
-        p.kernel = pick_tile(M, N, Q, &S);
+        kernel = cheapest(M, N, K, many ? kTile32 : kOne4, &S);
     }
-    if (S < 1) S = 1;
-    const int qs = (int)((Q + S - 1) / S);      // quads a slice
-    p.S = (Q + qs - 1) / qs;
-    p.gs = 4 * qs;
+    const int qs = (Q + S - 1) / S;             // quads a slice
+    Plan p{kernel, wn, (Q + qs - 1) / qs, 4 * qs, 0};
+    if (p.S > 1) p.workspace = (size_t)p.S * M * part_row(N) * 4;
     return p;
 }
 
-}  // namespace
-
-size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M == 0) return 0;
-    const Plan p = plan_gemm(M, N, K);
-    return p.S > 1 ? (size_t)p.S * M * part_row(N) * 4 : 0;
-}
-
-hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
-    const Plan p = plan_gemm(a.M, a.N, a.K);
+hipError_t launch_gemm(GemmArgs a, const Plan& p, void* ws, hipStream_t s) {
     a.S = p.S;
     a.gs = p.gs;
     a.part = static_cast<float*>(ws);
-    Kernel k = p.kernel;
+    int k = p.kernel;
     if (k >= kTile32 && (a.ldv >= kFarRows || a.lds >= kFarRows)) {
         k = kTwo4;
         a.S = 1;
@@ -754,11 +749,11 @@ hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s) {
     switch (k) {
         case kOne8: return launch_small<1, 8>(a, s);
         case kTwo4: return launch_small<2, 4>(a, s);
-        case kTwo8: return launch_small<2, 8>(a, s);
-        case kMid16x2: return launch_mid<1, 2, 2>(a, s);
         case kMid16:
-            return p.wn == 5 ? launch_mid<1, 5, 1>(a, s) : launch_mid<1, 4, 1>(a, s);
-        case kMid32: return launch_mid<2, 4, 1>(a, s);
+            return p.wn == 5 ? launch_mid<1, 5, 1, 1>(a, s) : launch_mid<1, 4, 1, 1>(a, s);
+        case kMid16x2: return launch_mid<1, 2, 2, 2>(a, s);
+        case kMid16x4: return launch_mid<1, 4, 2, 2>(a, s);
+        case kMid32x4: return launch_mid<2, 4, 2, 1>(a, s);
         case kTile32: return launch_tile<2, 2, 4, 2>(a, s);
         case kTile64: return launch_tile<4, 2, 4, 2>(a, s);
         case kTile64x5: return launch_tile<4, 2, 5, 2>(a, s);

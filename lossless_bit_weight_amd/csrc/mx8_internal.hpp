@@ -142,7 +142,13 @@ hipError_t launch_dequantize(const uint8_t* values, int64_t ldv, const uint8_t* 
                              int64_t lds, int64_t R, int64_t K, void* y, int y_f32, int64_t ldy,
                              hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
-size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
-hipError_t launch_gemm(GemmArgs a, void* ws, hipStream_t s);
+// Kernel and split of a product.
+struct Plan {
+    int kernel, wn;         // one of mx8_gemm.hip's; its waves beside each other, if it chooses
+    int S, gs;              // K slices, groups a slice (a multiple of 4)
+    size_t workspace;       // bytes
+};
+Plan plan_gemm(int64_t M, int64_t N, int64_t K);
+hipError_t launch_gemm(GemmArgs a, const Plan& p, void* ws, hipStream_t s);
 
 }  // namespace mx8

@@ -265,9 +265,9 @@ def test_norm_of_views():
 # ---- product -----------------------------------------------------------------------------
 
 # few rows, tiles of 16, 32, 64, 128 rows and one past them; ragged N and K; a long K; then
-# every kernel by its rule: waves that split K over one tile (4, 8 of them) and two, 16 rows
-# shared by 2 x 2 waves and by 4 and 5, 32 rows, tiles of
-# 32 x 128, 64 x 128 and 64 x 160 (whole and in slices) and 64 x 256
+# every kernel by its rule, whole and in slices: waves that split K over one tile (4, 8 of
+# them) and two, 16 rows shared by 4 and 5 waves, by 2 x 2 and 4 x 2, 32 rows by 4 x 2, tiles
+# of 32 x 128, 64 x 128, 64 x 160 and 64 x 256
 GEMM_SHAPES = [(16, 5000, 544), (16, 7000, 6176), (13, 512, 6176), (129, 3000, 160),
                (5, 16400, 4128), (16, 23000, 4096), (160, 5120, 640), (256, 5000, 12320),
                (2050, 3333, 288), (60, 16500, 160), (1, 16, 32), (1, 7168, 5120), (2, 48, 160), (3, 1000, 2080), (16, 512, 544),
@@ -275,7 +275,10 @@ GEMM_SHAPES = [(16, 5000, 544), (16, 7000, 6176), (13, 512, 6176), (129, 3000, 1
                (65, 1040, 512), (128, 2048, 2560), (129, 300, 4128), (200, 5120, 640),
                (300, 96, 65536), (513, 1100, 288), (1024, 4096, 1024), (1, 20000, 96),
                (5, 34816, 256), (20, 17000, 544), (50, 20500, 320), (2000, 3000, 160),
-               (64, 40900, 544), (127, 20001, 1056), (250, 1601, 12320)]
+               (64, 40900, 544), (127, 20001, 1056), (250, 1601, 12320),
+               (17, 2414, 1120), (18, 71, 8992), (19, 4295, 1120), (19, 423, 9792), (17, 10090, 1568),
+               (899, 64, 16768), (20, 64, 2272), (322, 9169, 544), (176, 11193, 1056),
+               (1664, 129, 9056), (1665, 3912, 544), (70, 11072, 8800)]
 
 
 @pytest.mark.parametrize("out", ["bf16", "f32"])
