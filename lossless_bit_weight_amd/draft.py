@@ -86,7 +86,8 @@ def _small(t: torch.Tensor, what: str, shape: tuple, dtypes: tuple, dev: int) ->
             or not t.is_contiguous():
         _same(dev, _gpu(t, what))
         if t.dtype not in dtypes:
-            raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
+            raise TypeError("%s must be %s, got %s"
+                            % (what, " or ".join(map(str, dtypes)), t.dtype))
         raise ValueError("%s must be contiguous %s, got %s" % (what, shape, tuple(t.shape)))
     return t.data_ptr()
 

@@ -98,7 +98,8 @@ def test_route_of_the_most_tokens():
     T, l = 1 << 24, _randn(P, 4, dtype=torch.float32)
     e, s = mx4.mx4_route(l, 1)
     ee, ss = mx4.mx4_route(l.repeat(T // P, 1), 1)
-    assert bool((ee.view(-1, P) == e.view(1, P)).all()) and bool((ss.view(-1, P) == s.view(1, P)).all())
+    assert bool((ee.view(-1, P) == e.view(1, P)).all())
+    assert bool((ss.view(-1, P) == s.view(1, P)).all())
 
 
 @pytest.mark.parametrize("probs", [False, True])
