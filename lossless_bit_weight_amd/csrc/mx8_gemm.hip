@@ -714,6 +714,9 @@ Kernel cheapest(int64_t M, int64_t N, int64_t K, Kernel first, int* slices) {
 //     (34816 x 5120 M = 16 19.5 us, two tiles without sharing 27.0); a short K is over before
 //     sharing pays (65536 x 1024 M = 1 8.4, shared 10.0), above 8 rows two tiles a wave read
 //     x once for both;
+//   up to four rows: one tile a workgroup, by eight waves from six quads on (beyond the
+//     last-level cache: 7168 x 5120 M = 1 5.8, 16 x 32 6.1; 5120 x 17408 M = 1 13.8 and 15.1,
+//     M = 4 14.8 and 15.2; 1024 x 4096 4.0, four waves 4.4);
 //   up to two quads: workgroups of one tile and one wave a quad overlap further than the
 //     costs say (6144 x 544 M = 33 4.1, 16 x 64 5.2, 64 x 128 5.8);
 //   more rows than 16 and many tiles: tiles.
@@ -726,6 +729,8 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
     if (many && M <= 16) {
         kernel = Q >= 8 ? kMid16 : M <= 8 ? kOne4 : kTwo4;
         wn = spread(nt);
+    } else if (M <= 4) {
+        kernel = Q >= 6 ? kOne8 : kOne4;
     } else if (Q <= 2 && t <= 1400) {
         kernel = kOne4;
     } else {
