@@ -56,10 +56,12 @@ size_t mx8_scale_row_bytes(int64_t K) {
 
 int mx8_quantize(const void* x, int x_type, int64_t R, int64_t K, int64_t ldx, void* values,
                  int64_t ldv, void* scales, int64_t lds, void* stream) {
+    const bool fine = (x_type & MX8_FINE_STEPS) != 0;
+    x_type &= ~MX8_FINE_STEPS;
     if (int rc = codec(x, x_type, R, K, ldx, values, ldv, scales, lds)) return rc;
     if (R == 0) return W12_OK;
-    return status_of(mx8::launch_quantize(x, x_type == W12_OUT_F32, R, K, ldx,
-                                          static_cast<uint8_t*>(values), ldv,
+    return status_of(mx8::launch_quantize(x, x_type == W12_OUT_F32, mx8::quarters_below(fine), R, K,
+                                          ldx, static_cast<uint8_t*>(values), ldv,
                                           static_cast<uint8_t*>(scales), lds,
                                           static_cast<hipStream_t>(stream)));
 }
@@ -81,7 +83,7 @@ int mx8_rms_norm(const void* x, int x_type, int64_t ldx, const void* residual, v
     if (M < 0 || M > kMaxM) return W12_ERR_SHAPE;
     if (int rc = check_container(1, M, K)) return rc;
     if (K > MX8_MAX_NORM_K) return W12_ERR_UNSUPPORTED;
-    const bool out8 = y_type == MX8_OUT;
+    const bool fine = y_type == (MX8_OUT | MX8_FINE_STEPS), out8 = fine || y_type == MX8_OUT;
     if (type_bytes(x_type) == 0 || type_bytes(w_type) == 0 || (!out8 && type_bytes(y_type) == 0))
         return W12_ERR_DTYPE;
     if (residual != nullptr && type_bytes(res_type) == 0) return W12_ERR_DTYPE;
@@ -117,7 +119,7 @@ int mx8_rms_norm(const void* x, int x_type, int64_t ldx, const void* residual, v
     a.x_f32 = x_type == W12_OUT_F32;
     a.res_f32 = res_type == W12_OUT_F32;
     a.w_f32 = w_type == W12_OUT_F32;
-    a.y_type = y_type;
+    a.y_type = fine ? 3 : y_type;
     return status_of(mx8::launch_norm(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -27,8 +27,9 @@ __device__ __forceinline__ int64_t wave_index() {
 }
 
 template <bool F32>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restrict__ x, int64_t R,
-                                                            int K, int Q, int64_t ldx,
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restrict__ x,
+                                                            float quarters, int64_t R, int K,
+                                                            int Q, int64_t ldx,
                                                             uint8_t* __restrict__ values,
                                                             int64_t ldv,
                                                             uint8_t* __restrict__ scales,
@@ -41,7 +42,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restri
     Eight v;
     v.load<F32>(x, r * ldx + (in ? k : 0));
     uint32_t e;
-    const u32x2_t d = v.encode(e);
+    const u32x2_t d = v.encode(e, quarters);
     if (in) *reinterpret_cast<u32x2_t*>(values + r * ldv + k) = d;
     if ((lane & 3) == 0) scales[r * lds + scale_place(k)] = (uint8_t)(in ? e : 127u);
 }
@@ -78,17 +79,17 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
 
 }  // namespace
 
-hipError_t launch_quantize(const void* x, int x_f32, int64_t R, int64_t K, int64_t ldx,
-                           uint8_t* values, int64_t ldv, uint8_t* scales, int64_t lds,
-                           hipStream_t s) {
+hipError_t launch_quantize(const void* x, int x_f32, float quarters, int64_t R, int64_t K,
+                           int64_t ldx, uint8_t* values, int64_t ldv, uint8_t* scales,
+                           int64_t lds, hipStream_t s) {
     const int Q = (int)mx4::quads(K);
     const dim3 grid = grid_of(R * Q);
     if (x_f32)
-        hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(kThreads), 0, s, x, R, (int)K, Q, ldx,
-                           values, ldv, scales, lds);
+        hipLaunchKernelGGL(quantize_kernel<true>, grid, dim3(kThreads), 0, s, x, quarters, R,
+                           (int)K, Q, ldx, values, ldv, scales, lds);
     else
-        hipLaunchKernelGGL(quantize_kernel<false>, grid, dim3(kThreads), 0, s, x, R, (int)K, Q, ldx,
-                           values, ldv, scales, lds);
+        hipLaunchKernelGGL(quantize_kernel<false>, grid, dim3(kThreads), 0, s, x, quarters, R,
+                           (int)K, Q, ldx, values, ldv, scales, lds);
     return hipGetLastError();
 }
 

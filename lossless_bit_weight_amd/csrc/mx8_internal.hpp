@@ -70,10 +70,10 @@ struct Eight {
     }
     // As MX8: the four lanes of a quad hold one block between them.  The largest
     // magnitude lies in [256, 512) * 2^(e - 127); multiplying by the power of two is
-    // exact (but for what rounds to zero anyway).  Below 4, where E4M3 goes finer,
-    // values are rounded to multiples of 1/4 first (the header says why); what is above
-    // 448 is brought there, as the conversion would make a NaN of it.
-    __device__ __forceinline__ u32x2_t encode(uint32_t& e) const {
+    // exact (but for what rounds to zero anyway).  Below `quarters` (4, where E4M3 goes
+    // finer; 0 for MX8_FINE_STEPS) values are rounded to multiples of 1/4 first (the header
+    // says why); what is above 448 is brought there, as the conversion would make a NaN of it.
+    __device__ __forceinline__ u32x2_t encode(uint32_t& e, float quarters) const {
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -87,8 +87,8 @@ struct Eight {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float v = f[j] * s;
-            t[j] = __builtin_fabsf(v) < 4.f ? __builtin_rintf(v * 4.f) * 0.25f
-                                            : __builtin_amdgcn_fmed3f(v, -448.f, 448.f);
+            t[j] = __builtin_fabsf(v) < quarters ? __builtin_rintf(v * 4.f) * 0.25f
+                                                 : __builtin_amdgcn_fmed3f(v, -448.f, 448.f);
         }
         u32x2_t v;
 #pragma unroll
@@ -102,6 +102,9 @@ struct Eight {
         return v;
     }
 };
+
+// Eight::encode's `quarters`, in units of the block.
+__host__ __device__ constexpr float quarters_below(bool fine) { return fine ? 0.f : 4.f; }
 
 struct NormArgs {
     const void* x;
@@ -117,7 +120,8 @@ struct NormArgs {
     int64_t ldy;
     uint8_t* ys;
     int64_t lds;
-    int x_f32, res_f32, w_f32, y_type;
+    int x_f32, res_f32, w_f32;
+    int y_type;             // 0 BF16, 1 fp32, 2 MX8, 3 MX8 in fine steps
 };
 
 struct GemmArgs {
@@ -135,9 +139,9 @@ struct GemmArgs {
     float* part;            // S > 1: partial sums [S][M][N rounded up to 4]
 };
 
-hipError_t launch_quantize(const void* x, int x_f32, int64_t R, int64_t K, int64_t ldx,
-                           uint8_t* values, int64_t ldv, uint8_t* scales, int64_t lds,
-                           hipStream_t s);
+hipError_t launch_quantize(const void* x, int x_f32, float quarters, int64_t R, int64_t K,
+                           int64_t ldx, uint8_t* values, int64_t ldv, uint8_t* scales,
+                           int64_t lds, hipStream_t s);
 hipError_t launch_dequantize(const uint8_t* values, int64_t ldv, const uint8_t* scales,
                              int64_t lds, int64_t R, int64_t K, void* y, int y_f32, int64_t ldy,
                              hipStream_t s);

@@ -114,12 +114,12 @@ __global__ __launch_bounds__(T != 0 ? 256 : kMost) void norm_kernel(NormArgs a) 
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const double y = (double)v[i].f[j] * r * (double)wi.f[j];
-            v[i].f[j] = a.y_type == 2 ? to_odd(y) : (float)y;
+            v[i].f[j] = a.y_type >= 2 ? to_odd(y) : (float)y;
         }
         const bool in = live && k < a.K;
-        if (a.y_type == 2) {
+        if (a.y_type >= 2) {
             uint32_t e;
-            const u32x2_t d = v[i].encode(e);
+            const u32x2_t d = v[i].encode(e, quarters_below(a.y_type == 3));
             uint8_t* y = static_cast<uint8_t*>(a.y);
             if (in) *reinterpret_cast<u32x2_t*>(y + row * a.ldy + k) = d;
             if ((t & 3) == 0 && live && k < a.K)
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(T != 0 ? 256 : kMost) void norm_kernel(NormArgs a) 
         }
     }
     // the scales past K
-    if (a.y_type == 2 && live) {
+    if (a.y_type >= 2 && live) {
         const int first = a.K / 32, n = (int)mx4::quads(a.K) * 16 - first;
         for (int i = t; i < n; i += TPR)
             a.ys[row * a.lds + scale_place((first + i) * 32)] = 127;

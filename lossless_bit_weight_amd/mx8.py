@@ -1,6 +1,8 @@
 """Python binding of libw12.so's MX8 calls (include/mx8.h): activations in 8-bit
 floating point under a shared scale per 32 values, the residual addition and
-norm that writes them, and their product with MX4 weights.
+norm that writes them, and their product with MX4 weights.  The bytes are
+E4M3's; by default values are multiples of 1/4 of their block's unit, with
+fine=True they take all of E4M3's steps (include/mx8.h says what either loses).
 
 As mx4.py this marshals arguments only; outputs and workspaces come from
 torch's allocator on the current stream of the tensors' device, one per call.
@@ -24,6 +26,7 @@ from .w12 import STATUS, W12Error
 BLOCK = 32
 MAX_NORM_K = 32768
 OUT_MX8 = 2
+FINE_STEPS = 16
 VALUES = torch.float8_e4m3fn        # as an output type: a whole MX8Tensor
 
 _u8 = torch.uint8
@@ -182,13 +185,15 @@ def _target(out, R: int, K: int, dev: int, like: torch.Tensor) -> tuple:
     return out, parts
 
 
-def mx8_quantize(x: torch.Tensor, out: MX8Tensor | None = None) -> MX8Tensor:
-    """x [R, K] (BF16 or fp32, unit column stride) as MX8."""
+def mx8_quantize(x: torch.Tensor, out: MX8Tensor | None = None,
+                 fine: bool = False) -> MX8Tensor:
+    """x [R, K] (BF16 or fp32, unit column stride) as MX8, in all of E4M3's steps if
+    `fine`."""
     dev = _gpu(x, "x")
     if _away(dev):
         with torch.cuda.device(dev):
-            return mx8_quantize(x, out)
-    xt = _type_of(x.dtype)
+            return mx8_quantize(x, out, fine)
+    xt = _type_of(x.dtype) | (FINE_STEPS if fine else 0)
     R, K, ld = _rows(x, "x")
     out, (_, _, vp, ldv, sp, lds, _) = _target(out, R, K, dev, x)
     _check(lib().mx8_quantize(x.data_ptr(), xt, R, K, ld, vp, ldv, sp, lds, _raw_stream(dev)),
@@ -211,15 +216,16 @@ def mx8_dequantize(q: MX8Tensor, out_dtype: torch.dtype = torch.bfloat16,
 
 def mx8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
                  residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
-                 out_dtype: torch.dtype = VALUES, out=None):
+                 out_dtype: torch.dtype = VALUES, out=None, fine: bool = False):
     """s / sqrt(mean(s^2) + eps) * weight over the rows of s = x + residual
-    (rounded to the residual's type) or s = x: an MX8Tensor, or BF16 or fp32 as
-    out_dtype (or `out`) says.  With a residual: (that, s); s goes to
-    residual_out, which may be the residual itself, or to a new tensor."""
+    (rounded to the residual's type) or s = x: an MX8Tensor (in all of E4M3's
+    steps if `fine`), or BF16 or fp32 as out_dtype (or `out`) says.  With a
+    residual: (that, s); s goes to residual_out, which may be the residual itself,
+    or to a new tensor."""
     dev = _gpu(x, "x")
     if _away(dev):
         with torch.cuda.device(dev):
-            return mx8_rms_norm(x, weight, eps, residual, residual_out, out_dtype, out)
+            return mx8_rms_norm(x, weight, eps, residual, residual_out, out_dtype, out, fine)
     M, K, ldx = _rows(x, "x")
     if weight.dim() != 1 or weight.shape[0] != K or (K > 1 and weight.stride(0) != 1):
         raise ValueError("weight must be %d contiguous values" % K)
@@ -244,7 +250,9 @@ def mx8_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         raise ValueError("residual_out without a residual")
     if isinstance(out, MX8Tensor) or (out is None and out_dtype is VALUES):
         out, (_, _, yp, ldy, sp, lds, _) = _target(out, M, K, dev, x)
-        yt = OUT_MX8
+        yt = OUT_MX8 | FINE_STEPS if fine else OUT_MX8
+    elif fine:
+        raise ValueError("fine steps are those of an MX8 output")
     else:
         out, ldy, yt = _output(out, M, K, out_dtype, dev, x)
         yp, sp, lds = out.data_ptr(), None, 0
