@@ -1,9 +1,10 @@
-// mx8_api.hip -- the C ABI declared in include/mx8.h: host-side argument checks
-// and launches on the caller's stream.  Nothing here allocates, synchronises or
+// mx8_api.hip -- the C ABI declared in include/mx8.h and include/mx8_plan.h: host-side
+// argument checks and launches on the caller's stream.  Nothing here allocates, synchronises or
 // keeps state.
 #include <stdint.h>
 
 #include "../../include/mx8.h"
+#include "../../include/mx8_plan.h"
 #include "mx4_checks.hpp"
 #include "mx8_internal.hpp"
 
@@ -129,6 +130,14 @@ int mx8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
     if (int rc = check_gemm_shape(M, N, K)) return rc;
     if (M > 0) *bytes = mx8::plan_gemm(M, N, K).workspace;
     return W12_OK;
+}
+
+const char* mx8_gemm_plan(int64_t M, int64_t N, int64_t K, int* slices) {
+    if (slices != nullptr) *slices = 0;
+    if (M < 1 || check_gemm_shape(M, N, K) != W12_OK) return nullptr;
+    const mx8::Plan plan = mx8::plan_gemm(M, N, K);
+    if (slices != nullptr) *slices = plan.S;
+    return mx8::kernel_name(plan);
 }
 
 int mx8_gemm(const void* x_values, int64_t ldv, const void* x_scales, int64_t lds, int64_t M,

@@ -742,6 +742,22 @@ Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
     return p;
 }
 
+const char* kernel_name(const Plan& p) {
+    switch (p.kernel) {
+        case kOne8: return "small_kernel<1, 8>";
+        case kTwo4: return "small_kernel<2, 4>";
+        case kMid16: return p.wn == 5 ? "mid_kernel<1, 5, 1, 1>" : "mid_kernel<1, 4, 1, 1>";
+        case kMid16x2: return "mid_kernel<1, 2, 2, 2>";
+        case kMid16x4: return "mid_kernel<1, 4, 2, 2>";
+        case kMid32x4: return "mid_kernel<2, 4, 2, 1>";
+        case kTile32: return "tile_kernel<2, 2, 4, 2>";
+        case kTile64: return "tile_kernel<4, 2, 4, 2>";
+        case kTile64x5: return "tile_kernel<4, 2, 5, 2>";
+        case kTile64x8: return "tile_kernel<4, 4, 4, 1>";
+        default: return "small_kernel<1, 4>";
+    }
+}
+
 hipError_t launch_gemm(GemmArgs a, const Plan& p, void* ws, hipStream_t s) {
     a.S = p.S;
     a.gs = p.gs;

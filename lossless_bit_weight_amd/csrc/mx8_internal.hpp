@@ -153,6 +153,7 @@ struct Plan {
     size_t workspace;       // bytes
 };
 Plan plan_gemm(int64_t M, int64_t N, int64_t K);
+const char* kernel_name(const Plan& p);     // with its template arguments
 hipError_t launch_gemm(GemmArgs a, const Plan& p, void* ws, hipStream_t s);
 
 }  // namespace mx8

@@ -59,6 +59,8 @@ def lib() -> ctypes.CDLL:
                                p, i32, i64, p, i64, p]
     L.mx8_gemm_workspace_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
     L.mx8_gemm.argtypes = [p, i64, p, i64, i64, p, p, i64, i64, p, i64, i32, p, sz, p]
+    L.mx8_gemm_plan.argtypes = [i64, i64, i64, ctypes.POINTER(ctypes.c_int)]
+    L.mx8_gemm_plan.restype = ctypes.c_char_p
     for name in ("mx8_quantize", "mx8_dequantize", "mx8_rms_norm", "mx8_gemm_workspace_bytes",
                  "mx8_gemm"):
         getattr(L, name).restype = i32
@@ -80,6 +82,16 @@ def mx8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
     _check(lib().mx8_gemm_workspace_bytes(int(M), int(N), int(K), ctypes.byref(n)),
            "mx8_gemm_workspace_bytes")
     return int(n.value)
+
+
+def mx8_gemm_plan(M: int, N: int, K: int) -> tuple:
+    """(name, slices of K) of the kernel that mx8_gemm of this shape takes
+    (include/mx8_plan.h)."""
+    n = ctypes.c_int(0)
+    name = lib().mx8_gemm_plan(int(M), int(N), int(K), ctypes.byref(n))
+    if name is None:
+        raise MX8Error(-2, "mx8_gemm_plan")
+    return name.decode(), n.value
 
 
 def _check(status: int, what: str) -> None:
