@@ -1,6 +1,9 @@
 """Shapes that take every kernel of the product of MX8 with MX4, whole and in slices of
-K, most of them with ragged rows, columns and last groups."""
+K, most of them with ragged rows, columns and last groups; and operands at the edge of
+what the matrix units add without loss."""
 from __future__ import annotations
+
+import numpy as np
 
 # (kernel, in slices): shapes
 KERNEL_SHAPES = {
@@ -27,3 +30,37 @@ KERNEL_SHAPES = {
     ("tile_kernel<4, 4, 4, 1>", True): [(66, 11052, 9568)],
 }
 SHAPES = [s for shapes in KERNEL_SHAPES.values() for s in shapes]
+
+
+def edges(M: int, N: int, K: int) -> tuple:
+    """(x [M, K], w [N, K]) whose products lie as far apart as MX8 and MX4 let them under
+    scales of 1: in each block of x one or two of +-448, the second of the other sign in the
+    same eight, among multiples of 1/4; in each of w +-6 among +-0.5 and others.  Every sum
+    of products is a multiple of 1/8 below 2^21, which fp32 holds."""
+    rng = np.random.default_rng(M + N + K)
+    n = K // 32
+    x = rng.choice([0.25, -0.25, 0.75, -0.25, 0.5, 1.75, 0.0], (M, n, 32))
+    at, sign = rng.integers(0, 32, (M, n)), rng.choice([-448.0, 448.0], (M, n))
+    np.put_along_axis(x, at[..., None], sign[..., None], 2)
+    beside = at ^ rng.integers(1, 8, (M, n))
+    two = rng.random((M, n)) < 0.5
+    np.put_along_axis(x, np.where(two, beside, at)[..., None],
+                      np.where(two, -sign, sign)[..., None], 2)
+    w = rng.choice([0.5, -0.5, 0.5, 1.5, -6.0, 6.0, 0.0], (N, n, 32))
+    np.put_along_axis(w, rng.integers(0, 32, (N, n))[..., None],
+                      rng.choice([-6.0, 6.0], (N, n))[..., None], 2)
+    return x.reshape(M, K), w.reshape(N, K)
+
+
+def summed_in_eights(x: np.ndarray, w: np.ndarray, bits: int) -> np.ndarray:
+    """x w^T where each eight neighbours along K lose what lies more than `bits` below the
+    exponent (of the operands, added) of their largest product."""
+    y = np.zeros((len(x), len(w)))
+    with np.errstate(divide="ignore"):
+        ex, ew = (np.floor(np.log2(np.abs(v))) for v in (x, w))
+    for k in range(0, x.shape[1], 8):
+        p = x[:, None, k:k + 8] * w[None, :, k:k + 8]
+        e = (ex[:, None, k:k + 8] + ew[None, :, k:k + 8]).max(-1, keepdims=True)
+        step = np.exp2(np.where(np.isfinite(e), e, 0.0) - bits)
+        y += (np.trunc(p / step) * step).sum(-1)
+    return y
