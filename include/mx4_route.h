@@ -41,10 +41,15 @@ enum {
  * an exponential below exp(-707) counts as 0.
  * An expert whose logit or whose bias is -inf is in no S(t) and adds nothing to
  * its group's value; a token with fewer than top_k others gets -1 and share 0
- * in the places left.  A NaN logit ranks above all others and makes every share
- * of its token NaN that it goes into: its own, and under softmax or
- * renormalisation all of them.  A logit of +inf makes its token's softmax
- * shares NaN.  A NaN bias ranks above all other ranks.
+ * in the places left.
+ * A NaN rank, a logit's or a bias's, is above all others, a group's value NaN
+ * that it goes into (or, of two terms, a NaN score) above all other groups',
+ * and ties go to the lowest as elsewhere.  A NaN logit makes its own share NaN,
+ * and under softmax or renormalisation all of its token's.  Under softmax a
+ * token with a logit of NaN or +inf has no scores: all its shares are NaN, and
+ * where scores decide all its ranks (with a bias) or all its groups' values (of
+ * two terms) are alike, so that the lowest experts or groups are taken that have
+ * or hold a logit and a bias above -inf.
  *   logits  : device [T, E], BF16 bits or fp32 as logits_type (a w12_out_t)
  *             says, row stride ldl >= E elements, aligned to its type.
  *   bias    : device fp32 [E], or NULL.
