@@ -152,6 +152,8 @@ class MX8Tensor:
     def parts(self, what: str) -> tuple:
         """(R, K, values pointer, stride, scales pointer, stride, device)."""
         if self._parts is not None:
+            if self._parts[-1] < 0:
+                raise ValueError("%s must be on the GPU" % what)
             return self._parts
         v, s = self._values, self._scales
         dev = _gpu(v, what)
