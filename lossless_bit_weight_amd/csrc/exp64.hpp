@@ -19,15 +19,7 @@ __device__ __forceinline__ double exp2_fraction(double f) {
     return __builtin_fma(p, f, 1.0000000000000135);
 }
 
-// 2^t, t = n + f with n the nearest whole number.  Below -1100 it is 0, above 1100
-// infinite; a NaN counts as -1100.
-__device__ __forceinline__ double exp2_64(double t) {
-    t = __builtin_fmin(__builtin_fmax(t, -1100.0), 1100.0);
-    const double n = __builtin_rint(t);
-    return __builtin_ldexp(exp2_fraction(t - n), (int)n);
-}
-
-// 2^(d rate) for |d rate| up to 1021 in fewer instructions, none of them a conversion.
+// 2^(d rate) for |d rate| up to 1021, without an instruction that converts.
 __device__ __forceinline__ double exp2_64_within(double d, double rate) {
     // the nearest whole number in the last bits of the sum with 3 * 2^51
     const double shifted = __builtin_fma(d, rate, 0x1.8p52);
