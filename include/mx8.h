@@ -107,8 +107,9 @@ int mx8_dequantize(const void *values, int64_t ldv, const void *scales, int64_t 
  *                   aligned.
  *   y             : device output [M, K], row stride ldy elements: BF16 bits,
  *                   fp32, or (y_type MX8_OUT, or MX8_OUT | MX8_FINE_STEPS) E4M3
- *                   bytes, with their scales in y_scales, row stride lds bytes.  Apart from the inputs,
- *                   except that y may be x (of the same type and stride).
+ *                   bytes, with their scales in y_scales, row stride lds bytes.
+ *                   Apart from the inputs, except that y may be x (of the same type
+ *                   and stride).
  * K % 32 == 0, K <= MX8_MAX_NORM_K.
  * Errors: W12_ERR_NULL, W12_ERR_SHAPE, W12_ERR_DTYPE, W12_ERR_ALIGN,
  *         W12_ERR_UNSUPPORTED (K over its limit), W12_ERR_HIP.

@@ -751,10 +751,12 @@ struct Plan {
 
 // Waves beside each other that spread nt tiles best over 256 CUs: the CU with the
 // most of them decides; up to 16 rows a CU with one workgroup, whose barriers nothing
-// fills, counts a fifth more.  us (tiles of that CU): gate+up, 2176 tiles, M = 16,
-// 5 waves 24.4 (2 x 5), 9 25.4 (9), 7 26.8 (2 x 7), 12 28.6 (12), 4 27.6 (3 x 4);
-// M = 32, 9 waves 30.1, 5 31.3, 12 32.0, 7 35.0, 4 42.4; 1792 tiles, M = 16, 4 waves
-// 15.5 (2 x 4), 7 17.6 (7).  Of equals the most waves, which share x.
+// fills, counts a fifth more.  us over 560 MB of weights in turn (tiles of that CU):
+// gate+up, 2176 tiles, M = 16, 9 waves 21.6 (9), 12 22 (12), 5 23.0 (2 x 5), 4 25.3
+// (3 x 4), 7 26.1 (2 x 7); M = 32, 9 waves 26.0, 12 26.6, 5 28.7, 7 34, 4 37.8; 1792
+// tiles, M = 16, 7 waves 15.1 (7), 4 15.2 (2 x 4), 9 16.6, 5 17.1.  (The fifth is of
+// kernels with slower loads; it takes 5 waves for 9 there now, 6% more.)  Of equals the
+// most waves, which share x.
 int spread(int64_t nt, bool few_rows) {
     static const int kWaves[] = {12, 9, 7, 5, 4};
     int best = 4;
@@ -770,38 +772,42 @@ int spread(int64_t nt, bool few_rows) {
     return best;
 }
 
-// The figures below were taken with flat loads in the tile and 16-row kernels; as global
-// ones they take 2 to 17% less on either side of these rules.
 // By rows of x (M), tiles of 16 weight rows (nt) and groups of K (G).  Measured on
-// QKV (nt = 448, G = 40), gate+up (2176, 40) and down (320, 136), us:
-//   up to 16 rows, BF16 x: every wave on its own x for few tiles (QKV M = 1 6.9 against
-//     7.8 through LDS, M = 16 9.8 against 11.1); shared through LDS for many tiles
-//     (gate+up M = 1 18.5 against 22.1, M = 16 23.6 against 29.2) or a long K (down
-//     M = 1 14.3 against 15.6, M = 16, K in six slices, 17.5 against 23.5).  MX4 x
-//     is a quarter of the bytes: shared or not within 3%.  A long K for so few tiles
-//     that they leave CUs idle is cut (M = 1, K = 17408, N = 1024 8.9, uncut 11.5; MX4 x
-//     8.0 and 11.4).
+// QKV (nt = 448, G = 40), gate+up (2176, 40) and down (320, 136), us in graphs over
+// weights in turn, 155 MB of them (QKV and smaller: they stay in the last-level cache) or
+// 560 MB and more; where these lie in memory moves a figure by up to a tenth:
+//   up to 16 rows, BF16 x: every wave on its own x for few tiles (QKV M = 16 9.3 against
+//     10.6 through LDS, M = 1 6.7 to 7.8 against 7.3); shared through LDS for many tiles
+//     (gate+up M = 1 18.4 against 23.5, M = 16 22 against 34) or a long K (down M = 1
+//     13.9 against 15.5, M = 16, K in six slices, 17.0 against 23.2).  MX4 x is a quarter
+//     of the bytes: shared or not within 7% (gate+up M = 16 20.9 and 19.5).  A long K for
+//     so few tiles that they leave CUs idle is cut (M = 1, K = 17408, N = 1024 8.6, uncut
+//     11.0; MX4 x 7.6, uncut 8.3).
 //   above and few tiles: 16 (MX4 x: 16, 32) rows a workgroup, whose weights the row
-//     blocks beside it find in L2, up to the grids that those fill (QKV M = 64 16.9,
-//     M = 128 21.5; 64 x 128 tiles in four slices 21.2 and 24.9.  N = K = 1024, M = 512
-//     6.0, tiles 9.2.  MX4 x: 16 rows at M = 48 10.4, 32 rows 11.1, at M = 128 17.6 and
-//     14.4; N = 896 on K = 5120, M = 128, 6.3 and 8.7); a long K in slices (down M = 33 24.5,
-//     MX4 x, M = 17, six slices, 16.3; 64 rows, five slices, 20.7).
+//     blocks beside it find in L2, up to the grids that those fill (QKV M = 64 13.3,
+//     M = 128 18.9; 32 x 256 tiles in three slices 16.5 and 21.8.  N = K = 1024, M = 512
+//     5.5, tiles 7.3.  MX4 x: 16 rows at M = 48 7.9, 32 rows 7.4, at M = 128 12.7 and
+//     10.3; N = 896 on K = 5120, M = 128, 4.7 and 6.8); a long K in slices (down M = 33
+//     24.0, uncut 36; MX4 x, M = 17, six slices, 15.5, uncut 23.8; 64 rows at M = 128 in
+//     four 27.6, 64 x 128 tiles in eight 30.5).
 //   17 to 32 and many tiles: 32 rows, waves as spread() says (MX4 x: four), unless BF16
-//     tiles of 32 x 256 nearly fill the GPU (gate+up M = 32, 136 of them, 37.2, by waves
-//     29.8; N = 65536 on K = 2048, 256 of them, 20.0 and 26.8).
+//     tiles of 32 x 256 nearly fill the GPU (gate+up M = 32, 136 of them, 27.1, by waves
+//     26.0; N = 65536 on K = 2048, 256 of them, 16.3 and 26.9).
 //   33 to 64 and many tiles: the tiles below, BF16 x 64 x 256 from about one a CU on, else
-//     32 x 256 (K = 5120, M = 64: N = 65536 53.5, 32 rows by two tiles a wave 72.1; N = 50000
-//     51.4 and 65.0, N = 34816 42.3 and 41.7, N = 20480 31.4 and 35.7).
-//   above: 128 x 256 if that gives 440 workgroups (QKV M = 2048 115, 64 x 256 125.5);
-//     else, BF16 x, 64 x 256 if that gives 440 (QKV M = 1024 64.9, 128 x 256 75.5) or
-//     nearly one a CU (QKV M = 512 39.2, 128 x 256 51.7), then 32 x 256 (QKV M = 256
-//     29.2, 64 x 256 in two slices 32.4; gate+up M = 128 59.4, 64 x 256 on 272
-//     workgroups 64.1); MX4 x 128 x 128, then 64 x 128 (QKV M = 512 21.8, 128 x 256
-//     30.2).  Slices cost about 4 us to write, wait for and join: for a long K (down
-//     M = 256, MX4 x, four slices of 64 x 128 37.2, one 60), and BF16 x on K = 4096 and more
-//     where one slice leaves CUs idle (O M = 192 22.9 with three, 28.1 with one; K = 2560
-//     18.9 and 16.7).
+//     32 x 256 (K = 5120, M = 64: N = 65536 51 and 54.6, N = 34816 39 and 40).
+//   above: 128 x 256 if that gives 440 workgroups (QKV M = 2048 112, 64 x 256 126);
+//     else, BF16 x, 64 x 256 if that gives 440 (QKV M = 1024 64, 128 x 256 72) or
+//     nearly one a CU (QKV M = 512 39.2, 128 x 256 70), then 32 x 256 (QKV M = 256
+//     25.1, 64 x 256 in two slices 31; gate+up M = 128 58, 64 x 256 on 272
+//     workgroups 64); MX4 x 128 x 128, then 64 x 128 (QKV M = 512 17.2, 128 x 128 19.3,
+//     128 x 256 25.5).  Slices cost about 4 us to write, wait for and join: for a long K
+//     (down M = 256, MX4 x, four slices of 64 x 128 37.7, one 52), and BF16 x on K = 4096 and
+//     more where one slice leaves CUs idle (N = 5120, M = 192: K = 5120 22.0 with three, 24.4
+//     with one; K = 4096 20.3 and 19.9; K = 2560 18.3 and 13.8).
+// The borders were set when these kernels' loads were slower, and take the slower side here
+// and there: 32 x 256 tiles just below one 64 x 256 a CU (K = 5120, M = 64, N = 50000 50,
+// 64 x 256 43.5), three slices with many tiles (N = 20480 there 31, uncut 26), MX4 x at
+// M = 48 above.
 Plan plan_gemm(int64_t M, int64_t N, int64_t K, bool xm) {
     const int G = (int)groups(K), Q = (int)quads(K);
     const int64_t nt = tiles(N);

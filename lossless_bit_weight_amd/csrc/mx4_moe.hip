@@ -807,11 +807,11 @@ size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Each token by itself, weights that several of them chose read again: two launches
 // instead of four, at the cost of the repeated bytes.  Whole layer, us, so / by slots,
-// and the bytes expected: 2 tokens, 2 of 8 experts, H = 5120, I = 1280 18.7 / 23.7 (5 MB);
-// 4 tokens, 8 of 127, H = 2080, I = 736 31.3 / 31.6 (7 MB); 3 tokens, 6 of 64, H = 4096,
-// I = 1408 42.0 / 46.8 (16 MB); 16 tokens, 4 of 64, H = 1024, I = 512 26.4 / 23.7 (25 MB);
-// 4 tokens, 6 of 64, H = 5120, I = 1280 58.7 / 55.1 (35 MB); 32 tokens, 1 of 22,
-// H = 800, I = 320 18.4 / 18.8 (9 MB), 64, 1 of 64, 31.1 / 21.8 (13 MB).
+// and the bytes expected: 2 tokens, 2 of 8 experts, H = 5120, I = 1280 18.1 / 23.9 (5 MB);
+// 4 tokens, 8 of 127, H = 2080, I = 736 30.1 / 31.0 (7 MB); 3 tokens, 6 of 64, H = 4096,
+// I = 1408 40.9 / 41.2 (16 MB); 16 tokens, 4 of 64, H = 1024, I = 512 26.3 / 23.4 (25 MB);
+// 4 tokens, 6 of 64, H = 5120, I = 1280 56.9 / 54.5 (35 MB); 32 tokens, 1 of 22,
+// H = 800, I = 320 18.1 / 18.3 (9 MB), 64, 1 of 64, 30.3 / 21.6 (13 MB).
 constexpr int kOneByOne = 32;               // tokens
 constexpr int64_t kRepeatedBytes = 16 << 20;
 bool one_by_one(int64_t T, int64_t H, int64_t I, int64_t E, int64_t top_k) {
@@ -842,9 +842,9 @@ void launch_expert(const MoeArgs& a, hipStream_t s) {
 
 // Waves beside each other share a slot's rows, waves that split K let a few slots fill
 // the GPU.  Up, H = 5120, I = 1280, 12 tokens, 2 of 8 experts (at most 360 workgroups of
-// 2 x 2 waves): whole layer 38.0 us, with 1 x 4 waves 37.3; 48 tokens, 2 of 16 (880):
-// 57.3 and 61.7.  Above four rows a slot units of two groups: 128 tokens, 4 of 16, 103
-// with units of one, 96.
+// 2 x 2 waves): whole layer 36.6 us, with 1 x 4 waves 34.9; 48 tokens, 2 of 16 (880):
+// 54.6 and 58.8.  Above four rows a slot units of two groups: 128 tokens, 4 of 16, 100
+// with units of one, 93.
 void launch_up(const MoeArgs& a, hipStream_t s) {
     if ((int64_t)a.max_slots * ((a.I + 31) / 32) < 512)
         launch_expert<true, kF32, 2, 1, 4, 2, 1>(a, s);
@@ -853,11 +853,12 @@ void launch_up(const MoeArgs& a, hipStream_t s) {
 }
 
 // Down, by workgroups of 4 x 1 waves, 2 x 2 and 2 x 4, whole layer, us.  16 tokens, 6 of 64
-// experts, H = 5120, I = 1280 (2800 of 4 x 1): 104.4 by the first, 106.5 by the second.
-// 2 of 8 experts, H = 4096, I = 14336: 128 tokens (768) 337 by the first; 80 tokens (576)
-// 293 by the second, 274 by the third; 12 tokens (288) 169 and 147.  H = 1024: 24 tokens,
-// 2 of 8, I = 1024 24.5 and 23.4; 16 tokens, 4 of 64, I = 512 23.5 and 25.1; H = 2048,
-// 16 tokens, 4 of 32, I = 768 32.6 and 33.5.
+// experts, H = 5120, I = 1280 (2800 of 4 x 1): 99 by the first, 107 by the second.
+// 2 of 8 experts, H = 4096, I = 14336: 128 tokens (768) 339, 358 and 359; 80 tokens (576)
+// 271, 291 and 278; 12 tokens (288) 175, 145 and 128.  H = 1024: 24 tokens, 2 of 8,
+// I = 1024 25.2, 23.3 and 22.6; 16 tokens, 4 of 64, I = 512 24.0, 22.9 and 24.5; H = 2048,
+// 16 tokens, 4 of 32, I = 768 (576) 30.0, 31.4 and 32.3.  (The border lies a little high:
+// both of 576 go faster by the first.)
 template <Hidden F>
 void launch_down(const MoeArgs& a, hipStream_t s) {
     if ((int64_t)a.max_slots * ((a.H + 127) / 128) >= 640)

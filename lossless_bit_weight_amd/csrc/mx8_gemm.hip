@@ -11,10 +11,12 @@
 // values gives sums that are 0 off the exact ones' fp32 rounding; with all of E4M3's
 // finest steps they were 4.5e-6 off.
 // Few rows are bound by the weights' bytes and the launch's start and end (7168 x 5120, M = 1:
-// 6.2 us, 19.5 MB; 34816 x 5120, M = 16: 19.9, 94.7 MB, 4.8 TB/s), many rows by the matrix
-// units, whose rate with one 8-bit side is that of two (34816 x 5120, M = 4096: 580 to 600 us,
-// 2.4 to 2.5 PFLOP/s, the matrix units 65% busy under the power limit, as far as the library's
-// 8-bit product of that shape, 588).  The rules stand at plan_gemm.
+// 6.2 to 6.7 us, 19.5 MB; 34816 x 5120, M = 16: 20 to 21, 94.7 MB, 4.6 TB/s), many rows by the
+// matrix units, whose rate with one 8-bit side is that of two (34816 x 5120, M = 4096: 584 us,
+// 2.5 PFLOP/s, the matrix units 65% busy under the power limit, as far as the library's 8-bit
+// product of that shape, 588).  The rules stand at plan_gemm.  All figures are of graphs over
+// weights in turn, 155 MB of them up to 7168 x 5120 and 560 MB of larger ones; where these lie
+// in memory moves one by up to a tenth.
 #include <type_traits>
 
 #include "mx8_internal.hpp"
@@ -632,30 +634,31 @@ enum Kernel : int {
 };
 
 // Four or five waves beside each other, whichever spreads nt tiles better over 256 CUs: the
-// CU with the most of them decides (34816 x 5120, 2176 tiles, M = 1 / 16: five 17.1 / 19.5 us,
-// four 18.8 / 23.7).
+// CU with the most of them decides (34816 x 5120, 2176 tiles, M = 1 / 16: five 18.5 / 21 us,
+// four 19.1 / 24.5).
 int spread(int64_t nt) {
     const auto most = [&](int64_t w) { return ((nt + w - 1) / w + 255) / 256 * w; };
     return most(5) <= most(4) ? 5 : 4;
 }
 
-// What a product costs in us: a launch and its start, `start`; for each of a wave's quads of K
-// `fixed` and, for every workgroup that the busiest CU has, `each` and `rows` times the share
-// of its rows that x has, `least` at least, and for all of them what the weights' bytes take
-// (7.7 TB/s: these come from the last-level cache in part); and with K in slices a launch
-// that joins their sums, written and read.  Fitted to 730 products, of 1 to 2048 rows, 512 to
-// 65536 weight rows and K = 544 to 17408, by every kernel here in 1 to 12 slices: the choice
-// takes 0.9% more than the best of them in the mean, a fifth at most.
-// Graphs over weights in turn, us:
+// What a product costs beside others, in us: a launch and its start, `start`; for each of a
+// wave's quads of K `fixed` and, for every workgroup that the busiest CU has, `each` and `rows`
+// times the share of its rows that x has, `least` at least, and for all of them what the
+// weights' bytes take (7.7 TB/s: these come from the last-level cache in part); and with K in
+// slices a launch that joins their sums, written and read.  Fitted to 730 products, of 1 to
+// 2048 rows, 512 to 65536 weight rows and K = 544 to 17408, by every kernel here in 1 to 12
+// slices: the choice takes 0.9% more than the best of them in the mean, a fifth at most.  It
+// ranks kernels, and is no time where a CU has many workgroups (34816 x 5120 M = 512 57, taken
+// 91; M = 4096 290, taken 584).
 //                      16x16/4 16x16/8  16x32  16x64  32x64 32x128 64x128 64x160 64x256
-//   7168 x 5120  M = 1     6.1     6.2    6.5    7.6
-//                M = 16    9.6     9.8    7.3    9.5   12.1
-//                M = 64                  17.2   15.8   13.4   16.2   17.4
-//   4096 x 4096  M = 64   10.6            8.7    7.4    9.0   10.1
-//   34816 x 5120 M = 64                                       30.5   34.4   26.3   39.1
-//                M = 128                                      45.8   40.9   38.4   40.9
-//                M = 256                                      76     63     77     55
-//   5120 x 17408 M = 64 in 6 slices                                  20.3 (3: 27.4, 12: 22.5)
+//   7168 x 5120  M = 1     6.1     6.2    6.5    7.7
+//                M = 16    9.6    10.0    7.4    9.6   10.5
+//                M = 64                  16.8   14.8   11.1   13.0   17.0
+//   4096 x 4096  M = 64   12.7            8.9    7.4   10.4   12.9
+//   34816 x 5120 M = 64                                       30.3   33.5   25.6   38.0
+//                M = 128                                      45.3   40.3   37.5   40.4
+//                M = 256                                      74     63     78     55
+//   5120 x 17408 M = 64 in 6 slices                                  21.0 (3: 27.6, 12: 23.1)
 struct Cost {
     Kernel kernel;
     int bm, bn, waves_k;
@@ -711,14 +714,14 @@ Kernel cheapest(int64_t M, int64_t N, int64_t K, Kernel first, int* slices) {
 // By rows of x (M), tiles of 16 weight rows (nt), pairs of a weight tile and 16 rows of x
 // (t) and quads of K: cheapest(), but for
 //   up to 16 rows and many tiles: x shared by the waves of as many tiles as spread() says
-//     (34816 x 5120 M = 16 19.5 us, two tiles without sharing 27.0); a short K is over before
-//     sharing pays (65536 x 1024 M = 1 8.4, shared 10.0), above 8 rows two tiles a wave read
-//     x once for both;
-//   up to four rows: one tile a workgroup, by eight waves from six quads on (beyond the
-//     last-level cache: 7168 x 5120 M = 1 5.8, 16 x 32 6.1; 5120 x 17408 M = 1 13.8 and 15.1,
-//     M = 4 14.8 and 15.2; 1024 x 4096 4.0, four waves 4.4);
+//     (34816 x 5120 M = 16 21 us, two tiles without sharing 29); a short K is over before
+//     sharing pays (65536 x 1024 M = 1 8.6, shared 10.0), above 8 rows two tiles a wave
+//     read x once for both (M = 16 11.0, one tile 12.8, shared 10.9);
+//   up to four rows: one tile a workgroup, by eight waves from six quads on (7168 x 5120
+//     M = 1 6.2, four waves 6.1, 16 x 32 6.5; 5120 x 17408 M = 1 13.5 to 14.0, 16 x 32 12.9
+//     to 15.4, but M = 4 14.6 and 13.0; 1024 x 4096 3.4, four waves 3.8);
 //   up to two quads: workgroups of one tile and one wave a quad overlap further than the
-//     costs say (6144 x 544 M = 33 4.1, 16 x 64 5.2, 64 x 128 5.8);
+//     costs say (6144 x 544 M = 33 4.1, 16 x 64 7.1, 64 x 128 6.2);
 //   more rows than 16 and many tiles: tiles.
 Plan plan_gemm(int64_t M, int64_t N, int64_t K) {
     const int Q = (int)mx4::quads(K);
