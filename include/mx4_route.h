@@ -38,7 +38,8 @@ enum {
  *   share       = scale * s(t, e) / sum over S(t) of s(t, .)  (renormalize != 0;
  *                 0 where that sum is 0), or scale * s(t, e).
  * Scores, ranks and sums are held in 64 bits, shares are rounded once to fp32;
- * an exponential below exp(-707) counts as 0.
+ * an exponential is off by less than 2.8e-14 of itself (exp(0) is 1), and below
+ * exp(-707) counts as 0.
  * An expert whose logit or whose bias is -inf is in no S(t) and adds nothing to
  * its group's value; a token with fewer than top_k others gets -1 and share 0
  * in the places left.
